@@ -11,6 +11,10 @@ library's sm_103a kernels; there is no CPU or eager fallback.
     q = token_cat_fp8(attention, mlp, input_scale)
     q4, sf = token_cat_nvfp4(attention, mlp, global_scale)            # uint8 codes / scales
     jq, jk, jv = qkv_epilogue(txt, img, heads)      # per-head QK RMSNorm + RoPE, joint pack
+    q, s = rms_norm_quant(x, weight)                # 8-bit rows, one fp32 scale each
+    h, q, s = rms_norm_quant(x, weight, residual=r, dtype=torch.float8_e4m3fn)
+    q, s = silu_mul_quant(gate, up)                 # SiLU(gate) * up -> 8-bit rows
+    y = int8_matmul(q, s, w, w_scale, bias=b)       # int8 rows x int8 weights, scaled
     bits = device_error()                           # 0 unless a bounded kernel wait ran out
 """
 from __future__ import annotations
@@ -22,7 +26,8 @@ from ._build import build
 from ._capi import Fp8qError
 
 __all__ = ["nss_fp8", "scale_residual_nss_fp8", "bias_mul_add", "token_cat_fp8",
-           "token_cat_nvfp4", "nvfp4_scale_bytes", "qkv_epilogue", "device_error",
+           "token_cat_nvfp4", "nvfp4_scale_bytes", "qkv_epilogue", "rms_norm_quant", "silu_mul_quant",
+           "int8_matmul", "device_error",
            "row_pieces", "build",
            "Fp8qError", "library_path"]
 
@@ -203,6 +208,138 @@ def qkv_epilogue(txt: dict, img: dict, heads: int, *, out=None, stream=None):
     st = _capi.lib().fp8q_qkv_epilogue(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
                                        ts, ims, heads, _stream_handle(stream))
     _capi.check(st, "fp8q_qkv_epilogue")
+    return out
+
+
+_QTYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
+_OUT_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _on_current_device(x: torch.Tensor, name: str, others) -> None:
+    """The library launches on the current device: x and the other tensors have to be there."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise TypeError(f"{name}: expected a CUDA tensor, got {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise TypeError(f"tensors on {dev} and on {t.device}: expected one device")
+    if dev.index != torch.cuda.current_device():
+        raise TypeError(f"{name} is on {dev}, but the current device is "
+                        f"cuda:{torch.cuda.current_device()}")
+
+
+def _new(out, shape, dtype, like: torch.Tensor, name: str, stream) -> torch.Tensor:
+    """A given output, checked, or a new one that belongs to the stream it is written on."""
+    if out is not None or stream is None:
+        return _out(out, shape, dtype, like, name)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _strided_rows(t: torch.Tensor, dtype, name: str):
+    """(rows, cols, row stride) of a tensor whose rows lie at one stride, columns adjacent."""
+    if t.dtype != dtype or t.dim() < 1:
+        raise TypeError(f"{name}: expected a {dtype} tensor [..., cols], got {t.dtype} "
+                        f"{tuple(t.shape)}")
+    cols = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // cols if cols else 0), cols, cols
+    try:
+        v = t.view(-1, cols)
+    except RuntimeError:
+        v = None
+    if v is None or v.stride(1) != 1:
+        raise TypeError(f"{name}: rows of shape {tuple(t.shape)} and strides {t.stride()} do "
+                        "not lie at one row stride with adjacent columns")
+    return v.shape[0], cols, (v.stride(0) if v.shape[0] > 1 else cols)
+
+
+def _row_scale(t: torch.Tensor, n: int, name: str) -> None:
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise TypeError(f"{name}: expected {n} contiguous float32 values, got {t.dtype} "
+                        f"{tuple(t.shape)}")
+
+
+def rms_norm_quant(x, weight, *, residual=None, dtype=torch.int8, eps: float = EPS,
+                   residual_out=None, q=None, scale=None, stream=None):
+    """RMSNorm(x + residual) * weight as 8-bit rows with one float32 scale each: (q, scale),
+    or (h, q, scale) with a residual, h = bfloat16 x + residual (residual_out may be the
+    residual itself). x: [..., cols]; q: `dtype` int8 or float8_e4m3fn; scale: [...]; the
+    normalised value is about q * scale."""
+    qt = _QTYPES.get(dtype)
+    if qt is None:
+        raise TypeError(f"dtype: expected torch.int8 or torch.float8_e4m3fn, got {dtype}")
+    _on_current_device(x, "x", (weight, residual, residual_out, q, scale))
+    _bf16(x, "x"), _bf16(weight, "weight")
+    shape = x.shape
+    rows, cols = _rows_cols(x)
+    if weight.numel() != cols:
+        raise TypeError(f"weight: expected {cols} values, got {tuple(weight.shape)}")
+    h = None
+    if residual is not None:
+        if _bf16(residual, "residual").shape != shape:
+            raise TypeError(f"residual: expected {tuple(shape)}, got {tuple(residual.shape)}")
+        h = _new(residual_out, shape, torch.bfloat16, x, "residual_out", stream)
+    elif residual_out is not None:
+        raise TypeError("residual_out: given without a residual")
+    q = _new(q, shape, dtype, x, "q", stream)
+    scale = _new(scale, shape[:-1], torch.float32, x, "scale", stream)
+    st = _capi.lib().fp8q_rms_norm_quant(None if h is None else h.data_ptr(), q.data_ptr(),
+                                         scale.data_ptr(), x.data_ptr(),
+                                         None if h is None else residual.data_ptr(),
+                                         weight.data_ptr(), qt, rows, cols, eps,
+                                         _stream_handle(stream))
+    if st:
+        _capi.check(st, "fp8q_rms_norm_quant")
+    return (q, scale) if h is None else (h, q, scale)
+
+
+def silu_mul_quant(gate, up, *, dtype=torch.int8, q=None, scale=None, stream=None):
+    """SiLU(gate) * up as 8-bit rows with one float32 scale each: (q, scale). gate, up:
+    [..., cols] bfloat16 of one shape and row stride, e.g. the halves of a packed product."""
+    qt = _QTYPES.get(dtype)
+    if qt is None:
+        raise TypeError(f"dtype: expected torch.int8 or torch.float8_e4m3fn, got {dtype}")
+    _on_current_device(gate, "gate", (up, q, scale))
+    rows, cols, ld = _strided_rows(gate, torch.bfloat16, "gate")
+    if up.shape != gate.shape or _strided_rows(up, torch.bfloat16, "up")[2] != ld:
+        raise TypeError(f"gate {tuple(gate.shape)} {gate.stride()} and up {tuple(up.shape)} "
+                        f"{up.stride()}: expected one shape and one row stride")
+    shape = gate.shape
+    q = _new(q, shape, dtype, gate, "q", stream)
+    scale = _new(scale, shape[:-1], torch.float32, gate, "scale", stream)
+    st = _capi.lib().fp8q_silu_mul_quant(q.data_ptr(), scale.data_ptr(), gate.data_ptr(),
+                                         up.data_ptr(), ld, qt, rows, cols,
+                                         _stream_handle(stream))
+    if st:
+        _capi.check(st, "fp8q_silu_mul_quant")
+    return q, scale
+
+
+def int8_matmul(a, a_scale, w, w_scale, *, bias=None, out_dtype=torch.bfloat16, out=None,
+                stream=None):
+    """(a @ w.T) * w_scale * a_scale[..., None] (+ bias): a int8 [..., k] (rows at one stride, a
+    multiple of 16), a_scale float32 one per row, w int8 [n, k], w_scale float32 [n], bias
+    bfloat16 [n]. Returns [..., n] in out_dtype (bfloat16 or float32)."""
+    ot = _OUT_TYPES.get(out_dtype)
+    if ot is None:
+        raise TypeError(f"out_dtype: expected torch.bfloat16 or torch.float32, got {out_dtype}")
+    _on_current_device(a, "a", (a_scale, w, w_scale, bias, out))
+    m, k, lda = _strided_rows(a, torch.int8, "a")
+    if w.dtype != torch.int8 or w.dim() != 2 or w.shape[1] != k or not w.is_contiguous():
+        raise TypeError(f"w: expected a contiguous int8 [n, {k}], got {w.dtype} {tuple(w.shape)}")
+    n = w.shape[0]
+    _row_scale(a_scale, m, "a_scale")
+    _row_scale(w_scale, n, "w_scale")
+    if bias is not None and _bf16(bias, "bias").numel() != n:
+        raise TypeError(f"bias: expected {n} values, got {tuple(bias.shape)}")
+    out = _new(out, (*a.shape[:-1], n), out_dtype, a, "out", stream)
+    st = _capi.lib().fp8q_int8_matmul(out.data_ptr(), a.data_ptr(), lda, a_scale.data_ptr(),
+                                      w.data_ptr(), w_scale.data_ptr(),
+                                      None if bias is None else bias.data_ptr(), ot, m, n, k,
+                                      _stream_handle(stream))
+    if st:
+        _capi.check(st, "fp8q_int8_matmul")
     return out
 
 

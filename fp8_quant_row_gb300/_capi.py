@@ -20,7 +20,8 @@ STATUS = {0: "FP8Q_OK", 1: "FP8Q_ERR_NULL", 2: "FP8Q_ERR_ALIGN", 3: "FP8Q_ERR_SH
 #: every function include/fp8q.h declares
 SYMBOLS = ("fp8q_nss_fp8", "fp8q_scale_residual_nss_fp8", "fp8q_bias_mul_add",
            "fp8q_token_cat_fp8", "fp8q_token_cat_nvfp4", "fp8q_nvfp4_scale_bytes",
-           "fp8q_qkv_epilogue", "fp8q_device_error",
+           "fp8q_qkv_epilogue", "fp8q_rms_norm_quant", "fp8q_silu_mul_quant",
+           "fp8q_int8_matmul", "fp8q_device_error",
            "fp8q_status_string", "fp8q_last_cuda_error",
            "fp8q_last_error_detail", "fp8q_version")
 
@@ -62,10 +63,14 @@ def lib():
         L.fp8q_token_cat_nvfp4.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, vp]
         L.fp8q_qkv_epilogue.argtypes = [vp, vp, vp, ctypes.POINTER(QkvStream),
                                          ctypes.POINTER(QkvStream), i64, vp]
+        L.fp8q_rms_norm_quant.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i64, f32, vp]
+        L.fp8q_silu_mul_quant.argtypes = [vp, vp, vp, vp, i64, i32, i64, i64, vp]
+        L.fp8q_int8_matmul.argtypes = [vp, vp, i64, vp, vp, vp, vp, i32, i64, i64, i64, vp]
         L.fp8q_nvfp4_scale_bytes.argtypes = [i64, i64]
         L.fp8q_nvfp4_scale_bytes.restype = i64
         for name in ("fp8q_nss_fp8", "fp8q_scale_residual_nss_fp8", "fp8q_bias_mul_add",
-                     "fp8q_token_cat_fp8", "fp8q_token_cat_nvfp4", "fp8q_qkv_epilogue"):
+                     "fp8q_token_cat_fp8", "fp8q_token_cat_nvfp4", "fp8q_qkv_epilogue",
+                     "fp8q_rms_norm_quant", "fp8q_silu_mul_quant", "fp8q_int8_matmul"):
             getattr(L, name).restype = i32
         L.fp8q_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint)]
         L.fp8q_device_error.restype = i32

@@ -16,16 +16,20 @@
 
 #include "fp8q.h"
 #include "elementwise_kernels.cuh"
+#include "int8_matmul_kernels.cuh"
 #include "nss_kernels.cuh"
 #include "nss_ws_kernels.cuh"
 #include "nvfp4_kernels.cuh"
 #include "qkv_kernels.cuh"
+#include "row_quant_kernels.cuh"
 
 namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxLnCols = 32768;
 constexpr int64_t kMaxEwCols = int64_t(1) << 30;
+constexpr int64_t kMaxSiluCols = int64_t(1) << 20;
+constexpr int64_t kMaxMmK = 131056;  // |sum| < 2^31
 
 thread_local int g_last_cuda_error = 0;
 thread_local char g_last_detail[160] = "";
@@ -127,6 +131,7 @@ fp8q_status blocks_per_sm(const void* fn, int threads, size_t smem, int* blocks)
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 // Bytes spanned by `tokens` rows of `width` BF16 values at a stride of `ld` values.
@@ -283,6 +288,40 @@ fp8q_status check_ln_shape(int64_t rows, int64_t cols, int64_t mod_rows, float e
 
 int64_t mod_count(int64_t rows, int64_t mod_rows) {
   return mod_rows > 0 ? (rows + mod_rows - 1) / mod_rows : 1;
+}
+
+// ------------------------------------------------------------------------------------------
+// 8-bit rows with a scale each, and their product
+// ------------------------------------------------------------------------------------------
+
+template <bool INT8, bool RESID>
+fp8q_status launch_rms(const fp8q::RmsParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  auto* fn = fp8q::rms_norm_quant_kernel<INT8, RESID>;
+  const size_t smem = size_t(p.cols) * 2;
+  int bps = 0;
+  fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kRqThreads, smem, &bps);
+  if (st != FP8Q_OK) return st;
+  const int64_t grid = std::min<int64_t>(p.rows, int64_t(dev.sms) * std::max(bps, 1));
+  return launch(fn, dim3(unsigned(grid)), dim3(fp8q::kRqThreads), smem, stream, p);
+}
+
+template <bool INT8>
+fp8q_status launch_silu(const fp8q::SiluParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  auto* fn = fp8q::silu_mul_quant_kernel<INT8>;
+  int bps = 0;
+  fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kRqThreads, 0, &bps);
+  if (st != FP8Q_OK) return st;
+  const int64_t grid = std::min<int64_t>(p.rows, int64_t(dev.sms) * std::max(bps, 1));
+  return launch(fn, dim3(unsigned(grid)), dim3(fp8q::kRqThreads), 0, stream, p);
+}
+
+template <bool F32>
+fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
+                               cudaStream_t stream) {
+  const unsigned gx = unsigned((p.n + fp8q::kMmTile - 1) / fp8q::kMmTile);
+  const unsigned gy = unsigned(std::min<int64_t>((p.m + fp8q::kMmTile - 1) / fp8q::kMmTile, 65535));
+  return launch(fp8q::int8_matmul_dp4a_kernel<F32>, dim3(gx, gy), dim3(fp8q::kMmThreads), 0,
+                stream, p);
 }
 
 }  // namespace
@@ -584,6 +623,117 @@ fp8q_status fp8q_qkv_epilogue(void* joint_q, void* joint_k, void* joint_v,
   }
   const unsigned gx = unsigned(total < 0x7FFFFFFF ? total : 0x7FFFFFFF);
   return launch(fp8q::qkv_epilogue_kernel, dim3(gx), dim3(fp8q::kQkvWarps * 32), 0, stream, p);
+}
+
+fp8q_status fp8q_rms_norm_quant(void* residual_out, void* q, float* q_scale, const void* x_bf16,
+                                const void* residual_bf16, const void* weight_bf16, int q_type,
+                                int64_t rows, int64_t cols, float eps, cudaStream_t stream) {
+  fp8q_status st = check_ln_shape(rows, cols, 0, eps);
+  if (st != FP8Q_OK) return st;
+  if (rows > INT64_MAX / cols / 4) return FP8Q_ERR_SHAPE;
+  if (q_type != FP8Q_INT8 && q_type != FP8Q_E4M3) return FP8Q_ERR_VALUE;
+  if (rows == 0) return FP8Q_OK;
+  if (!q || !q_scale || !x_bf16 || !weight_bf16 || !residual_out != !residual_bf16)
+    return FP8Q_ERR_NULL;
+  if (!aligned16(q) || !aligned16(x_bf16) || !aligned16(weight_bf16) || !aligned4(q_scale) ||
+      (residual_bf16 && (!aligned16(residual_out) || !aligned16(residual_bf16))))
+    return FP8Q_ERR_ALIGN;
+  const size_t n = size_t(rows) * size_t(cols);
+  const Range ro{residual_out, n * 2}, qr{q, n}, sr{q_scale, size_t(rows) * 4};
+  const Range x{x_bf16, n * 2}, res{residual_bf16, n * 2}, w{weight_bf16, size_t(cols) * 2};
+  for (Range out : {ro, qr, sr})
+    for (Range in : {x, res, w}) {
+      if (out.p == ro.p && same(ro, res) && in.p == res.p) continue;  // in-place residual
+      if (overlap(out, in)) return FP8Q_ERR_ALIAS;
+    }
+  if (overlap(ro, qr) || overlap(ro, sr) || overlap(qr, sr)) return FP8Q_ERR_ALIAS;
+  const DeviceInfo* dev = nullptr;
+  st = current_device(&dev);
+  if (st != FP8Q_OK) return st;
+  fp8q::RmsParams p{};
+  p.x = static_cast<const uint16_t*>(x_bf16);
+  p.residual = static_cast<const uint16_t*>(residual_bf16);
+  p.weight = static_cast<const uint16_t*>(weight_bf16);
+  p.h = static_cast<uint16_t*>(residual_out);
+  p.q = static_cast<uint8_t*>(q);
+  p.scale = q_scale;
+  p.rows = rows;
+  p.cols = int(cols);
+  p.eps = eps;
+  if (q_type == FP8Q_INT8)
+    return residual_bf16 ? launch_rms<true, true>(p, *dev, stream)
+                         : launch_rms<true, false>(p, *dev, stream);
+  return residual_bf16 ? launch_rms<false, true>(p, *dev, stream)
+                       : launch_rms<false, false>(p, *dev, stream);
+}
+
+fp8q_status fp8q_silu_mul_quant(void* q, float* q_scale, const void* gate_bf16,
+                                const void* up_bf16, int64_t ld, int q_type, int64_t rows,
+                                int64_t cols, cudaStream_t stream) {
+  if (rows < 0 || cols < 8 || cols % 8 != 0 || cols > kMaxSiluCols) return FP8Q_ERR_SHAPE;
+  if (ld < cols || ld % 8 != 0 || ld > kMaxEwCols || rows > INT64_MAX / ld / 4)
+    return FP8Q_ERR_SHAPE;
+  if (q_type != FP8Q_INT8 && q_type != FP8Q_E4M3) return FP8Q_ERR_VALUE;
+  if (rows == 0) return FP8Q_OK;
+  if (!q || !q_scale || !gate_bf16 || !up_bf16) return FP8Q_ERR_NULL;
+  if (!aligned16(q) || !aligned16(gate_bf16) || !aligned16(up_bf16) || !aligned4(q_scale))
+    return FP8Q_ERR_ALIGN;
+  const Range qr{q, size_t(rows) * size_t(cols)}, sr{q_scale, size_t(rows) * 4};
+  const Range g{gate_bf16, strided_bytes(rows, ld, cols)};
+  const Range u{up_bf16, strided_bytes(rows, ld, cols)};
+  for (Range out : {qr, sr})
+    if (overlap(out, g) || overlap(out, u)) return FP8Q_ERR_ALIAS;
+  if (overlap(qr, sr)) return FP8Q_ERR_ALIAS;
+  const DeviceInfo* dev = nullptr;
+  fp8q_status st = current_device(&dev);
+  if (st != FP8Q_OK) return st;
+  fp8q::SiluParams p{};
+  p.gate = static_cast<const uint16_t*>(gate_bf16);
+  p.up = static_cast<const uint16_t*>(up_bf16);
+  p.ld = ld;
+  p.q = static_cast<uint8_t*>(q);
+  p.scale = q_scale;
+  p.rows = rows;
+  p.cols = int(cols);
+  return q_type == FP8Q_INT8 ? launch_silu<true>(p, *dev, stream)
+                             : launch_silu<false>(p, *dev, stream);
+}
+
+fp8q_status fp8q_int8_matmul(void* out, const int8_t* a, int64_t lda, const float* a_scale,
+                             const int8_t* w, const float* w_scale, const void* bias_bf16,
+                             int out_type, int64_t m, int64_t n, int64_t k, cudaStream_t stream) {
+  if (m < 0 || n < 1 || n > INT32_MAX || m > INT32_MAX || k < 16 || k % 16 != 0 || k > kMaxMmK ||
+      lda < k || lda % 16 != 0 || lda > kMaxEwCols)
+    return FP8Q_ERR_SHAPE;
+  if (out_type != FP8Q_OUT_BF16 && out_type != FP8Q_OUT_FP32) return FP8Q_ERR_VALUE;
+  if (m == 0) return FP8Q_OK;
+  if (!out || !a || !a_scale || !w || !w_scale) return FP8Q_ERR_NULL;
+  const size_t width = out_type == FP8Q_OUT_FP32 ? 4 : 2;
+  if (!aligned16(a) || !aligned16(w) || !aligned4(a_scale) || !aligned4(w_scale) ||
+      (reinterpret_cast<uintptr_t>(out) & (width - 1)) != 0 ||
+      (reinterpret_cast<uintptr_t>(bias_bf16) & 1) != 0)
+    return FP8Q_ERR_ALIGN;
+  const Range o{out, size_t(m) * size_t(n) * width};
+  for (Range in : {Range{a, size_t(m - 1) * size_t(lda) + size_t(k)},
+                   Range{w, size_t(n) * size_t(k)}, Range{a_scale, size_t(m) * 4},
+                   Range{w_scale, size_t(n) * 4}, Range{bias_bf16, size_t(n) * 2}})
+    if (overlap(o, in)) return FP8Q_ERR_ALIAS;
+  const DeviceInfo* dev = nullptr;
+  fp8q_status st = current_device(&dev);
+  if (st != FP8Q_OK) return st;
+  fp8q::MmParams p{};
+  p.a = a;
+  p.w = w;
+  p.a_scale = a_scale;
+  p.w_scale = w_scale;
+  p.bias = static_cast<const uint16_t*>(bias_bf16);
+  p.out = out;
+  p.lda = lda;
+  p.m = m;
+  p.n = n;
+  p.k = k;
+  return out_type == FP8Q_OUT_FP32 ? launch_int8_matmul<true>(p, *dev, stream)
+                                   : launch_int8_matmul<false>(p, *dev, stream);
 }
 
 fp8q_status fp8q_device_error(unsigned int* bits) {

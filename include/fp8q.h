@@ -10,6 +10,10 @@
  *                           of the same row concat.
  *   qkv_epilogue            after the packed QKV GEMM: per-head Q/K RMSNorm + interleaved RoPE,
  *                           V copy, joint [text, image] attention inputs.
+ *   rms_norm_quant          [residual addition ->] RMSNorm -> 8-bit rows, one fp32 scale each.
+ *   silu_mul_quant          SiLU(gate) * up -> 8-bit rows, one fp32 scale each.
+ *   int8_matmul             product of int8 rows and int8 weights with a scale for each row
+ *                           (token) and each weight row (output channel).
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers to row-major, contiguous arrays on the current
@@ -19,7 +23,8 @@
  *     only enqueues work on `stream` (0 = the legacy default stream). Outputs are complete
  *     when that stream reaches the launch.
  *   - Every tensor pointer must be 16-byte aligned (FP8Q_ERR_ALIGN otherwise); the NVFP4
- *     and QKV entry points need 32 bytes for their data pointers (see each call).
+ *     and QKV entry points need 32 bytes for their data pointers, scale arrays of 8-bit rows
+ *     and the product's output only their element's alignment (see each call).
  *   - rows == 0 returns FP8Q_OK without touching any pointer or launching anything.
  *   - Argument errors are reported synchronously, before any launch, with a status code; a
  *     failed launch returns FP8Q_ERR_CUDA (fp8q_last_cuda_error() gives the cudaError_t).
@@ -69,7 +74,7 @@ typedef enum fp8q_status {
     FP8Q_ERR_UNSUPPORTED = 4, /* current device is not compute capability 10.3                */
     FP8Q_ERR_ALIAS = 5,       /* an output overlaps an input or another output (see per call) */
     FP8Q_ERR_CUDA = 6,        /* a CUDA runtime query or the kernel launch failed             */
-    FP8Q_ERR_VALUE = 7        /* a scalar argument is out of range (eps < 0 or not finite)    */
+    FP8Q_ERR_VALUE = 7        /* a scalar argument is out of range (eps, q_type, out_type)     */
 } fp8q_status;
 
 /*
@@ -239,6 +244,82 @@ typedef struct fp8q_qkv_stream {
 fp8q_status fp8q_qkv_epilogue(void* joint_q, void* joint_k, void* joint_v,
                               const fp8q_qkv_stream* txt, const fp8q_qkv_stream* img,
                               int64_t heads, cudaStream_t stream);
+
+/* Element types of the 8-bit rows (q_type) and of the product's output (out_type). */
+#define FP8Q_INT8 0     /* two's complement, codes -127 .. 127 */
+#define FP8Q_E4M3 1     /* e4m3fn codes, up to +-448            */
+#define FP8Q_OUT_BF16 0
+#define FP8Q_OUT_FP32 1
+
+/*
+ * RMSNorm -> 8-bit rows with one scale each, optionally after the residual's addition.
+ * With QMAX = 127 (FP8Q_INT8) or 448 (FP8Q_E4M3), for each row:
+ *   h     = residual ? RN_bf16(x + residual) : x           (written to residual_out)
+ *   p_j   = h_j * w_j                                       exact in fp32
+ *   P     = max_j |p_j|,  inv = RN_fp32(QMAX / P)
+ *   q_j   = RNE(p_j * inv), the product unrounded            FP8Q_INT8
+ *           E4M3(RN_fp32(p_j * inv))                         FP8Q_E4M3
+ *   scale = P / sqrt(mean_j(h_j^2) + eps) / QMAX             in fp32
+ * so q_j * scale approximates the normalised h_j * w_j / rms. 1/rms cancels in q: the codes
+ * are those of exact products whatever the order of the sum.
+ *
+ *   residual_out  out [rows, cols] bf16; NULL exactly when residual_bf16 is; may be exactly
+ *                     the residual buffer (in-place update)
+ *   q             out [rows, cols] int8 or e4m3 codes
+ *   q_scale       out [rows] fp32 (4-byte aligned)
+ *   x, residual   in  [rows, cols] bf16 (residual may be NULL)
+ *   weight_bf16   in  [cols] bf16
+ *   cols          multiple of 8, 8 <= cols <= 32768;  eps >= 0 and finite
+ *   Aliasing: residual_out may equal residual exactly; every other overlap of an output with
+ *   an input or another output is rejected.
+ *   A row with a NaN or infinite product, or whose squares overflow fp32, gets the scale NaN
+ *   (and, where a product is not finite, codes 0); a row with P < 2^-100 counts as zero: scale
+ *   and codes 0. With eps = 0 a row whose squares underflow fp32 is outside the contract.
+ */
+fp8q_status fp8q_rms_norm_quant(void* residual_out, void* q, float* q_scale, const void* x_bf16,
+                                const void* residual_bf16, const void* weight_bf16, int q_type,
+                                int64_t rows, int64_t cols, float eps, cudaStream_t stream);
+
+/*
+ * Gated activation -> 8-bit rows with one scale each:
+ *   s_j = RN_bf16(RN_fp32(silu(gate_j))), silu(g) = g / (1 + exp(-g)); 0 for
+ *         finite g < -87, NaN for -infinity
+ *   p_j = s_j * up_j (exact in fp32), P, inv, q_j as above,  scale = P / QMAX
+ * The gate's activation is rounded to bf16 (as where it is a tensor of its own), so that the
+ * products are exact and the codes do not depend on how the exponential is computed.
+ *
+ *   q         out [rows, cols] codes, contiguous
+ *   q_scale   out [rows] fp32 (4-byte aligned)
+ *   gate, up  in  bf16, row r at gate + r*ld / up + r*ld values: two tensors, or the column
+ *                 halves of one packed [rows, 2*cols] product
+ *   ld        row stride in values, >= cols, a multiple of 8
+ *   cols      multiple of 8, 8 <= cols <= 2^20
+ *   Aliasing: no output may overlap an input or the other output.
+ *   NaN, infinite and tiny rows as above.
+ */
+fp8q_status fp8q_silu_mul_quant(void* q, float* q_scale, const void* gate_bf16,
+                                const void* up_bf16, int64_t ld, int q_type, int64_t rows,
+                                int64_t cols, cudaStream_t stream);
+
+/*
+ * Product of 8-bit integers with scales for each row and output channel:
+ *   out[i, j] = RN(RN_fp32(acc * w_scale[j]) * a_scale[i] + bias[j]),
+ *   acc = sum_k a[i, k] * w[j, k]
+ *
+ *   out       out [m, n] bf16 (FP8Q_OUT_BF16) or fp32 (FP8Q_OUT_FP32), contiguous, aligned to
+ *                 its element
+ *   a         in  [m, k] int8, row stride lda (>= k, a multiple of 16)
+ *   a_scale   in  [m] fp32 (4-byte aligned)
+ *   w         in  [n, k] int8, contiguous
+ *   w_scale   in  [n] fp32 (4-byte aligned)
+ *   bias      in  [n] bf16 or NULL
+ *   m, n      0 <= m < 2^31, 1 <= n < 2^31;  k a multiple of 16, 16 <= k <= 131056
+ *   Aliasing: out may not overlap an input.
+ *   A NaN scale makes its row or column NaN.
+ */
+fp8q_status fp8q_int8_matmul(void* out, const int8_t* a, int64_t lda, const float* a_scale,
+                             const int8_t* w, const float* w_scale, const void* bias_bf16,
+                             int out_type, int64_t m, int64_t n, int64_t k, cudaStream_t stream);
 
 /* Bits of the device error word (fp8q_device_error). */
 #define FP8Q_DEVERR_WAIT_TIMEOUT 1u /* a kernel gave up on a bounded shared-memory wait */
