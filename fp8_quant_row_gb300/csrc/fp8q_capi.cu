@@ -297,7 +297,7 @@ int64_t mod_count(int64_t rows, int64_t mod_rows) {
 template <bool INT8, bool RESID>
 fp8q_status launch_rms(const fp8q::RmsParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   auto* fn = fp8q::rms_norm_quant_kernel<INT8, RESID>;
-  const size_t smem = size_t(p.cols) * 2;
+  const size_t smem = size_t(p.cols) * 2 + 64 * sizeof(float);
   int bps = 0;
   fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kRqThreads, smem, &bps);
   if (st != FP8Q_OK) return st;

@@ -3,7 +3,7 @@
 //   silu_mul_quant   p = RN_bf16(silu(gate)) * up
 //
 // Both form products p of two bf16 values, exact in fp32 (16 significant bits), take the row's
-// largest magnitude P and emit codes of p * inv with inv = RN(QMAX / P):
+// largest magnitude P and emit codes of p * inv with inv = RN(QMAX * RN(1 / P)):
 //   int8   RNE(p * inv), the product unrounded (one FMA against 1.5 * 2^23 rounds it to the
 //          integer held in the low byte of the sum)
 //   e4m3   E4M3(RN(p * inv))
@@ -32,10 +32,11 @@ __device__ __forceinline__ constexpr float rq_qmax() {
   return INT8 ? 127.0f : 448.0f;
 }
 
-// RN(QMAX / top), 0 for a row that has no codes (top tiny, infinite or NaN).
+// RN(QMAX * RN(1 / top)), 0 for a row that has no codes (top tiny, infinite or NaN).
 template <bool INT8>
 __device__ __forceinline__ float rq_inverse(float top) {
-  return top >= kRqTiny && top <= 3.402823466e38f ? __fdiv_rn(rq_qmax<INT8>(), top) : 0.0f;
+  return top >= kRqTiny && top <= 3.402823466e38f ? __fmul_rn(rq_qmax<INT8>(), __frcp_rn(top))
+                                                  : 0.0f;
 }
 
 // Four codes of p * inv in one word.
@@ -53,8 +54,9 @@ __device__ __forceinline__ uint32_t rq_codes4(float p0, float p1, float p2, floa
 }
 
 // RN_bf16(RN_fp32(silu(g))) of two gates as fp32 values. silu(g) = g / (1 + 2^(-g log2 e)); the
-// two approximate instructions leave an error of about 2^-21, and for each of the 65536 bf16
-// gates the result rounds to the same bf16 value as the exact one (the test goes over all).
+// product in the exponent and the two approximate instructions leave a relative error of up to
+// 2^-18 (at g = -87; 2^-22 near 0), and for each of the 65536 bf16 gates the result rounds to
+// the same bf16 value as the exact one (the test goes over all of them).
 // The flushing reciprocal gives 0 for g <= -87.5.
 __device__ __forceinline__ float rq_sigmoid_denominator(float g) {
   float e;
@@ -104,8 +106,8 @@ struct RmsParams {
 // second forms the codes.
 template <bool INT8, bool RESID>
 __global__ void __launch_bounds__(kRqThreads) rms_norm_quant_kernel(RmsParams p) {
-  extern __shared__ uint4 rq_row[];
-  __shared__ float red[64];
+  extern __shared__ uint4 rq_row[];  // [cols] bf16, then the reduction's 64 floats
+  float* red = reinterpret_cast<float*>(rq_row + (p.cols >> 3));
   allow_dependents();
   wait_for_producers();
   const int chunks = p.cols >> 3;

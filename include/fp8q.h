@@ -256,7 +256,7 @@ fp8q_status fp8q_qkv_epilogue(void* joint_q, void* joint_k, void* joint_v,
  * With QMAX = 127 (FP8Q_INT8) or 448 (FP8Q_E4M3), for each row:
  *   h     = residual ? RN_bf16(x + residual) : x           (written to residual_out)
  *   p_j   = h_j * w_j                                       exact in fp32
- *   P     = max_j |p_j|,  inv = RN_fp32(QMAX / P)
+ *   P     = max_j |p_j|,  inv = RN_fp32(QMAX * RN_fp32(1 / P))
  *   q_j   = RNE(p_j * inv), the product unrounded            FP8Q_INT8
  *           E4M3(RN_fp32(p_j * inv))                         FP8Q_E4M3
  *   scale = P / sqrt(mean_j(h_j^2) + eps) / QMAX             in fp32

@@ -30,7 +30,7 @@ def codes(p, dtype):
     top = p.abs().amax(-1, keepdim=True)
     ok = torch.isfinite(p).all(-1, keepdim=True) & (top >= TINY)
     qmax = 127.0 if dtype == torch.int8 else 448.0
-    inv = torch.where(ok, torch.tensor(qmax, device=p.device) / top.float(), 0.0)
+    inv = torch.where(ok, top.float().reciprocal() * qmax, 0.0)  # each step rounded to fp32
     t = torch.where(ok, p, 0.0) * inv.double()  # 16 x 24 bits: exact in 64
     if dtype == torch.int8:
         q = t.round()
@@ -182,7 +182,7 @@ def test_silu_of_every_bf16_gate():
     big = finite & (want.float().abs() >= TINY)
     assert bool(big.sum() > 30000)
     top = want.double().abs()
-    assert torch.equal(s[big], (top[big].float() / 127))
+    assert torch.equal(s[big], (top[big] / 127).float())  # divided in 64 bits
     assert torch.equal(q[big][:, 0], (127 * torch.sign(want[big].double())).to(torch.int8))
     small = finite & ~big
     assert not s[small].any() and not q[small].any()
