@@ -17,6 +17,7 @@
 #include "fp8q.h"
 #include "elementwise_kernels.cuh"
 #include "int8_matmul_kernels.cuh"
+#include "int8_matmul_tc_kernels.cuh"
 #include "nss_kernels.cuh"
 #include "nss_ws_kernels.cuh"
 #include "nvfp4_kernels.cuh"
@@ -315,9 +316,88 @@ fp8q_status launch_silu(const fp8q::SiluParams& p, const DeviceInfo& dev, cudaSt
   return launch(fn, dim3(unsigned(grid)), dim3(fp8q::kRqThreads), 0, stream, p);
 }
 
+// The driver's tensor-map encoder, through the runtime (the library links no libcuda).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+fp8q_status encode_tiled(EncodeTiled* fn) {
+  static std::once_flag once;
+  static void* entry = nullptr;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult found;
+    err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &entry, 12000,
+                                           cudaEnableDefault, &found);
+    if (err == cudaSuccess && found != cudaDriverEntryPointSuccess) err = cudaErrorSymbolNotFound;
+  });
+  if (err != cudaSuccess) return cuda_fail(err, "cudaGetDriverEntryPointByVersion");
+  *fn = reinterpret_cast<EncodeTiled>(entry);
+  return FP8Q_OK;
+}
+
+// Tensor map of int8 rows [rows, k] at stride ld: boxes of 128 values of k x `box` rows, 128-byte
+// swizzle; values past k and rows past `rows` read as zero.
+fp8q_status int8_map(CUtensorMap* map, const int8_t* p, int64_t rows, int64_t k, int64_t ld,
+                     int box) {
+  EncodeTiled fn = nullptr;
+  const fp8q_status st = encode_tiled(&fn);
+  if (st != FP8Q_OK) return st;
+  const cuuint64_t dims[2] = {cuuint64_t(k), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(ld)};
+  const cuuint32_t boxes[2] = {cuuint32_t(fp8q::kTcStep), cuuint32_t(box)};
+  const cuuint32_t steps[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims,
+                        strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled", r);
+  return FP8Q_OK;
+}
+
+template <int CG, int BT, bool F32>
+fp8q_status launch_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, cudaStream_t stream) {
+  using L = fp8q::TcLayout<CG, BT>;
+  auto* fn = fp8q::int8_matmul_tc_kernel<CG, BT, F32>;
+  fp8q::TcParams p;
+  p.mm = mm;
+  p.tiles_n = (mm.n + 128 * CG - 1) / (128 * CG);
+  p.tiles_m = (mm.m + BT - 1) / BT;
+  p.tiles = p.tiles_n * p.tiles_m;
+  p.steps = int((mm.k + fp8q::kTcStep - 1) / fp8q::kTcStep);
+  CUtensorMap map_w, map_a;
+  fp8q_status st = int8_map(&map_w, mm.w, mm.n, mm.k, mm.k, 128);
+  if (st != FP8Q_OK) return st;
+  st = int8_map(&map_a, mm.a, mm.m, mm.k, mm.lda, L::kRowsB);
+  if (st != FP8Q_OK) return st;
+  int bps = 0;
+  st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kTcThreads, L::kBytes, &bps);
+  if (st != FP8Q_OK) return st;
+  const int64_t grid = CG * std::min<int64_t>(p.tiles, dev.sms / CG);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(fp8q::kTcThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, map_w, map_a, p);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx", (long long)L::kBytes);
+  return FP8Q_OK;
+}
+
 template <bool F32>
 fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
                                cudaStream_t stream) {
+  if (p.m > 32) return launch_tc<2, 256, F32>(p, dev, stream);
   const unsigned gx = unsigned((p.n + fp8q::kMmTile - 1) / fp8q::kMmTile);
   const unsigned gy = unsigned(std::min<int64_t>((p.m + fp8q::kMmTile - 1) / fp8q::kMmTile, 65535));
   return launch(fp8q::int8_matmul_dp4a_kernel<F32>, dim3(gx, gy), dim3(fp8q::kMmThreads), 0,

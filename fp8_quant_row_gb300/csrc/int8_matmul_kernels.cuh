@@ -22,12 +22,19 @@ __device__ __forceinline__ float mm_value(float acc, float ws, float as, float b
   return __fmaf_rn(__fmul_rn(acc, ws), as, bias);
 }
 
+// A load and a store that keep their place in the program.
+__device__ __forceinline__ float ld_volatile(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
 template <bool F32>
-__device__ __forceinline__ void mm_store(void* out, int64_t i, float v) {
+__device__ __forceinline__ void mm_store(void* out, float v) {
   if (F32)
-    static_cast<float*>(out)[i] = v;
+    asm volatile("st.global.f32 [%0], %1;" ::"l"(out), "f"(v) : "memory");
   else
-    static_cast<uint16_t*>(out)[i] = uint16_t(pack_bf16x2(v, 0.0f));
+    asm volatile("st.global.b16 [%0], %1;" ::"l"(out), "h"(uint16_t(pack_bf16x2(v, 0.0f)))
+                 : "memory");
 }
 
 // 64 x 64 outputs per CTA of 256 threads, 4 x 4 per thread, products of four int8 by dp4a.
@@ -71,7 +78,7 @@ __global__ void __launch_bounds__(kMmThreads) int8_matmul_dp4a_kernel(MmParams p
       for (int j = 0; j < 4; ++j) {
         const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
         if (m < p.m && n < p.n)
-          mm_store<F32>(p.out, m * p.n + n,
+          mm_store<F32>(static_cast<uint8_t*>(p.out) + (m * p.n + n) * (F32 ? 4 : 2),
                         mm_value(float(acc[i][j]), p.w_scale[n], p.a_scale[m],
                                  p.bias ? __uint_as_float(uint32_t(p.bias[n]) << 16) : 0.0f));
       }

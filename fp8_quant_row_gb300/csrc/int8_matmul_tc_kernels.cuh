@@ -1,0 +1,456 @@
+// int8_matmul_tc_kernels.cuh -- the int8 product on the 5th-generation tensor cores (sm_103a).
+//
+// sm_103a has no 8-bit integer tcgen05 kind (and its legacy integer matrix instruction runs at
+// 258 products a clock and SM). An int8 is exactly an fp16, a product of two at most 2^14 and a
+// sum of 1024 products at most 2^24: tcgen05.mma kind::f16 with fp32 accumulators adds them
+// exactly. So the tiles are brought in as int8 (half the bytes), converted in the SM, multiplied
+// as fp16, and every 1024 values of k the accumulators are drained into fp32 registers
+// (exact while |sum| <= 2^24; beyond, one rounding for each drain).
+//
+// The weights' rows (output channels) are the matrix instruction's M side, tokens its N side:
+// lane = channel, column = token. CG CTAs (a pair where CG = 2) share a tile of CG * 128 channels
+// x BT tokens; each brings and converts its own 128 channels and BT / CG tokens:
+//
+//   warp 0       TMA: 128 bytes of k for 128 + BT / CG rows per stage, 128-byte swizzle
+//   warp 1       (first CTA of the pair) issues the matrix instructions
+//   warps 4-7    weights: int8 stage -> fp16 in tensor memory, thread = row
+//   warps 8-11   tokens: int8 stage -> fp16 in shared memory (128-byte swizzled K-major tiles)
+//   warps 12-19  drain the accumulators, scale, store
+//
+// Conversion of four int8: flip the sign bits (value + 128), place each byte under the fp16
+// exponent of 1024 (1024 + 128 + value, exact), subtract 1152.
+//
+// Every wait is bounded; a wait that runs out records the device error bit, the role stops, and
+// the CTA pair meets at the end, where tensor memory is freed.
+#pragma once
+
+#include <cuda.h>
+
+#include "int8_matmul_kernels.cuh"
+
+namespace fp8q {
+
+constexpr int kTcThreads = 640;
+constexpr int kTcStep = 128;        // k values per stage
+constexpr int kTcChunk = 1024;      // k values per drain
+constexpr int kTcSmemLimit = 227 * 1024;
+
+template <int CG, int BT>
+struct TcLayout {
+  static constexpr int kRowsB = BT / CG;
+  static constexpr int kRawA = 128 * kTcStep, kRawB = kRowsB * kTcStep, kRaw = kRawA + kRawB;
+  static constexpr int kConvB = kRowsB * kTcStep * 2;
+  static constexpr int kConvStages = 3;
+  static constexpr int kBarBytes = 256;
+  static constexpr int kRawStages0 = (kTcSmemLimit - 1024 - kBarBytes - kConvStages * kConvB) / kRaw;
+  static constexpr int kRawStages = kRawStages0 > 8 ? 8 : kRawStages0;
+  static constexpr int kBytes = 1024 + kRawStages * kRaw + kConvStages * kConvB + kBarBytes;
+  static constexpr int kColsA = BT;  // first column of the converted weights
+  static constexpr int kCols = BT + kConvStages * 64 <= 256 ? 256 : 512;
+  static_assert(kBytes <= kTcSmemLimit && kRawStages >= 2 && BT + kConvStages * 64 <= 512, "");
+  static_assert(8 * (2 * kRawStages + 2 * kConvStages + 3) <= kBarBytes, "");
+};
+
+// ---- instructions -------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Address of `addr` (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait whose acquire covers the other CTA's writes; reports when it runs out.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_cluster(bar, parity))
+    if (clock64() - t0 > kWaitLimitCycles) {
+      report_device_error(kDevErrWaitTimeout);
+      return false;
+    }
+  return true;
+}
+// The same for a whole warp: one answer for all lanes.
+__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity));
+}
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+  if (CG == 2)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(slot)),
+                 "r"(cols)
+                 : "memory");
+  else
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(slot)),
+                 "r"(cols)
+                 : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+  if (CG == 2) {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+  } else {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+  }
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// D += A (tensor memory) * B (shared memory), 16 values of k.
+template <int CG>
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// One arrival on `bar` (in both CTAs of a pair) once the matrix instructions so far are done.
+template <int CG>
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  if (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_addr(bar)),
+        "h"(uint16_t(3))
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+// Eight columns; the wait is part of the statement, so nothing uses the values before it.
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7])
+      : "r"(addr)
+      : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Four int8 of a word as two fp16 pairs.
+__device__ __forceinline__ void int8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+
+// ---- kernel -------------------------------------------------------------------------------
+
+struct TcParams {
+  MmParams mm;
+  int64_t tiles, tiles_n, tiles_m;  // tiles_n: of CG * 128 channels, tiles_m: of BT tokens
+  int steps;                        // ceil(k / kTcStep)
+};
+
+// Token tiles are taken in groups of up to 16, inside a group all channel tiles in order, tokens
+// fastest: the tiles at work at one time share few rows of either operand.
+__device__ __forceinline__ void tc_tile(const TcParams& p, int64_t t, int64_t& tn, int64_t& tm) {
+  const int64_t per = 16 * p.tiles_n, g = t / per, in = t - g * per;
+  const int64_t left = p.tiles_m - 16 * g, w = left < 16 ? left : 16;
+  tn = in / w;
+  tm = 16 * g + (in - tn * w);
+}
+
+template <int CG, int BT, bool F32>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    int8_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w,
+                          const __grid_constant__ CUtensorMap map_a, const TcParams p) {
+  using L = TcLayout<CG, BT>;
+  extern __shared__ uint8_t tc_smem_raw[];
+  uint8_t* smem = tc_smem_raw + ((1024u - (smem_addr(tc_smem_raw) & 1023u)) & 1023u);
+  uint8_t* raw = smem;
+  uint8_t* conv = smem + L::kRawStages * L::kRaw;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(conv + L::kConvStages * L::kConvB);
+  uint64_t* raw_full = bars;
+  uint64_t* raw_empty = raw_full + L::kRawStages;
+  uint64_t* conv_full = raw_empty + L::kRawStages;   // first CTA's counts for the pair
+  uint64_t* conv_empty = conv_full + L::kConvStages;
+  uint64_t* d_full = conv_empty + L::kConvStages;
+  uint64_t* d_empty = d_full + 1;                    // first CTA's counts for the pair
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_empty + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const int64_t first = CG == 2 ? blockIdx.x >> 1 : blockIdx.x;
+  const int64_t stride = CG == 2 ? gridDim.x >> 1 : gridDim.x;
+
+  allow_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kRawStages; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 8);
+    }
+    for (int i = 0; i < L::kConvStages; ++i) {
+      mbar_init(&conv_full[i], 8 * CG);
+      mbar_init(&conv_empty[i], 1);
+    }
+    mbar_init(d_full, 1);
+    mbar_init(d_empty, 8 * CG);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 1) tmem_alloc<CG>(tmem_slot, L::kCols);
+  tc_fence_before();
+  if (CG == 2) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  wait_for_producers();
+
+  if (warp < 4) {
+    reg_dec<32>();
+    if (warp == 0 && lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t t = first; t < p.tiles && ok; t += stride) {
+        int64_t tn, tm;
+        tc_tile(p, t, tn, tm);
+        const int yw = int(tn * (128 * CG) + rank * 128), ya = int(tm * BT + rank * L::kRowsB);
+        for (int s = 0; s < p.steps; ++s, ++it) {
+          const uint32_t st = it % L::kRawStages, use = it / L::kRawStages;
+          ok = tc_wait(&raw_empty[st], (use & 1) ^ 1);
+          if (!ok) break;
+          uint8_t* dst = raw + st * L::kRaw;
+          mbar_arrive_expect_tx(&raw_full[st], L::kRaw);
+          tma_load_2d(dst, &map_w, s * kTcStep, yw, &raw_full[st]);
+          tma_load_2d(dst + L::kRawA, &map_a, s * kTcStep, ya, &raw_full[st]);
+        }
+      }
+      // copies still in flight land before the CTA ends
+      for (uint32_t i = it > L::kRawStages ? it - L::kRawStages : 0; i < it; ++i)
+        tc_wait(&raw_full[i % L::kRawStages], (i / L::kRawStages) & 1);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // fp32 accumulators, fp16 operands, K-major, N = BT, M = CG * 128
+      constexpr uint32_t idesc = (1u << 4) | (uint32_t(BT / 8) << 17) | (uint32_t(CG * 8) << 24);
+      // 128-byte swizzle, 1024 bytes between groups of eight rows
+      constexpr uint64_t desc0 = (uint64_t(2) << 61) | (uint64_t(1) << 46) | (uint64_t(64) << 32) |
+                                 (uint64_t(1) << 16);
+      uint32_t it = 0, chunk = 0;
+      bool ok = true;
+      for (int64_t t = first; t < p.tiles && ok; t += stride) {
+        for (int s = 0; s < p.steps; ++s, ++it) {
+          if (s % (kTcChunk / kTcStep) == 0) {
+            ok = tc_wait(d_empty, (chunk & 1) ^ 1);
+            ++chunk;
+            if (!ok) break;
+          }
+          const uint32_t st = it % L::kConvStages, use = it / L::kConvStages;
+          ok = tc_wait(&conv_full[st], use & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = tmem + L::kColsA + st * 64;
+          const uint32_t b = smem_addr(conv + st * L::kConvB);
+#pragma unroll
+          for (int j = 0; j < kTcStep / 16; ++j) {
+            const uint32_t addr = b + (j / 4) * (L::kRowsB * 128) + (j % 4) * 32;
+            tc_mma<CG>(tmem, a + j * 8, desc0 | uint64_t((addr & 0x3FFFFu) >> 4), idesc,
+                       (s % (kTcChunk / kTcStep) != 0 || j != 0) ? 1u : 0u);
+          }
+          tc_commit<CG>(&conv_empty[st]);
+          if (s % (kTcChunk / kTcStep) == kTcChunk / kTcStep - 1 || s == p.steps - 1)
+            tc_commit<CG>(d_full);
+        }
+      }
+      // matrix instructions still in flight are done before tensor memory is freed
+      if (chunk > 0 && ok) tc_wait(d_full, (chunk - 1) & 1);
+    }
+  } else if (warp < 12) {
+    reg_dec<64>();
+    uint32_t it = 0;
+    bool ok = true;
+    const bool weights = warp < 8;
+    const int tid = (warp & 3) * 32 + lane;
+    const uint32_t full0 = map_rank(smem_addr(conv_full), 0);
+    for (int64_t t = first; t < p.tiles && ok; t += stride) {
+      for (int s = 0; s < p.steps; ++s, ++it) {
+        const uint32_t rs = it % L::kRawStages, cs = it % L::kConvStages;
+        ok = tc_wait_warp(&raw_full[rs], (it / L::kRawStages) & 1);
+        if (!ok) break;
+        ok = tc_wait_warp(&conv_empty[cs], ((it / L::kConvStages) & 1) ^ 1);
+        if (!ok) break;
+        if (weights) {
+          tc_fence_after();
+          const uint8_t* row = raw + rs * L::kRaw + tid * 128;
+          const uint32_t dst = tmem + L::kColsA + cs * 64 + (uint32_t(warp & 3) << 21);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint4 w = *reinterpret_cast<const uint4*>(row + (((h * 4 + c) ^ (tid & 7)) << 4));
+              int8_to_f16(w.x, v[c * 8 + 0], v[c * 8 + 1]);
+              int8_to_f16(w.y, v[c * 8 + 2], v[c * 8 + 3]);
+              int8_to_f16(w.z, v[c * 8 + 4], v[c * 8 + 5]);
+              int8_to_f16(w.w, v[c * 8 + 6], v[c * 8 + 7]);
+            }
+            tmem_store32(dst + h * 32, v);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+        } else {
+          // each thread converts kRowsB bytes of one token's 128
+          constexpr int kParts = L::kRowsB / 16;
+          const int r = tid % L::kRowsB, part = tid / L::kRowsB;
+          const uint8_t* row = raw + rs * L::kRaw + L::kRawA + r * 128;
+          uint8_t* dst = conv + cs * L::kConvB + r * 128;
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            const int c = part * kParts + i;
+            const uint4 w = *reinterpret_cast<const uint4*>(row + ((c ^ (r & 7)) << 4));
+            uint4 a, b;
+            int8_to_f16(w.x, a.x, a.y);
+            int8_to_f16(w.y, a.z, a.w);
+            int8_to_f16(w.z, b.x, b.y);
+            int8_to_f16(w.w, b.z, b.w);
+            uint8_t* at = dst + (c >> 2) * (L::kRowsB * 128);
+            *reinterpret_cast<uint4*>(at + ((((c & 3) * 2) ^ (r & 7)) << 4)) = a;
+            *reinterpret_cast<uint4*>(at + ((((c & 3) * 2 + 1) ^ (r & 7)) << 4)) = b;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[rs]);
+          if (CG == 2) mbar_arrive_cluster(full0 + cs * 8);
+          else mbar_arrive(&conv_full[cs]);
+        }
+      }
+    }
+  } else {
+    reg_inc<160>();
+    constexpr int kAcc = BT / 2;  // token columns of this warp
+    const int half = (warp - 12) >> 2, quarter = warp & 3;
+    const uint32_t src = tmem + half * kAcc + (uint32_t(quarter) << 21);
+    const uint32_t empty0 = map_rank(smem_addr(d_empty), 0);
+    uint32_t chunk = 0;
+    bool ok = true;
+    for (int64_t t = first; t < p.tiles && ok; t += stride) {
+      float acc[kAcc];
+#pragma unroll
+      for (int i = 0; i < kAcc; ++i) acc[i] = 0.0f;
+      for (int s = 0; s < p.steps; s += kTcChunk / kTcStep, ++chunk) {
+        ok = tc_wait_warp(d_full, chunk & 1);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kAcc / 8; ++c) {
+          float v[8];
+          tmem_load8(src + c * 8, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[c * 8 + i] += v[i];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2) mbar_arrive_cluster(empty0);
+          else mbar_arrive(d_empty);
+        }
+      }
+      if (!ok) break;
+      int64_t tn, tm;
+      tc_tile(p, t, tn, tm);
+      const int64_t n = tn * (128 * CG) + rank * 128 + quarter * 32 + lane;
+      const int64_t m0 = tm * BT + half * kAcc;
+      if (n < p.mm.n) {
+        const float ws = p.mm.w_scale[n];
+        const float bias = p.mm.bias ? __uint_as_float(uint32_t(p.mm.bias[n]) << 16) : 0.0f;
+        const int64_t left = p.mm.m - m0;
+        const int rows = left < kAcc ? int(left) : kAcc;
+        const float* as = p.mm.a_scale + m0;
+        uint8_t* o = static_cast<uint8_t*>(p.mm.out) + (m0 * p.mm.n + n) * (F32 ? 4 : 2);
+        const int64_t step = p.mm.n * (F32 ? 4 : 2);
+        // eight tokens at a time (volatile: the scales are not all loaded ahead, the registers
+        // hold the accumulators)
+#pragma unroll
+        for (int c = 0; c < kAcc; c += 8) {
+          float sc[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sc[i] = c + i < rows ? ld_volatile(as + c + i) : 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i, o += step)
+            if (c + i < rows) mm_store<F32>(o, mm_value(acc[c + i], ws, sc[i], bias));
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (CG == 2) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free<CG>(tmem, L::kCols);
+}
+
+}  // namespace fp8q
