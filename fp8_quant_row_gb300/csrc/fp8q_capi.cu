@@ -16,6 +16,7 @@
 
 #include "fp8q.h"
 #include "elementwise_kernels.cuh"
+#include "int8_matmul_few_kernels.cuh"
 #include "int8_matmul_kernels.cuh"
 #include "int8_matmul_tc_kernels.cuh"
 #include "nss_kernels.cuh"
@@ -394,9 +395,31 @@ fp8q_status launch_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, cudaStrea
   return FP8Q_OK;
 }
 
+template <int NT, bool F32>
+fp8q_status launch_few(const fp8q::MmParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  const int64_t groups = (p.n + 15) / 16;  // of 16 channels
+  auto* fn = fp8q::int8_matmul_few_kernel<NT, F32>;
+  const size_t smem = fp8q::few_smem_bytes<NT>();
+  int bps = 0;
+  fp8q_status st =
+      blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kFewWarps * 32, smem, &bps);
+  if (st != FP8Q_OK) return st;
+  int split = fp8q::kFewWarps;  // warps that share a group's k, each with 128 values at least
+  while (split > 1 && p.k < split * 128) split /= 2;
+  // no more CTAs than are resident at once, each with the same number of groups (one more or less
+  // by the last): they draw on the memory evenly and end together
+  const int64_t per_cta = fp8q::kFewWarps / split;
+  const int64_t rounds = (groups + dev.sms * bps * per_cta - 1) / (dev.sms * bps * per_cta);
+  const int64_t grid = (groups + rounds * per_cta - 1) / (rounds * per_cta);
+  return launch(fn, dim3(unsigned(grid)), dim3(fp8q::kFewWarps * 32), smem, stream, p, split,
+                int(rounds));
+}
+
 template <bool F32>
 fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
                                cudaStream_t stream) {
+  if (p.m <= 8) return launch_few<1, F32>(p, dev, stream);
+  if (p.m <= 16) return launch_few<2, F32>(p, dev, stream);
   if (p.m > 32) return launch_tc<2, 256, F32>(p, dev, stream);
   const unsigned gx = unsigned((p.n + fp8q::kMmTile - 1) / fp8q::kMmTile);
   const unsigned gy = unsigned(std::min<int64_t>((p.m + fp8q::kMmTile - 1) / fp8q::kMmTile, 65535));

@@ -37,6 +37,13 @@ __device__ __forceinline__ void mm_store(void* out, float v) {
                  : "memory");
 }
 
+// Four int8 of a word as two fp16 pairs.
+__device__ __forceinline__ void int8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+
 // 64 x 64 outputs per CTA of 256 threads, 4 x 4 per thread, products of four int8 by dp4a.
 constexpr int kMmTile = 64, kMmThreads = 256, kMmStep = 64;
 
