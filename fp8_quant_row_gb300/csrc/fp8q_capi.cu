@@ -357,6 +357,35 @@ fp8q_status int8_map(CUtensorMap* map, const int8_t* p, int64_t rows, int64_t k,
   return FP8Q_OK;
 }
 
+// Clusters of `size` CTAs that are resident at one time, cached per device.
+struct ClusterEntry {
+  int dev;
+  const void* fn;
+  int size, clusters;
+};
+ClusterEntry g_cluster[256];
+int g_cluster_n = 0;
+
+fp8q_status clusters_resident(const void* fn, cudaLaunchConfig_t* cfg, int size, int* clusters) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lock(g_occ_mu);
+  for (int i = 0; i < g_cluster_n; ++i)
+    if (g_cluster[i].dev == dev && g_cluster[i].fn == fn && g_cluster[i].size == size) {
+      *clusters = g_cluster[i].clusters;
+      return FP8Q_OK;
+    }
+  cfg->gridDim = dim3(unsigned(size));
+  cfg->attrs[0].val.clusterDim.x = unsigned(size);
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, fn, cfg);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters", size);
+  if (g_cluster_n < 256) g_cluster[g_cluster_n++] = ClusterEntry{dev, fn, size, n};
+  *clusters = n;
+  return FP8Q_OK;
+}
+
 template <int CG, int BT, bool F32>
 fp8q_status launch_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, cudaStream_t stream) {
   using L = fp8q::TcLayout<CG, BT>;
@@ -367,28 +396,47 @@ fp8q_status launch_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, cudaStrea
   p.tiles_m = (mm.m + BT - 1) / BT;
   p.tiles = p.tiles_n * p.tiles_m;
   p.steps = int((mm.k + fp8q::kTcStep - 1) / fp8q::kTcStep);
-  CUtensorMap map_w, map_a;
-  fp8q_status st = int8_map(&map_w, mm.w, mm.n, mm.k, mm.k, 128);
-  if (st != FP8Q_OK) return st;
-  st = int8_map(&map_a, mm.a, mm.m, mm.k, mm.lda, L::kRowsB);
-  if (st != FP8Q_OK) return st;
   int bps = 0;
-  st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kTcThreads, L::kBytes, &bps);
+  fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), L::kThreads, L::kBytes, &bps);
   if (st != FP8Q_OK) return st;
-  const int64_t grid = CG * std::min<int64_t>(p.tiles, dev.sms / CG);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(grid));
-  cfg.blockDim = dim3(fp8q::kTcThreads);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // Fewer tiles than SMs: CTAs of a cluster share a tile's k, each with two stages at least, as
+  // many as leave all clusters resident at once (a cluster stays within one GPC, so larger ones
+  // do not fill all SMs).
+  p.split = 1;
+  p.steps_per = p.steps;
+  if (CG == 1) {
+    for (int s = int(std::min<int64_t>({8, dev.sms / p.tiles, p.steps / 2})); s > 1; --s) {
+      int fit = 0;
+      st = clusters_resident(reinterpret_cast<const void*>(fn), &cfg, s, &fit);
+      if (st != FP8Q_OK) return st;
+      if (fit < p.tiles) continue;
+      p.steps_per = (p.steps + s - 1) / s;
+      p.split = (p.steps + p.steps_per - 1) / p.steps_per;
+      break;
+    }
+  }
+  const int ctas = CG == 2 ? 2 : p.split;
+  CUtensorMap map_w, map_a;
+  st = int8_map(&map_w, mm.w, mm.n, mm.k, mm.k, 128);
+  if (st != FP8Q_OK) return st;
+  st = int8_map(&map_a, mm.a, mm.m, mm.k, mm.lda, L::kRowsB);
+  if (st != FP8Q_OK) return st;
+  const int64_t grid = ctas * std::min<int64_t>(p.tiles, dev.sms / ctas);
+  cfg.gridDim = dim3(unsigned(grid));
+  attr[0].val.clusterDim.x = unsigned(ctas);
   cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, map_w, map_a, p);
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx", (long long)L::kBytes);
@@ -420,11 +468,10 @@ fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
                                cudaStream_t stream) {
   if (p.m <= 8) return launch_few<1, F32>(p, dev, stream);
   if (p.m <= 16) return launch_few<2, F32>(p, dev, stream);
-  if (p.m > 32) return launch_tc<2, 256, F32>(p, dev, stream);
-  const unsigned gx = unsigned((p.n + fp8q::kMmTile - 1) / fp8q::kMmTile);
-  const unsigned gy = unsigned(std::min<int64_t>((p.m + fp8q::kMmTile - 1) / fp8q::kMmTile, 65535));
-  return launch(fp8q::int8_matmul_dp4a_kernel<F32>, dim3(gx, gy), dim3(fp8q::kMmThreads), 0,
-                stream, p);
+  if (p.m <= 32) return launch_tc<1, 32, F32>(p, dev, stream);
+  if (p.m <= 64) return launch_tc<1, 64, F32>(p, dev, stream);
+  if (p.m <= 128) return launch_tc<1, 128, F32>(p, dev, stream);
+  return launch_tc<2, 256, F32>(p, dev, stream);
 }
 
 }  // namespace

@@ -20,7 +20,13 @@
 namespace fp8q {
 
 constexpr int kFewWarps = 8;
-constexpr int kFewStages = 4;                     // groups of 128 values of k in the ring
+#ifndef FEW_ST
+#define FEW_ST 4
+#endif
+#ifndef FEW_MB
+#define FEW_MB 3
+#endif
+constexpr int kFewStages = FEW_ST;                     // groups of 128 values of k in the ring
 constexpr int kFewStageBytes = 4 * 512;           // per warp: 16 channels x 128 values
 constexpr int kFewFlush = 1024 / 128;             // groups between drains: sums stay exact
 constexpr int kFewRing = kFewWarps * kFewStages * kFewStageBytes;
@@ -46,7 +52,7 @@ __device__ __forceinline__ void cp_async16_if(uint32_t dst, const int8_t* src, b
 
 // rounds: channel groups of 16 a team of `split` warps takes, one grid apart.
 template <int NT, bool F32>
-__global__ void __launch_bounds__(kFewWarps * 32, 3)
+__global__ void __launch_bounds__(kFewWarps * 32, FEW_MB)
     int8_matmul_few_kernel(MmParams p, int split, int rounds) {
   extern __shared__ uint4 few_smem[];
   allow_dependents();
@@ -90,6 +96,19 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3)
 #pragma unroll
   for (int i = 0; i < kFewStages - 1; ++i) fetch();
 
+  // This lane's tokens of group i, loaded one group ahead (past k the weights are zero).
+  uint4 an[2][NT];
+  auto tokens = [&](int i) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int off = k0 + i * step + h * 64;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        an[h][j] = __ldg(reinterpret_cast<const uint4*>(a[j] + (off < k ? off : 0)));
+    }
+  };
+  tokens(0);
+
   int cs = 0;
   for (int r = 0; r < rounds; ++r) {
     float sum[NT][4] = {};
@@ -97,12 +116,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3)
     for (int i = 0; i < per; ++i) {
       uint4 av[2][NT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int off = k0 + i * step + h * 64;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)  // (past k the weights are zero)
-          av[h][j] = __ldg(reinterpret_cast<const uint4*>(a[j] + (off < k ? off : 0)));
-      }
+        for (int j = 0; j < NT; ++j) av[h][j] = an[h][j];
+      tokens(i + 1 < per ? i + 1 : 0);
       fetch();
       cp_async_wait<kFewStages - 1>();
       const uint4* stage = ring + cs * (kFewStageBytes / 16);

@@ -22,12 +22,7 @@ __device__ __forceinline__ float mm_value(float acc, float ws, float as, float b
   return __fmaf_rn(__fmul_rn(acc, ws), as, bias);
 }
 
-// A load and a store that keep their place in the program.
-__device__ __forceinline__ float ld_volatile(const float* p) {
-  float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
-  return v;
-}
+// A store that keeps its place in the program.
 template <bool F32>
 __device__ __forceinline__ void mm_store(void* out, float v) {
   if (F32)

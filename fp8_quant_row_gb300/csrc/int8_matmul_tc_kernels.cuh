@@ -8,14 +8,20 @@
 // (exact while |sum| <= 2^24; beyond, one rounding for each drain).
 //
 // The weights' rows (output channels) are the matrix instruction's M side, tokens its N side:
-// lane = channel, column = token. CG CTAs (a pair where CG = 2) share a tile of CG * 128 channels
-// x BT tokens; each brings and converts its own 128 channels and BT / CG tokens:
+// lane = channel, column = token. A tile is CG * 128 channels x BT tokens:
 //
-//   warp 0       TMA: 128 bytes of k for 128 + BT / CG rows per stage, 128-byte swizzle
-//   warp 1       (first CTA of the pair) issues the matrix instructions
-//   warps 4-7    weights: int8 stage -> fp16 in tensor memory, thread = row
-//   warps 8-11   tokens: int8 stage -> fp16 in shared memory (128-byte swizzled K-major tiles)
-//   warps 12-19  drain the accumulators, scale, store
+//   CG = 2   a pair of CTAs shares a tile; each brings and converts its own 128 channels and half
+//            the tokens (half the operand traffic per product; for many tokens)
+//   CG = 1   one CTA; a cluster of `split` CTAs shares the tile's k where there are fewer tiles
+//            than SMs, and exchanges partial sums at the end (for few tokens, where bringing the
+//            weights in is what counts)
+//
+//   warpgroup 0          warp 0: TMA, 128 bytes of k for 128 + BT / CG rows per stage, 128-byte
+//                        swizzle; warp 1 (first CTA of a pair): issues the matrix instructions
+//   kGroupsA warpgroups  weights: int8 stage -> fp16 in tensor memory, thread = row; where there
+//                        are two they take stages in turn
+//   one warpgroup        tokens: int8 stage -> fp16 in shared memory (128-byte swizzled K-major)
+//   two warpgroups       drain the accumulators, scale, store
 //
 // Conversion of four int8: flip the sign bits (value + 128), place each byte under the fp16
 // exponent of 1024 (1024 + 128 + value, exact), subtract 1152.
@@ -30,25 +36,34 @@
 
 namespace fp8q {
 
-constexpr int kTcThreads = 640;
 constexpr int kTcStep = 128;        // k values per stage
 constexpr int kTcChunk = 1024;      // k values per drain
 constexpr int kTcSmemLimit = 227 * 1024;
 
 template <int CG, int BT>
 struct TcLayout {
+  static constexpr int kGroupsA = CG == 2 ? 1 : 2;
+  static constexpr int kThreads = 128 * (kGroupsA + 4);
+  // registers a thread: the roles' shares of what the launch gives (96 x 640 or 80 x 768)
+  static constexpr int kRegsIssue = CG == 2 ? 32 : 40, kRegsConvert = 64;
+  static constexpr int kRegsDrain = CG == 2 ? 160 : 120;
+  static_assert(kRegsIssue + (kGroupsA + 1) * kRegsConvert + 2 * kRegsDrain <= 480, "");
   static constexpr int kRowsB = BT / CG;
   static constexpr int kRawA = 128 * kTcStep, kRawB = kRowsB * kTcStep, kRaw = kRawA + kRawB;
   static constexpr int kConvB = kRowsB * kTcStep * 2;
   static constexpr int kConvStages = 3;
   static constexpr int kBarBytes = 256;
-  static constexpr int kRawStages0 = (kTcSmemLimit - 1024 - kBarBytes - kConvStages * kConvB) / kRaw;
-  static constexpr int kRawStages = kRawStages0 > 8 ? 8 : kRawStages0;
-  static constexpr int kBytes = 1024 + kRawStages * kRaw + kConvStages * kConvB + kBarBytes;
+  static constexpr int kScaleBytes = 8 * (BT / 2) * 4;  // each draining warp's token scales
+  static constexpr int kRawStages0 =
+      (kTcSmemLimit - 1024 - kBarBytes - kScaleBytes - kConvStages * kConvB) / kRaw;
+  static constexpr int kRawStages = kRawStages0 > 10 ? 10 : kRawStages0;
+  static constexpr int kBytes = 1024 + kRawStages * kRaw + kConvStages * kConvB + kBarBytes + kScaleBytes;
   static constexpr int kColsA = BT;  // first column of the converted weights
   static constexpr int kCols = BT + kConvStages * 64 <= 256 ? 256 : 512;
+  // partial sums, sent and got, over the stages (free by then)
+  static_assert(CG == 2 || (2 * BT + 8) * 512 <= kRawStages * kRaw + kConvStages * kConvB, "");
   static_assert(kBytes <= kTcSmemLimit && kRawStages >= 2 && BT + kConvStages * 64 <= 512, "");
-  static_assert(8 * (2 * kRawStages + 2 * kConvStages + 3) <= kBarBytes, "");
+  static_assert(8 * (2 * kRawStages + 2 * kConvStages + 6) <= kBarBytes, "");
 };
 
 // ---- instructions -------------------------------------------------------------------------
@@ -65,8 +80,17 @@ __device__ __forceinline__ void cluster_sync() {
 // Address of `addr` (this CTA's shared memory) in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
+}
+// `bytes` of this CTA's shared memory to another's, counted by that CTA's barrier.
+__device__ __forceinline__ void bulk_send(uint32_t cluster_dst, uint32_t src, uint32_t bytes,
+                                          uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+      "[%3];" ::"r"(cluster_dst),
+      "r"(src), "r"(bytes), "r"(cluster_bar)
+      : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
@@ -181,6 +205,14 @@ __device__ __forceinline__ void tmem_load8(uint32_t addr, float (&v)[8]) {
       : "memory");
 }
 
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -196,6 +228,7 @@ struct TcParams {
   MmParams mm;
   int64_t tiles, tiles_n, tiles_m;  // tiles_n: of CG * 128 channels, tiles_m: of BT tokens
   int steps;                        // ceil(k / kTcStep)
+  int split, steps_per;             // CG = 1: CTAs that share a tile's k, stages of each
 };
 
 // Token tiles are taken in groups of up to 16, inside a group all channel tiles in order, tokens
@@ -208,7 +241,7 @@ __device__ __forceinline__ void tc_tile(const TcParams& p, int64_t t, int64_t& t
 }
 
 template <int CG, int BT, bool F32>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(TcLayout<CG, BT>::kThreads, 1)
     int8_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w,
                           const __grid_constant__ CUtensorMap map_a, const TcParams p) {
   using L = TcLayout<CG, BT>;
@@ -223,12 +256,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* conv_empty = conv_full + L::kConvStages;
   uint64_t* d_full = conv_empty + L::kConvStages;
   uint64_t* d_empty = d_full + 1;                    // first CTA's counts for the pair
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_empty + 1);
+  uint64_t* peers_ready = d_empty + 1;               // CG = 1: the others' stages are free
+  uint64_t* sums_full = peers_ready + 1;             // CG = 1: the others' sums are here
+  uint64_t* sums_laid = sums_full + 1;               // CG = 1: this CTA's sums are in its memory
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums_laid + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-  const int64_t first = CG == 2 ? blockIdx.x >> 1 : blockIdx.x;
-  const int64_t stride = CG == 2 ? gridDim.x >> 1 : gridDim.x;
+  const uint32_t rank = cluster_rank();
+  const uint32_t half = CG == 2 ? rank : 0u;         // which 128 channels and tokens of the tile
+  const int ctas = CG == 2 ? 2 : p.split;
+  const int64_t first = blockIdx.x / unsigned(ctas), stride = gridDim.x / unsigned(ctas);
+  const int s0 = CG == 2 ? 0 : int(rank) * p.steps_per;
+  const int steps = CG == 2 ? p.steps : min(p.steps_per, p.steps - s0);
 
   allow_dependents();
   if (threadIdx.x == 0) {
@@ -242,40 +281,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     mbar_init(d_full, 1);
     mbar_init(d_empty, 8 * CG);
+    mbar_init(peers_ready, CG == 1 && ctas > 1 ? ctas - 1 : 1);
+    mbar_init(sums_full, 1);
+    mbar_init(sums_laid, 8);
     fence_mbar_init();
   }
   __syncwarp();
   if (warp == 1) tmem_alloc<CG>(tmem_slot, L::kCols);
   tc_fence_before();
-  if (CG == 2) cluster_sync();
+  if (ctas > 1) cluster_sync();
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   wait_for_producers();
 
   if (warp < 4) {
-    reg_dec<32>();
+    reg_dec<L::kRegsIssue>();
     if (warp == 0 && lane == 0) {
       uint32_t it = 0;
       bool ok = true;
       for (int64_t t = first; t < p.tiles && ok; t += stride) {
         int64_t tn, tm;
         tc_tile(p, t, tn, tm);
-        const int yw = int(tn * (128 * CG) + rank * 128), ya = int(tm * BT + rank * L::kRowsB);
-        for (int s = 0; s < p.steps; ++s, ++it) {
+        const int yw = int(tn * (128 * CG) + half * 128), ya = int(tm * BT + half * L::kRowsB);
+        for (int s = 0; s < steps; ++s, ++it) {
           const uint32_t st = it % L::kRawStages, use = it / L::kRawStages;
           ok = tc_wait(&raw_empty[st], (use & 1) ^ 1);
           if (!ok) break;
           uint8_t* dst = raw + st * L::kRaw;
           mbar_arrive_expect_tx(&raw_full[st], L::kRaw);
-          tma_load_2d(dst, &map_w, s * kTcStep, yw, &raw_full[st]);
-          tma_load_2d(dst + L::kRawA, &map_a, s * kTcStep, ya, &raw_full[st]);
+          tma_load_2d(dst, &map_w, (s0 + s) * kTcStep, yw, &raw_full[st]);
+          tma_load_2d(dst + L::kRawA, &map_a, (s0 + s) * kTcStep, ya, &raw_full[st]);
         }
       }
       // copies still in flight land before the CTA ends
       for (uint32_t i = it > L::kRawStages ? it - L::kRawStages : 0; i < it; ++i)
         tc_wait(&raw_full[i % L::kRawStages], (i / L::kRawStages) & 1);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && lane == 0 && half == 0) {
       // fp32 accumulators, fp16 operands, K-major, N = BT, M = CG * 128
       constexpr uint32_t idesc = (1u << 4) | (uint32_t(BT / 8) << 17) | (uint32_t(CG * 8) << 24);
       // 128-byte swizzle, 1024 bytes between groups of eight rows
@@ -284,7 +326,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint32_t it = 0, chunk = 0;
       bool ok = true;
       for (int64_t t = first; t < p.tiles && ok; t += stride) {
-        for (int s = 0; s < p.steps; ++s, ++it) {
+        for (int s = 0; s < steps; ++s, ++it) {
           if (s % (kTcChunk / kTcStep) == 0) {
             ok = tc_wait(d_empty, (chunk & 1) ^ 1);
             ++chunk;
@@ -303,22 +345,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                        (s % (kTcChunk / kTcStep) != 0 || j != 0) ? 1u : 0u);
           }
           tc_commit<CG>(&conv_empty[st]);
-          if (s % (kTcChunk / kTcStep) == kTcChunk / kTcStep - 1 || s == p.steps - 1)
+          if (s % (kTcChunk / kTcStep) == kTcChunk / kTcStep - 1 || s == steps - 1)
             tc_commit<CG>(d_full);
         }
       }
       // matrix instructions still in flight are done before tensor memory is freed
       if (chunk > 0 && ok) tc_wait(d_full, (chunk - 1) & 1);
     }
-  } else if (warp < 12) {
-    reg_dec<64>();
+  } else if (warp < 8 + 4 * L::kGroupsA) {
+    reg_dec<L::kRegsConvert>();
     uint32_t it = 0;
     bool ok = true;
-    const bool weights = warp < 8;
+    const bool weights = warp < 4 + 4 * L::kGroupsA;
     const int tid = (warp & 3) * 32 + lane;
-    const uint32_t full0 = map_rank(smem_addr(conv_full), 0);
+    const uint32_t full0 = map_rank(smem_addr(conv_full), rank - half);
     for (int64_t t = first; t < p.tiles && ok; t += stride) {
-      for (int s = 0; s < p.steps; ++s, ++it) {
+      for (int s = 0; s < steps; ++s, ++it) {
+        if (L::kGroupsA == 2 && weights && int(it & 1) != (warp - 4) / 4) continue;
         const uint32_t rs = it % L::kRawStages, cs = it % L::kConvStages;
         ok = tc_wait_warp(&raw_full[rs], (it / L::kRawStages) & 1);
         if (!ok) break;
@@ -333,7 +376,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint32_t v[32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint4 w = *reinterpret_cast<const uint4*>(row + (((h * 4 + c) ^ (tid & 7)) << 4));
+              const uint4 w =
+                  *reinterpret_cast<const uint4*>(row + (((h * 4 + c) ^ (tid & 7)) << 4));
               int8_to_f16(w.x, v[c * 8 + 0], v[c * 8 + 1]);
               int8_to_f16(w.y, v[c * 8 + 2], v[c * 8 + 3]);
               int8_to_f16(w.z, v[c * 8 + 4], v[c * 8 + 5]);
@@ -373,18 +417,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   } else {
-    reg_inc<160>();
+    reg_inc<L::kRegsDrain>();
     constexpr int kAcc = BT / 2;  // token columns of this warp
-    const int half = (warp - 12) >> 2, quarter = warp & 3;
-    const uint32_t src = tmem + half * kAcc + (uint32_t(quarter) << 21);
-    const uint32_t empty0 = map_rank(smem_addr(d_empty), 0);
+    const int side = (warp - 8 - 4 * L::kGroupsA) >> 2, quarter = warp & 3;
+    const uint32_t src = tmem + side * kAcc + (uint32_t(quarter) << 21);
+    const uint32_t empty0 = map_rank(smem_addr(d_empty), rank - half);
     uint32_t chunk = 0;
     bool ok = true;
+    float* scales = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + L::kBarBytes) +
+                    (warp - 8 - 4 * L::kGroupsA) * kAcc;
     for (int64_t t = first; t < p.tiles && ok; t += stride) {
+      int64_t tn, tm;
+      tc_tile(p, t, tn, tm);
+      const int64_t n = tn * (128 * CG) + half * 128 + quarter * 32 + lane;
+      const int64_t m0 = tm * BT + side * kAcc, left = p.mm.m - m0;
+      // the scales while the products run
+      __syncwarp();
+      for (int i = lane; i < kAcc; i += 32) scales[i] = i < left ? p.mm.a_scale[m0 + i] : 0.0f;
+      __syncwarp();
+      float ws = 0.0f, bias = 0.0f;
+      if (n < p.mm.n) {
+        ws = p.mm.w_scale[n];
+        if (p.mm.bias) bias = __uint_as_float(uint32_t(p.mm.bias[n]) << 16);
+      }
       float acc[kAcc];
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) acc[i] = 0.0f;
-      for (int s = 0; s < p.steps; s += kTcChunk / kTcStep, ++chunk) {
+      for (int s = 0; s < steps; s += kTcChunk / kTcStep, ++chunk) {
         ok = tc_wait_warp(d_full, chunk & 1);
         if (!ok) break;
         tc_fence_after();
@@ -403,35 +462,72 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       if (!ok) break;
-      int64_t tn, tm;
-      tc_tile(p, t, tn, tm);
-      const int64_t n = tn * (128 * CG) + rank * 128 + quarter * 32 + lane;
-      const int64_t m0 = tm * BT + half * kAcc;
-      if (n < p.mm.n) {
-        const float ws = p.mm.w_scale[n];
-        const float bias = p.mm.bias ? __uint_as_float(uint32_t(p.mm.bias[n]) << 16) : 0.0f;
-        const int64_t left = p.mm.m - m0;
-        const int rows = left < kAcc ? int(left) : kAcc;
-        const float* as = p.mm.a_scale + m0;
-        uint8_t* o = static_cast<uint8_t*>(p.mm.out) + (m0 * p.mm.n + n) * (F32 ? 4 : 2);
-        const int64_t step = p.mm.n * (F32 ? 4 : 2);
-        // eight tokens at a time (volatile: the scales are not all loaded ahead, the registers
-        // hold the accumulators)
+      uint8_t* const o0 = static_cast<uint8_t*>(p.mm.out) + (m0 * p.mm.n + n) * (F32 ? 4 : 2);
+      const int64_t step = p.mm.n * (F32 ? 4 : 2);
+      if (CG == 1 && ctas > 1) {
+        // The cluster has one tile. Each CTA finishes `per` of its columns. It lays its sums out
+        // as [column][channel] over its stages (free once all its products are in, as the last
+        // drain says), sends each other CTA that one's columns (in one bulk copy, once that one
+        // says that its stages are free) and gets its own columns as [CTA][column][channel].
+        // (Loops that stay loops: this code runs once, and its instructions come from memory;
+        // unrolled over the columns it took 26 us at 128 tokens.)
+        constexpr int kFirst = 8 + 4 * L::kGroupsA;
+        const int cols = min(BT, int(p.mm.m - tm * BT)), per = (cols + ctas - 1) / ctas;
+        const int own0 = min(int(rank) * per, cols), own1 = min(own0 + per, cols);
+        const uint32_t send = smem_addr(raw), get = send + BT * 512;
+        const uint32_t at = (quarter * 32 + lane) * 4;
+        if (warp == kFirst && lane == 0)
+          mbar_arrive_expect_tx(sums_full, uint32_t((ctas - 1) * (own1 - own0) * 512));
 #pragma unroll
-        for (int c = 0; c < kAcc; c += 8) {
-          float sc[8];
+        for (int c = 0; c < kAcc; ++c) sts_f32(send + (side * kAcc + c) * 512 + at, acc[c]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sums_laid);
+        ok = tc_wait_warp(sums_laid, 0);
+        if (warp == kFirst) {
+          if (lane < ctas && lane != int(rank))
+            mbar_arrive_cluster(map_rank(smem_addr(peers_ready), lane));
+          ok = tc_wait_warp(peers_ready, 0) && ok;
+          const int to0 = min(lane * per, cols), to1 = min(to0 + per, cols);
+          if (ok && lane < ctas && lane != int(rank) && to1 > to0)
+            bulk_send(map_rank(get + uint32_t(int(rank) * per * 512), lane), send + to0 * 512,
+                      uint32_t((to1 - to0) * 512), map_rank(smem_addr(sums_full), lane));
+        }
+        ok = tc_wait_warp(sums_full, 0) && ok;
+        if (!ok) break;
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        if (n < p.mm.n) {
+          uint8_t* o = o0 + (own0 + side - side * kAcc) * step;
+#pragma unroll 1
+          for (int col = own0 + side; col < own1; col += 2, o += 2 * step) {
+            float v = 0.0f;  // in the order of k
+#pragma unroll 4
+            for (int r = 0; r < ctas; ++r)
+              v += lds_f32((r == int(rank) ? send + uint32_t(col * 512)
+                                           : get + uint32_t((r * per + col - own0) * 512)) + at);
+            // the scale as the warp of this quarter and the column's side has it
+            const float as = scales[(col / kAcc - side) * 4 * kAcc + col % kAcc];
+            mm_store<F32>(o, mm_value(v, ws, as, bias));
+          }
+        }
+      } else if (n < p.mm.n) {
+        uint8_t* o = o0;
+        const int cols = left < kAcc ? int(left) : kAcc;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sc[i] = c + i < rows ? ld_volatile(as + c + i) : 0.0f;
+        for (int c = 0; c < kAcc; c += 4) {
+          const float4 sc = lds128(reinterpret_cast<const float4*>(scales + c));
 #pragma unroll
-          for (int i = 0; i < 8; ++i, o += step)
-            if (c + i < rows) mm_store<F32>(o, mm_value(acc[c + i], ws, sc[i], bias));
+          for (int i = 0; i < 4; ++i, o += step)
+            if (c + i < cols)
+              mm_store<F32>(o, mm_value(acc[c + i], ws,
+                                        i == 0 ? sc.x : i == 1 ? sc.y : i == 2 ? sc.z : sc.w, bias));
         }
       }
     }
   }
   __syncwarp();
   tc_fence_before();
-  if (CG == 2) cluster_sync();
+  if (ctas > 1) cluster_sync();
   else __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_free<CG>(tmem, L::kCols);
