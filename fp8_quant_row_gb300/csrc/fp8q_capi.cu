@@ -231,11 +231,11 @@ fp8q_status launch_ws(const fp8q::NssParams& p, const DeviceInfo& dev, int64_t n
   if (n_mod > grid) return FP8Q_OK;  // every CTA must sit inside one modulation group
   if (L::kSmemBytes > size_t(dev.smem_optin)) return FP8Q_OK;
   int bps = 0;
-  fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), L::kThreads, L::kSmemBytes, &bps);
+  fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kTcThreads, L::kSmemBytes, &bps);
   if (st != FP8Q_OK) return st;
   if (bps <= 0) return FP8Q_OK;
   *launched = true;
-  return launch(fn, dim3(unsigned(grid)), dim3(L::kThreads), L::kSmemBytes, stream, p, n_mod,
+  return launch(fn, dim3(unsigned(grid)), dim3(fp8q::kTcThreads), L::kSmemBytes, stream, p, n_mod,
                 kWsDepth);
 }
 
@@ -366,23 +366,77 @@ struct ClusterEntry {
 ClusterEntry g_cluster[256];
 int g_cluster_n = 0;
 
-fp8q_status clusters_resident(const void* fn, cudaLaunchConfig_t* cfg, int size, int* clusters) {
+fp8q_status clusters_resident(const void* fn, int threads, size_t smem, int size, int* clusters) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  int bps = 0;
+  const fp8q_status st = blocks_per_sm(fn, threads, smem, &bps);  // raises the smem limit
+  if (st != FP8Q_OK) return st;
   std::lock_guard<std::mutex> lock(g_occ_mu);
   for (int i = 0; i < g_cluster_n; ++i)
     if (g_cluster[i].dev == dev && g_cluster[i].fn == fn && g_cluster[i].size == size) {
       *clusters = g_cluster[i].clusters;
       return FP8Q_OK;
     }
-  cfg->gridDim = dim3(unsigned(size));
-  cfg->attrs[0].val.clusterDim.x = unsigned(size);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = unsigned(size);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(size));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, fn, cfg);
+  e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
   if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters", size);
   if (g_cluster_n < 256) g_cluster[g_cluster_n++] = ClusterEntry{dev, fn, size, n};
   *clusters = n;
+  return FP8Q_OK;
+}
+
+// Tiles of a CG x BT kernel for this product and an estimate of its time in us: rounds of tiles
+// times a tile's stages, plus a launch's fixed part (kTcStage and kTcFixed, fitted to 13 token counts
+// at five weight shapes; within about 10% of each measurement there).
+constexpr double kTcFixed = 4.0, kTcExchange = 4.0;  // the exchange and 0.03 a token column
+
+template <int CG, int BT>
+constexpr double tc_stage_us() {
+  return CG == 2 ? (BT == 256 ? 0.66 : 0.43) : BT == 128 ? 0.50 : BT == 64 ? 0.41 : 0.37;
+}
+
+template <int CG, int BT, bool F32>
+fp8q_status plan_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, fp8q::TcParams* p,
+                    double* cost) {
+  using L = fp8q::TcLayout<CG, BT>;
+  p->tiles_n = (mm.n + 128 * CG - 1) / (128 * CG);
+  p->tiles_m = (mm.m + BT - 1) / BT;
+  p->tiles = p->tiles_n * p->tiles_m;
+  p->steps = int((mm.k + fp8q::kTcStep - 1) / fp8q::kTcStep);
+  p->split = 1;
+  p->steps_per = p->steps;
+  // Fewer tiles than SMs: CTAs of a cluster share a tile's k, each with two stages at least, as
+  // many as leave all clusters resident at once (a cluster stays within one GPC, so larger ones
+  // do not fill all SMs: 46 of three CTAs, 36 of four, 15 of eight).
+  if (CG == 1) {
+    const void* fn = reinterpret_cast<const void*>(fp8q::int8_matmul_tc_kernel<CG, BT, F32>);
+    for (int s = int(std::min<int64_t>({8, dev.sms / p->tiles, p->steps / 2})); s > 1; --s) {
+      int fit = 0;
+      const fp8q_status st = clusters_resident(fn, fp8q::kTcThreads, L::kBytes, s, &fit);
+      if (st != FP8Q_OK) return st;
+      if (fit < p->tiles) continue;
+      p->steps_per = (p->steps + s - 1) / s;
+      p->split = (p->steps + p->steps_per - 1) / p->steps_per;
+      break;
+    }
+  }
+  const int64_t slots = dev.sms / CG;
+  const double rounds = p->split > 1 ? 1.0 : double((p->tiles + slots - 1) / slots);
+  *cost = rounds * p->steps_per * tc_stage_us<CG, BT>() + kTcFixed +
+          (p->split > 1 ? kTcExchange + 0.03 * double(std::min<int64_t>(mm.m, BT)) : 0.0);
   return FP8Q_OK;
 }
 
@@ -391,43 +445,13 @@ fp8q_status launch_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, cudaStrea
   using L = fp8q::TcLayout<CG, BT>;
   auto* fn = fp8q::int8_matmul_tc_kernel<CG, BT, F32>;
   fp8q::TcParams p;
-  p.mm = mm;
-  p.tiles_n = (mm.n + 128 * CG - 1) / (128 * CG);
-  p.tiles_m = (mm.m + BT - 1) / BT;
-  p.tiles = p.tiles_n * p.tiles_m;
-  p.steps = int((mm.k + fp8q::kTcStep - 1) / fp8q::kTcStep);
-  int bps = 0;
-  fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), L::kThreads, L::kBytes, &bps);
+  double cost = 0.0;
+  fp8q_status st = plan_tc<CG, BT, F32>(mm, dev, &p, &cost);
   if (st != FP8Q_OK) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(L::kThreads);
-  cfg.dynamicSmemBytes = L::kBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  // Fewer tiles than SMs: CTAs of a cluster share a tile's k, each with two stages at least, as
-  // many as leave all clusters resident at once (a cluster stays within one GPC, so larger ones
-  // do not fill all SMs).
-  p.split = 1;
-  p.steps_per = p.steps;
-  if (CG == 1) {
-    for (int s = int(std::min<int64_t>({8, dev.sms / p.tiles, p.steps / 2})); s > 1; --s) {
-      int fit = 0;
-      st = clusters_resident(reinterpret_cast<const void*>(fn), &cfg, s, &fit);
-      if (st != FP8Q_OK) return st;
-      if (fit < p.tiles) continue;
-      p.steps_per = (p.steps + s - 1) / s;
-      p.split = (p.steps + p.steps_per - 1) / p.steps_per;
-      break;
-    }
-  }
+  int bps = 0;
+  st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kTcThreads, L::kBytes, &bps);
+  if (st != FP8Q_OK) return st;
+  p.mm = mm;
   const int ctas = CG == 2 ? 2 : p.split;
   CUtensorMap map_w, map_a;
   st = int8_map(&map_w, mm.w, mm.n, mm.k, mm.k, 128);
@@ -435,8 +459,19 @@ fp8q_status launch_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, cudaStrea
   st = int8_map(&map_a, mm.a, mm.m, mm.k, mm.lda, L::kRowsB);
   if (st != FP8Q_OK) return st;
   const int64_t grid = ctas * std::min<int64_t>(p.tiles, dev.sms / ctas);
+  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(fp8q::kTcThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = unsigned(ctas);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
   cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, map_w, map_a, p);
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx", (long long)L::kBytes);
@@ -463,15 +498,51 @@ fp8q_status launch_few(const fp8q::MmParams& p, const DeviceInfo& dev, cudaStrea
                 int(rounds));
 }
 
+template <int CG, int BT, bool F32>
+fp8q_status consider_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, double* best, int* which) {
+  fp8q::TcParams p;
+  double cost = 0.0;
+  const fp8q_status st = plan_tc<CG, BT, F32>(mm, dev, &p, &cost);
+  if (st == FP8Q_OK && cost < *best) *best = cost, *which = CG * 1000 + BT;
+  return st;
+}
+
+// The kernel with the least estimated time. Measured at 6144 x 6144 weights (us; 8 and 16: the
+// kernel for few tokens, CGxBT: the tensor-memory kernel):
+//   tokens      8     16   1x32   1x64  1x128  2x128  2x256
+//        8   10.5   14.6   13.6   15.0   18.0   23.1   35.2
+//       32                 14.4   15.8   17.4   23.4   35.9
+//       64                 20.3   16.9   18.5   23.8   36.0
+//      128                 37.0   23.0   21.0   24.0   36.1
+//      256                 53.9   41.6   25.9   24.4   36.3
+//     1024                186.3  115.9   69.9   63.2   67.3
+//     4608                769.9  438.4  266.9  238.8  196.3
+// and with 36864 x 6144 weights 8 tokens take 43.7 / 51.6 / 39.8 us (8, 16, 1x32), 128 tokens
+// 52.0 / 47.7 / 70.1 us (1x128, 2x128, 2x256).
 template <bool F32>
 fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
                                cudaStream_t stream) {
-  if (p.m <= 8) return launch_few<1, F32>(p, dev, stream);
-  if (p.m <= 16) return launch_few<2, F32>(p, dev, stream);
-  if (p.m <= 32) return launch_tc<1, 32, F32>(p, dev, stream);
-  if (p.m <= 64) return launch_tc<1, 64, F32>(p, dev, stream);
-  if (p.m <= 128) return launch_tc<1, 128, F32>(p, dev, stream);
-  return launch_tc<2, 256, F32>(p, dev, stream);
+  double best = 1e30;
+  int which = 0;
+  const double weights = double(p.n) * double(p.k);
+  if (p.m <= 8) best = 3.0 + weights / 5.9e6, which = 8;
+  else if (p.m <= 16) best = 3.0 + weights / 3.6e6, which = 16;
+  fp8q_status st = FP8Q_OK;
+  if (p.m <= 64) st = consider_tc<1, 32, F32>(p, dev, &best, &which);
+  if (st == FP8Q_OK && p.m > 32 && p.m <= 128) st = consider_tc<1, 64, F32>(p, dev, &best, &which);
+  if (st == FP8Q_OK && p.m > 64 && p.m <= 512) st = consider_tc<1, 128, F32>(p, dev, &best, &which);
+  if (st == FP8Q_OK && p.m > 64) st = consider_tc<2, 128, F32>(p, dev, &best, &which);
+  if (st == FP8Q_OK && p.m > 128) st = consider_tc<2, 256, F32>(p, dev, &best, &which);
+  if (st != FP8Q_OK) return st;
+  switch (which) {
+    case 8: return launch_few<1, F32>(p, dev, stream);
+    case 16: return launch_few<2, F32>(p, dev, stream);
+    case 1032: return launch_tc<1, 32, F32>(p, dev, stream);
+    case 1064: return launch_tc<1, 64, F32>(p, dev, stream);
+    case 1128: return launch_tc<1, 128, F32>(p, dev, stream);
+    case 2128: return launch_tc<2, 128, F32>(p, dev, stream);
+    default: return launch_tc<2, 256, F32>(p, dev, stream);
+  }
 }
 
 }  // namespace

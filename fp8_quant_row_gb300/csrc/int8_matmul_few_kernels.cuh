@@ -20,13 +20,7 @@
 namespace fp8q {
 
 constexpr int kFewWarps = 8;
-#ifndef FEW_ST
-#define FEW_ST 4
-#endif
-#ifndef FEW_MB
-#define FEW_MB 3
-#endif
-constexpr int kFewStages = FEW_ST;                     // groups of 128 values of k in the ring
+constexpr int kFewStages = 4;                     // groups of 128 values of k in the ring
 constexpr int kFewStageBytes = 4 * 512;           // per warp: 16 channels x 128 values
 constexpr int kFewFlush = 1024 / 128;             // groups between drains: sums stay exact
 constexpr int kFewRing = kFewWarps * kFewStages * kFewStageBytes;
@@ -52,7 +46,7 @@ __device__ __forceinline__ void cp_async16_if(uint32_t dst, const int8_t* src, b
 
 // rounds: channel groups of 16 a team of `split` warps takes, one grid apart.
 template <int NT, bool F32>
-__global__ void __launch_bounds__(kFewWarps * 32, FEW_MB)
+__global__ void __launch_bounds__(kFewWarps * 32, 3)
     int8_matmul_few_kernel(MmParams p, int split, int rounds) {
   extern __shared__ uint4 few_smem[];
   allow_dependents();

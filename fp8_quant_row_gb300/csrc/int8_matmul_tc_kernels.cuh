@@ -18,10 +18,11 @@
 //
 //   warpgroup 0          warp 0: TMA, 128 bytes of k for 128 + BT / CG rows per stage, 128-byte
 //                        swizzle; warp 1 (first CTA of a pair): issues the matrix instructions
-//   kGroupsA warpgroups  weights: int8 stage -> fp16 in tensor memory, thread = row; where there
-//                        are two they take stages in turn
-//   one warpgroup        tokens: int8 stage -> fp16 in shared memory (128-byte swizzled K-major)
-//   two warpgroups       drain the accumulators, scale, store
+//   warpgroups 1, 2      weights: int8 stage -> fp16 in tensor memory, thread = row; they take
+//                        stages in turn
+//   warpgroups 3, 4      tokens: int8 stage -> fp16 in shared memory (128-byte swizzled K-major),
+//                        in turn
+//   warpgroups 5, 6      drain the accumulators, scale, store
 //
 // Conversion of four int8: flip the sign bits (value + 128), place each byte under the fp16
 // exponent of 1024 (1024 + 128 + value, exact), subtract 1152.
@@ -38,31 +39,31 @@ namespace fp8q {
 
 constexpr int kTcStep = 128;        // k values per stage
 constexpr int kTcChunk = 1024;      // k values per drain
+constexpr int kTcThreads = 896;
+constexpr int kTcFirstDrain = 20;   // first of the draining warps
 constexpr int kTcSmemLimit = 227 * 1024;
 
 template <int CG, int BT>
 struct TcLayout {
-  static constexpr int kGroupsA = CG == 2 ? 1 : 2;
-  static constexpr int kThreads = 128 * (kGroupsA + 4);
-  // registers a thread: the roles' shares of what the launch gives (96 x 640 or 80 x 768)
-  static constexpr int kRegsIssue = CG == 2 ? 32 : 40, kRegsConvert = 64;
-  static constexpr int kRegsDrain = CG == 2 ? 160 : 120;
-  static_assert(kRegsIssue + (kGroupsA + 1) * kRegsConvert + 2 * kRegsDrain <= 480, "");
+  // registers a thread: the roles' shares of what the launch gives (72 x 896 threads)
+  static constexpr int kRegsIssue = 40, kRegsConvert = BT > 128 ? 40 : 64;
+  static constexpr int kRegsDrain = BT > 128 ? 152 : 104;
+  static_assert(kRegsIssue + 4 * kRegsConvert + 2 * kRegsDrain <= 7 * 72, "");
   static constexpr int kRowsB = BT / CG;
   static constexpr int kRawA = 128 * kTcStep, kRawB = kRowsB * kTcStep, kRaw = kRawA + kRawB;
   static constexpr int kConvB = kRowsB * kTcStep * 2;
   static constexpr int kConvStages = 3;
   static constexpr int kBarBytes = 256;
-  static constexpr int kScaleBytes = 8 * (BT / 2) * 4;  // each draining warp's token scales
+  static constexpr int kScaleBytes = 2 * BT * 4;  // the token scales of two tiles in turn
   static constexpr int kRawStages0 =
-      (kTcSmemLimit - 1024 - kBarBytes - kScaleBytes - kConvStages * kConvB) / kRaw;
+      (kTcSmemLimit - kBarBytes - kScaleBytes - kConvStages * kConvB) / kRaw;
   static constexpr int kRawStages = kRawStages0 > 10 ? 10 : kRawStages0;
-  static constexpr int kBytes = 1024 + kRawStages * kRaw + kConvStages * kConvB + kBarBytes + kScaleBytes;
+  static constexpr int kBytes = kRawStages * kRaw + kConvStages * kConvB + kBarBytes + kScaleBytes;
   static constexpr int kColsA = BT;  // first column of the converted weights
-  static constexpr int kCols = BT + kConvStages * 64 <= 256 ? 256 : 512;
+  static constexpr int kCols = kColsA + kConvStages * 64 <= 256 ? 256 : 512;
   // partial sums, sent and got, over the stages (free by then)
   static_assert(CG == 2 || (2 * BT + 8) * 512 <= kRawStages * kRaw + kConvStages * kConvB, "");
-  static_assert(kBytes <= kTcSmemLimit && kRawStages >= 2 && BT + kConvStages * 64 <= 512, "");
+  static_assert(kBytes <= kTcSmemLimit && kRawStages >= 2 && kColsA + kConvStages * 64 <= 512, "");
   static_assert(8 * (2 * kRawStages + 2 * kConvStages + 6) <= kBarBytes, "");
 };
 
@@ -150,22 +151,29 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// D += A (tensor memory) * B (shared memory), 16 values of k.
-template <int CG>
-__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+// D (+)= A (tensor memory) * B (shared memory, descriptor hi:lo), 16 values of k.
+template <int CG, bool ADD>
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t add) {
   if (CG == 2)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(ADD ? 1u : add)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(ADD ? 1u : add)
         : "memory");
+}
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 // One arrival on `bar` (in both CTAs of a pair) once the matrix instructions so far are done.
 template <int CG>
@@ -182,16 +190,12 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
             smem_addr(bar))
         : "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31, %32};" ::"r"(addr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
-      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 // Eight columns; the wait is part of the statement, so nothing uses the values before it.
@@ -241,12 +245,11 @@ __device__ __forceinline__ void tc_tile(const TcParams& p, int64_t t, int64_t& t
 }
 
 template <int CG, int BT, bool F32>
-__global__ void __launch_bounds__(TcLayout<CG, BT>::kThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, 1)
     int8_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w,
                           const __grid_constant__ CUtensorMap map_a, const TcParams p) {
   using L = TcLayout<CG, BT>;
-  extern __shared__ uint8_t tc_smem_raw[];
-  uint8_t* smem = tc_smem_raw + ((1024u - (smem_addr(tc_smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* raw = smem;
   uint8_t* conv = smem + L::kRawStages * L::kRaw;
   uint64_t* bars = reinterpret_cast<uint64_t*>(conv + L::kConvStages * L::kConvB);
@@ -317,100 +320,121 @@ __global__ void __launch_bounds__(TcLayout<CG, BT>::kThreads, 1)
       // copies still in flight land before the CTA ends
       for (uint32_t i = it > L::kRawStages ? it - L::kRawStages : 0; i < it; ++i)
         tc_wait(&raw_full[i % L::kRawStages], (i / L::kRawStages) & 1);
-    } else if (warp == 1 && lane == 0 && half == 0) {
+    } else if (warp == 1 && half == 0) {
+      // The whole warp goes through the loop and one lane issues: values that the warp shares
+      // stay in uniform registers, where the instructions want them.
       // fp32 accumulators, fp16 operands, K-major, N = BT, M = CG * 128
       constexpr uint32_t idesc = (1u << 4) | (uint32_t(BT / 8) << 17) | (uint32_t(CG * 8) << 24);
       // 128-byte swizzle, 1024 bytes between groups of eight rows
-      constexpr uint64_t desc0 = (uint64_t(2) << 61) | (uint64_t(1) << 46) | (uint64_t(64) << 32) |
-                                 (uint64_t(1) << 16);
-      uint32_t it = 0, chunk = 0;
+      constexpr uint32_t desc_hi = (2u << 29) | (1u << 14) | 64u;
+      const uint32_t desc_lo = (1u << 16) | ((smem_addr(conv) & 0x3FFFFu) >> 4);
+      const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0);
+      const bool leader = elect_lane();
+      uint32_t st = 0, use = 0, chunk = 0;
       bool ok = true;
       for (int64_t t = first; t < p.tiles && ok; t += stride) {
-        for (int s = 0; s < steps; ++s, ++it) {
-          if (s % (kTcChunk / kTcStep) == 0) {
-            ok = tc_wait(d_empty, (chunk & 1) ^ 1);
+        for (int s = 0; s < steps; ++s) {
+          const bool fresh = s % (kTcChunk / kTcStep) == 0;
+          if (fresh) {
+            ok = tc_wait_warp(d_empty, (chunk & 1) ^ 1);
             ++chunk;
             if (!ok) break;
           }
-          const uint32_t st = it % L::kConvStages, use = it / L::kConvStages;
-          ok = tc_wait(&conv_full[st], use & 1);
+          ok = tc_wait_warp(&conv_full[st], use);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a = tmem + L::kColsA + st * 64;
-          const uint32_t b = smem_addr(conv + st * L::kConvB);
+          const uint32_t a = d + L::kColsA + st * 64, b = desc_lo + st * (L::kConvB >> 4);
+          if (leader) {
+            tc_mma<CG, false>(d, a, b, desc_hi, idesc, !fresh);
 #pragma unroll
-          for (int j = 0; j < kTcStep / 16; ++j) {
-            const uint32_t addr = b + (j / 4) * (L::kRowsB * 128) + (j % 4) * 32;
-            tc_mma<CG>(tmem, a + j * 8, desc0 | uint64_t((addr & 0x3FFFFu) >> 4), idesc,
-                       (s % (kTcChunk / kTcStep) != 0 || j != 0) ? 1u : 0u);
+            for (int j = 1; j < kTcStep / 16; ++j)
+              tc_mma<CG, true>(d, a + j * 8, b + (j / 4) * (L::kRowsB * 8) + (j % 4) * 2, desc_hi,
+                               idesc, 1);
+            tc_commit<CG>(&conv_empty[st]);
+            if (s % (kTcChunk / kTcStep) == kTcChunk / kTcStep - 1 || s == steps - 1)
+              tc_commit<CG>(d_full);
           }
-          tc_commit<CG>(&conv_empty[st]);
-          if (s % (kTcChunk / kTcStep) == kTcChunk / kTcStep - 1 || s == steps - 1)
-            tc_commit<CG>(d_full);
+          if (++st == L::kConvStages) st = 0, use ^= 1;
         }
       }
       // matrix instructions still in flight are done before tensor memory is freed
-      if (chunk > 0 && ok) tc_wait(d_full, (chunk - 1) & 1);
+      if (chunk > 0 && ok) tc_wait_warp(d_full, (chunk - 1) & 1);
     }
-  } else if (warp < 8 + 4 * L::kGroupsA) {
+  } else if (warp < kTcFirstDrain) {
     reg_dec<L::kRegsConvert>();
-    uint32_t it = 0;
     bool ok = true;
-    const bool weights = warp < 4 + 4 * L::kGroupsA;
+    const bool weights = warp < 12;
+    const uint32_t turn = (warp >> 2) - (weights ? 1 : 3);  // takes the stages of this parity
     const int tid = (warp & 3) * 32 + lane;
     const uint32_t full0 = map_rank(smem_addr(conv_full), rank - half);
+    constexpr int kParts = L::kRowsB / 16;  // 16-byte chunks of a token's stage a thread converts
+    const int row = weights ? tid : tid % L::kRowsB;
+    const int part = weights ? 0 : tid / L::kRowsB * kParts;  // its first chunk
+    const uint32_t chunks = weights ? 8 : kParts;
+    uint32_t it = 0;
     for (int64_t t = first; t < p.tiles && ok; t += stride) {
       for (int s = 0; s < steps; ++s, ++it) {
-        if (L::kGroupsA == 2 && weights && int(it & 1) != (warp - 4) / 4) continue;
+        if ((it & 1) != turn) continue;
         const uint32_t rs = it % L::kRawStages, cs = it % L::kConvStages;
         ok = tc_wait_warp(&raw_full[rs], (it / L::kRawStages) & 1);
         if (!ok) break;
-        ok = tc_wait_warp(&conv_empty[cs], ((it / L::kConvStages) & 1) ^ 1);
+        const uint8_t* src = raw + rs * L::kRaw + (weights ? 0 : L::kRawA) + row * 128;
+        uint8_t* dst = conv + cs * L::kConvB + row * 128;
+        const uint32_t dst_a = tmem + L::kColsA + cs * 64 + (uint32_t(warp & 3) << 21);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // half of this thread's share into registers, so that its loads overlap
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (h * 4 + i < chunks)
+              v[i] = *reinterpret_cast<const uint4*>(src + (((part + h * 4 + i) ^ (row & 7)) << 4));
+          if (h == 0) {
+            ok = tc_wait_warp(&conv_empty[cs], ((it / L::kConvStages) & 1) ^ 1);
+            if (!ok) break;
+            tc_fence_after();
+          } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_empty[rs]);
+          }
+          if (weights) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              uint32_t f[16];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                int8_to_f16(v[i + j].x, f[j * 8 + 0], f[j * 8 + 1]);
+                int8_to_f16(v[i + j].y, f[j * 8 + 2], f[j * 8 + 3]);
+                int8_to_f16(v[i + j].z, f[j * 8 + 4], f[j * 8 + 5]);
+                int8_to_f16(v[i + j].w, f[j * 8 + 6], f[j * 8 + 7]);
+              }
+              tmem_store16(dst_a + h * 32 + i * 8, f);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (h * 4 + i >= kParts) continue;
+              const int c = part + h * 4 + i;
+              uint4 a, b;
+              int8_to_f16(v[i].x, a.x, a.y);
+              int8_to_f16(v[i].y, a.z, a.w);
+              int8_to_f16(v[i].z, b.x, b.y);
+              int8_to_f16(v[i].w, b.z, b.w);
+              uint8_t* at = dst + (c >> 2) * (L::kRowsB * 128);
+              *reinterpret_cast<uint4*>(at + ((((c & 3) * 2) ^ (row & 7)) << 4)) = a;
+              *reinterpret_cast<uint4*>(at + ((((c & 3) * 2 + 1) ^ (row & 7)) << 4)) = b;
+            }
+          }
+        }
         if (!ok) break;
         if (weights) {
-          tc_fence_after();
-          const uint8_t* row = raw + rs * L::kRaw + tid * 128;
-          const uint32_t dst = tmem + L::kColsA + cs * 64 + (uint32_t(warp & 3) << 21);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint4 w =
-                  *reinterpret_cast<const uint4*>(row + (((h * 4 + c) ^ (tid & 7)) << 4));
-              int8_to_f16(w.x, v[c * 8 + 0], v[c * 8 + 1]);
-              int8_to_f16(w.y, v[c * 8 + 2], v[c * 8 + 3]);
-              int8_to_f16(w.z, v[c * 8 + 4], v[c * 8 + 5]);
-              int8_to_f16(w.w, v[c * 8 + 6], v[c * 8 + 7]);
-            }
-            tmem_store32(dst + h * 32, v);
-          }
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
         } else {
-          // each thread converts kRowsB bytes of one token's 128
-          constexpr int kParts = L::kRowsB / 16;
-          const int r = tid % L::kRowsB, part = tid / L::kRowsB;
-          const uint8_t* row = raw + rs * L::kRaw + L::kRawA + r * 128;
-          uint8_t* dst = conv + cs * L::kConvB + r * 128;
-#pragma unroll
-          for (int i = 0; i < kParts; ++i) {
-            const int c = part * kParts + i;
-            const uint4 w = *reinterpret_cast<const uint4*>(row + ((c ^ (r & 7)) << 4));
-            uint4 a, b;
-            int8_to_f16(w.x, a.x, a.y);
-            int8_to_f16(w.y, a.z, a.w);
-            int8_to_f16(w.z, b.x, b.y);
-            int8_to_f16(w.w, b.z, b.w);
-            uint8_t* at = dst + (c >> 2) * (L::kRowsB * 128);
-            *reinterpret_cast<uint4*>(at + ((((c & 3) * 2) ^ (r & 7)) << 4)) = a;
-            *reinterpret_cast<uint4*>(at + ((((c & 3) * 2 + 1) ^ (r & 7)) << 4)) = b;
-          }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&raw_empty[rs]);
           if (CG == 2) mbar_arrive_cluster(full0 + cs * 8);
           else mbar_arrive(&conv_full[cs]);
         }
@@ -419,22 +443,26 @@ __global__ void __launch_bounds__(TcLayout<CG, BT>::kThreads, 1)
   } else {
     reg_inc<L::kRegsDrain>();
     constexpr int kAcc = BT / 2;  // token columns of this warp
-    const int side = (warp - 8 - 4 * L::kGroupsA) >> 2, quarter = warp & 3;
+    const int side = (warp - kTcFirstDrain) >> 2, quarter = warp & 3;
     const uint32_t src = tmem + side * kAcc + (uint32_t(quarter) << 21);
     const uint32_t empty0 = map_rank(smem_addr(d_empty), rank - half);
     uint32_t chunk = 0;
     bool ok = true;
-    float* scales = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + L::kBarBytes) +
-                    (warp - 8 - 4 * L::kGroupsA) * kAcc;
+    float* scales = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + L::kBarBytes);
+    bool parity = false;
     for (int64_t t = first; t < p.tiles && ok; t += stride) {
       int64_t tn, tm;
       tc_tile(p, t, tn, tm);
       const int64_t n = tn * (128 * CG) + half * 128 + quarter * 32 + lane;
       const int64_t m0 = tm * BT + side * kAcc, left = p.mm.m - m0;
       // the scales while the products run
-      __syncwarp();
-      for (int i = lane; i < kAcc; i += 32) scales[i] = i < left ? p.mm.a_scale[m0 + i] : 0.0f;
-      __syncwarp();
+      constexpr int kMine = (kAcc + 31) / 32;
+      float as[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int c = i * 32 + lane;
+        as[i] = c < kAcc && c < left ? p.mm.a_scale[m0 + c] : 0.0f;
+      }
       float ws = 0.0f, bias = 0.0f;
       if (n < p.mm.n) {
         ws = p.mm.w_scale[n];
@@ -447,6 +475,15 @@ __global__ void __launch_bounds__(TcLayout<CG, BT>::kThreads, 1)
         ok = tc_wait_warp(d_full, chunk & 1);
         if (!ok) break;
         tc_fence_after();
+        if (s == 0) {
+          // The four warps of a side store the same values. Their buffer is free: this tile's
+          // first products were issued after every warp had drained the tile before, which is
+          // after it had finished with the one before that.
+#pragma unroll
+          for (int i = 0; i < kMine; ++i)
+            if (i * 32 + lane < kAcc) scales[side * kAcc + i * 32 + lane] = as[i];
+          __syncwarp();
+        }
 #pragma unroll
         for (int c = 0; c < kAcc / 8; ++c) {
           float v[8];
@@ -471,12 +508,11 @@ __global__ void __launch_bounds__(TcLayout<CG, BT>::kThreads, 1)
         // says that its stages are free) and gets its own columns as [CTA][column][channel].
         // (Loops that stay loops: this code runs once, and its instructions come from memory;
         // unrolled over the columns it took 26 us at 128 tokens.)
-        constexpr int kFirst = 8 + 4 * L::kGroupsA;
         const int cols = min(BT, int(p.mm.m - tm * BT)), per = (cols + ctas - 1) / ctas;
         const int own0 = min(int(rank) * per, cols), own1 = min(own0 + per, cols);
         const uint32_t send = smem_addr(raw), get = send + BT * 512;
         const uint32_t at = (quarter * 32 + lane) * 4;
-        if (warp == kFirst && lane == 0)
+        if (warp == kTcFirstDrain && lane == 0)
           mbar_arrive_expect_tx(sums_full, uint32_t((ctas - 1) * (own1 - own0) * 512));
 #pragma unroll
         for (int c = 0; c < kAcc; ++c) sts_f32(send + (side * kAcc + c) * 512 + at, acc[c]);
@@ -484,7 +520,7 @@ __global__ void __launch_bounds__(TcLayout<CG, BT>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(sums_laid);
         ok = tc_wait_warp(sums_laid, 0);
-        if (warp == kFirst) {
+        if (warp == kTcFirstDrain) {
           if (lane < ctas && lane != int(rank))
             mbar_arrive_cluster(map_rank(smem_addr(peers_ready), lane));
           ok = tc_wait_warp(peers_ready, 0) && ok;
@@ -505,8 +541,7 @@ __global__ void __launch_bounds__(TcLayout<CG, BT>::kThreads, 1)
             for (int r = 0; r < ctas; ++r)
               v += lds_f32((r == int(rank) ? send + uint32_t(col * 512)
                                            : get + uint32_t((r * per + col - own0) * 512)) + at);
-            // the scale as the warp of this quarter and the column's side has it
-            const float as = scales[(col / kAcc - side) * 4 * kAcc + col % kAcc];
+            const float as = scales[col];
             mm_store<F32>(o, mm_value(v, ws, as, bias));
           }
         }
@@ -515,7 +550,7 @@ __global__ void __launch_bounds__(TcLayout<CG, BT>::kThreads, 1)
         const int cols = left < kAcc ? int(left) : kAcc;
 #pragma unroll
         for (int c = 0; c < kAcc; c += 4) {
-          const float4 sc = lds128(reinterpret_cast<const float4*>(scales + c));
+          const float4 sc = lds128(reinterpret_cast<const float4*>(scales + side * kAcc + c));
 #pragma unroll
           for (int i = 0; i < 4; ++i, o += step)
             if (c + i < cols)
@@ -523,6 +558,8 @@ __global__ void __launch_bounds__(TcLayout<CG, BT>::kThreads, 1)
                                         i == 0 ? sc.x : i == 1 ? sc.y : i == 2 ? sc.z : sc.w, bias));
         }
       }
+      scales = parity ? scales - BT : scales + BT;
+      parity = !parity;
     }
   }
   __syncwarp();
