@@ -296,25 +296,96 @@ int64_t mod_count(int64_t rows, int64_t mod_rows) {
 // 8-bit rows with a scale each, and their product
 // ------------------------------------------------------------------------------------------
 
+// Threads of a row whose chunks of eight values are held in registers, up to `most` a thread. With
+// no more than two rows an SM a row gets a thread for each chunk, for its latency.
+struct RowShape {
+  int per_row, cpt, threads;
+  bool many;
+};
+
+RowShape row_shape(int64_t rows, int chunks, int most, int sms) {
+  RowShape s;
+  s.many = rows > 2 * sms;
+  s.per_row = 32;
+  const int limit = s.many ? 256 : 1024, want = s.many ? most : 1;
+  while (s.per_row < limit && s.per_row * want < chunks) s.per_row *= 2;
+  s.cpt = (chunks + s.per_row - 1) / s.per_row;
+  s.threads = s.per_row > 32 ? s.per_row : 128;
+  return s;
+}
+
+// No more CTAs than are resident at once, each with the same number of rows (one more or less by
+// the last): they share the memory evenly and end together. A CTA has one row where not `many`.
+template <typename Params>
+fp8q_status launch_rows(void (*fn)(Params, int), const Params& p, const RowShape& s,
+                        const DeviceInfo& dev, cudaStream_t stream) {
+  const int64_t ctas = (p.rows + s.threads / s.per_row - 1) / (s.threads / s.per_row);
+  int64_t rounds = 1;
+  if (s.many) {
+    int bps = 0;
+    const fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), s.threads, 0, &bps);
+    if (st != FP8Q_OK) return st;
+    const int64_t slots = int64_t(dev.sms) * std::max(bps, 1);
+    rounds = (ctas + slots - 1) / slots;
+  }
+  return launch(fn, dim3(unsigned((ctas + rounds - 1) / rounds)), dim3(s.threads), 0, stream, p,
+                s.per_row);
+}
+
+template <typename Params>
+fp8q_status launch_wide(void (*fn)(Params), const Params& p, size_t smem, const DeviceInfo& dev,
+                        cudaStream_t stream) {
+  int bps = 0;
+  const fp8q_status st =
+      blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kRqThreads, smem, &bps);
+  if (st != FP8Q_OK) return st;
+  const int64_t slots = int64_t(dev.sms) * std::max(bps, 1), rounds = (p.rows + slots - 1) / slots;
+  return launch(fn, dim3(unsigned((p.rows + rounds - 1) / rounds)), dim3(fp8q::kRqThreads), smem,
+                stream, p);
+}
+
+template <bool INT8, bool RESID, int CPT>
+fp8q_status launch_rms_rows(const fp8q::RmsParams& p, const RowShape& s, const DeviceInfo& dev,
+                            cudaStream_t stream) {
+  return s.many ? launch_rows(fp8q::rms_norm_quant_kernel<INT8, RESID, CPT, true>, p, s, dev, stream)
+                : launch_rows(fp8q::rms_norm_quant_kernel<INT8, RESID, CPT, false>, p, s, dev, stream);
+}
+
 template <bool INT8, bool RESID>
 fp8q_status launch_rms(const fp8q::RmsParams& p, const DeviceInfo& dev, cudaStream_t stream) {
-  auto* fn = fp8q::rms_norm_quant_kernel<INT8, RESID>;
-  const size_t smem = size_t(p.cols) * 2 + 64 * sizeof(float);
-  int bps = 0;
-  fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kRqThreads, smem, &bps);
-  if (st != FP8Q_OK) return st;
-  const int64_t grid = std::min<int64_t>(p.rows, int64_t(dev.sms) * std::max(bps, 1));
-  return launch(fn, dim3(unsigned(grid)), dim3(fp8q::kRqThreads), smem, stream, p);
+  const RowShape s = row_shape(p.rows, p.cols / 8, 4, dev.sms);
+  switch (s.cpt) {
+    case 1: return launch_rms_rows<INT8, RESID, 1>(p, s, dev, stream);
+    case 2: return launch_rms_rows<INT8, RESID, 2>(p, s, dev, stream);
+    case 3: return launch_rms_rows<INT8, RESID, 3>(p, s, dev, stream);
+    case 4: return launch_rms_rows<INT8, RESID, 4>(p, s, dev, stream);
+    default:
+      return launch_wide(fp8q::rms_norm_quant_wide_kernel<INT8, RESID>, p,
+                         size_t(p.cols) * 4 + fp8q::kRqRedBytes, dev, stream);
+  }
+}
+
+template <bool INT8, int CPT>
+fp8q_status launch_silu_rows(const fp8q::SiluParams& p, const RowShape& s, const DeviceInfo& dev,
+                             cudaStream_t stream) {
+  return s.many ? launch_rows(fp8q::silu_mul_quant_kernel<INT8, CPT, true>, p, s, dev, stream)
+                : launch_rows(fp8q::silu_mul_quant_kernel<INT8, CPT, false>, p, s, dev, stream);
 }
 
 template <bool INT8>
 fp8q_status launch_silu(const fp8q::SiluParams& p, const DeviceInfo& dev, cudaStream_t stream) {
-  auto* fn = fp8q::silu_mul_quant_kernel<INT8>;
-  int bps = 0;
-  fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kRqThreads, 0, &bps);
-  if (st != FP8Q_OK) return st;
-  const int64_t grid = std::min<int64_t>(p.rows, int64_t(dev.sms) * std::max(bps, 1));
-  return launch(fn, dim3(unsigned(grid)), dim3(fp8q::kRqThreads), 0, stream, p);
+  const RowShape s = row_shape(p.rows, p.cols / 8, 4, dev.sms);
+  switch (s.cpt) {
+    case 1: return launch_silu_rows<INT8, 1>(p, s, dev, stream);
+    case 2: return launch_silu_rows<INT8, 2>(p, s, dev, stream);
+    case 3: return launch_silu_rows<INT8, 3>(p, s, dev, stream);
+    case 4: return launch_silu_rows<INT8, 4>(p, s, dev, stream);
+    default: break;
+  }
+  const size_t smem = size_t(p.cols) * 4 + fp8q::kRqRedBytes;
+  if (smem <= size_t(dev.smem_optin))
+    return launch_wide(fp8q::silu_mul_quant_wide_kernel<INT8, true>, p, smem, dev, stream);
+  return launch_wide(fp8q::silu_mul_quant_wide_kernel<INT8, false>, p, fp8q::kRqRedBytes, dev, stream);
 }
 
 // The driver's tensor-map encoder, through the runtime (the library links no libcuda).

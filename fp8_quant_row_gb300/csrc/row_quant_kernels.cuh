@@ -18,6 +18,7 @@
 namespace fp8q {
 
 constexpr int kRqThreads = 256;
+constexpr int kRqRedBytes = 512;  // two buffers of a CTA's partial results
 constexpr float kRqTiny = 0x1p-100f;
 
 // max(|a|, |b|, |c|), NaN if any is NaN.
@@ -39,18 +40,48 @@ __device__ __forceinline__ float rq_inverse(float top) {
                                                   : 0.0f;
 }
 
-// Four codes of p * inv in one word.
+// Four codes of p * inv in one word, the products given as pairs.
 template <bool INT8>
-__device__ __forceinline__ uint32_t rq_codes4(float p0, float p1, float p2, float p3, float inv) {
+__device__ __forceinline__ uint32_t rq_codes4(f2 p0, f2 p1, float inv) {
+  const f2 inv2 = f2_make(inv, inv);
   if (INT8) {
-    const uint32_t a = __float_as_uint(__fmaf_rn(p0, inv, 12582912.0f));
-    const uint32_t b = __float_as_uint(__fmaf_rn(p1, inv, 12582912.0f));
-    const uint32_t c = __float_as_uint(__fmaf_rn(p2, inv, 12582912.0f));
-    const uint32_t d = __float_as_uint(__fmaf_rn(p3, inv, 12582912.0f));
-    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+    const f2 magic = f2_make(12582912.0f, 12582912.0f);
+    const f2 a = fma2(p0, inv2, magic), b = fma2(p1, inv2, magic);
+    return __byte_perm(__byte_perm(uint32_t(a.v), uint32_t(a.v >> 32), 0x0040),
+                       __byte_perm(uint32_t(b.v), uint32_t(b.v >> 32), 0x0040), 0x5410);
   }
-  return pack_e4m3x2(__fmul_rn(p0, inv), __fmul_rn(p1, inv)) |
-         (pack_e4m3x2(__fmul_rn(p2, inv), __fmul_rn(p3, inv)) << 16);
+  const f2 a = mul2(p0, inv2), b = mul2(p1, inv2);
+  return pack_e4m3x2(f2_lo(a), f2_hi(a)) | (pack_e4m3x2(f2_lo(b), f2_hi(b)) << 16);
+}
+
+// Products of two bf16 chunks of eight, and their largest magnitude.
+__device__ __forceinline__ void rq_products8(f2 (&p)[4], uint4 a, uint4 b, float& top) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[i] = mul2(bf2_to_f2(x[i]), bf2_to_f2(y[i]));
+    top = absmax3(top, f2_lo(p[i]), f2_hi(p[i]));
+  }
+}
+
+template <bool INT8>
+__device__ __forceinline__ uint2 rq_codes8(const f2 (&p)[4], float inv) {
+  if (inv == 0.0f) return make_uint2(0u, 0u);  // (the products may be NaN or infinite)
+  return make_uint2(rq_codes4<INT8>(p[0], p[1], inv), rq_codes4<INT8>(p[2], p[3], inv));
+}
+
+// Products kept in shared memory: 32 bytes a chunk.
+__device__ __forceinline__ void rq_keep(uint4* lo, uint4* hi, const f2 (&p)[4]) {
+  *lo = make_uint4(uint32_t(p[0].v), uint32_t(p[0].v >> 32), uint32_t(p[1].v),
+                   uint32_t(p[1].v >> 32));
+  *hi = make_uint4(uint32_t(p[2].v), uint32_t(p[2].v >> 32), uint32_t(p[3].v),
+                   uint32_t(p[3].v >> 32));
+}
+__device__ __forceinline__ void rq_kept(f2 (&p)[4], uint4 lo, uint4 hi) {
+  p[0] = f2_make(__uint_as_float(lo.x), __uint_as_float(lo.y));
+  p[1] = f2_make(__uint_as_float(lo.z), __uint_as_float(lo.w));
+  p[2] = f2_make(__uint_as_float(hi.x), __uint_as_float(hi.y));
+  p[3] = f2_make(__uint_as_float(hi.z), __uint_as_float(hi.w));
 }
 
 // RN_bf16(RN_fp32(silu(g))) of two gates as fp32 values. silu(g) = g / (1 + 2^(-g log2 e)); the
@@ -58,36 +89,46 @@ __device__ __forceinline__ uint32_t rq_codes4(float p0, float p1, float p2, floa
 // 2^-18 (at g = -87; 2^-22 near 0), and for each of the 65536 bf16 gates the result rounds to
 // the same bf16 value as the exact one (the test goes over all of them).
 // The flushing reciprocal gives 0 for g <= -87.5.
-__device__ __forceinline__ float rq_sigmoid_denominator(float g) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
-  return __fadd_rn(1.0f, e);
-}
-__device__ __forceinline__ float rq_silu(float g) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(rq_sigmoid_denominator(g)));
-  return __fmul_rn(g, r);
-}
 __device__ __forceinline__ uint32_t rq_silu2(uint32_t g) {
-  return pack_bf16x2(rq_silu(bf_lo(g)), rq_silu(bf_hi(g)));
+  const f2 v = bf2_to_f2(g);
+  const f2 t = mul2(v, f2_make(-1.4426950408889634f, -1.4426950408889634f));
+  float e0, e1, r0, r1;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(f2_lo(t)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(f2_hi(t)));
+  const f2 d = add2(f2_make(e0, e1), f2_make(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(f2_lo(d)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(f2_hi(d)));
+  const f2 s = mul2(v, f2_make(r0, r1));
+  return pack_bf16x2(f2_lo(s), f2_hi(s));
+}
+__device__ __forceinline__ uint4 rq_silu8(uint4 g) {
+  return make_uint4(rq_silu2(g.x), rq_silu2(g.y), rq_silu2(g.z), rq_silu2(g.w));
 }
 
-// Largest magnitude (NaN above infinity) and sum over the CTA, the same in every thread.
-__device__ __forceinline__ void rq_block_reduce(float& top, float& sum, float* red, int warps) {
+// Largest magnitude (NaN above infinity) and, with SUM, sum over the threads of a row: a warp, or
+// the whole CTA through `red` (64 floats), with one barrier after it before `red` is used again.
+template <bool SUM>
+__device__ __forceinline__ void rq_reduce(float& top, float& sum, float* red, int warps) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t t = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7FFFFFFFu);
+  if (SUM) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) {
-    red[warp] = __uint_as_float(t);
-    red[32 + warp] = sum;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
-  __syncthreads();
-  t = __float_as_uint(lane < warps ? red[lane] : 0.0f);
-  sum = lane < warps ? red[32 + lane] : 0.0f;
-  top = __uint_as_float(__reduce_max_sync(0xffffffffu, t));
+  if (warps > 1) {
+    if (lane == 0) {
+      red[warp] = __uint_as_float(t);
+      if (SUM) red[32 + warp] = sum;
+    }
+    __syncthreads();
+    t = __reduce_max_sync(0xffffffffu, __float_as_uint(lane < warps ? red[lane] : 0.0f));
+    if (SUM) {
+      sum = lane < warps ? red[32 + lane] : 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+  }
+  top = __uint_as_float(t);
 }
 
 struct RmsParams {
@@ -102,65 +143,152 @@ struct RmsParams {
   float eps;
 };
 
-// One CTA per row: first pass sums h^2 and takes max|p| with h kept in shared memory, the
-// second forms the codes.
-template <bool INT8, bool RESID>
-__global__ void __launch_bounds__(kRqThreads) rms_norm_quant_kernel(RmsParams p) {
-  extern __shared__ uint4 rq_row[];  // [cols] bf16, then the reduction's 64 floats
-  float* red = reinterpret_cast<float*>(rq_row + (p.cols >> 3));
+template <bool INT8>
+__device__ __forceinline__ void rms_store_scale(const RmsParams& p, int64_t row, float top,
+                                                float sum) {
+  const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(p.cols)), p.eps));
+  float s = 0.0f;
+  if (top >= kRqTiny) s = __fdiv_rn(__fmul_rn(top, rstd), rq_qmax<INT8>());
+  // NaN also where the squares leave fp32 (|h| from about 2^60)
+  if (!(top <= 3.402823466e38f) || !(sum <= 3.402823466e38f)) s = __uint_as_float(0x7FC00000u);
+  p.scale[row] = s;
+}
+
+__device__ __forceinline__ uint4 add_bf16x8(uint4 a, uint4 b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f2 v = add2(bf2_to_f2(x[i]), bf2_to_f2(y[i]));
+    r[i] = pack_bf16x2(f2_lo(v), f2_hi(v));
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+__device__ __forceinline__ f2 sum_squares8(f2 sum, uint4 h) {
+  const uint32_t x[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f2 v = bf2_to_f2(x[i]);
+    sum = fma2(v, v, sum);
+  }
+  return sum;
+}
+
+// A row lives in the registers of its threads: `per_row` threads (a warp, several rows a CTA; or
+// the whole CTA), CPT chunks of eight values each. With MANY rows a thread keeps its weights and
+// goes from row to row, one grid apart, with the next row's loads issued before the current
+// row's reduction (two CTAs of 256 threads an SM keep 50 KB and more in flight); without, a CTA
+// has one row.
+template <bool INT8, bool RESID, int CPT, bool MANY>
+__global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
+    rms_norm_quant_kernel(RmsParams p, int per_row) {
+  __shared__ float red[2][64];
   allow_dependents();
+  const int t = threadIdx.x % per_row, chunks = p.cols >> 3, warps = per_row >> 5;
+  const int rows_cta = blockDim.x / per_row;
   wait_for_producers();
-  const int chunks = p.cols >> 3;
-  const uint4* wv = reinterpret_cast<const uint4*>(p.weight);
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const uint4* xv = reinterpret_cast<const uint4*>(p.x + row * p.cols);
-    float top = 0.0f, sum = 0.0f;
-    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
-      uint4 h = xv[c];
-      const uint4 w = wv[c];
-      uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+  uint4 w[CPT], x[CPT], r[RESID ? CPT : 1];
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (t + i * per_row < chunks)
+      w[i] = __ldg(reinterpret_cast<const uint4*>(p.weight) + t + i * per_row);
+  }
+  auto load = [&](int64_t row) {
+    const uint4* xv = reinterpret_cast<const uint4*>(p.x) + row * chunks;
+    const uint4* rv = reinterpret_cast<const uint4*>(p.residual) + row * chunks;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (t + i * per_row < chunks) x[i] = ld_stream(xv + t + i * per_row);
+    }
+    if (RESID) {
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        r[RESID ? i : 0] = make_uint4(0, 0, 0, 0);
+        if (t + i * per_row < chunks) r[RESID ? i : 0] = ld_stream(rv + t + i * per_row);
+      }
+    }
+  };
+  int64_t row = int64_t(blockIdx.x) * rows_cta + threadIdx.x / per_row;
+  const int64_t stride = int64_t(gridDim.x) * rows_cta;
+  if (row < p.rows) load(row);
+  for (int flip = 0; row < p.rows; row += stride, flip ^= 1) {
+    const int64_t base = row * chunks;
+    float top = 0.0f;
+    f2 sum2 = f2_make(0.0f, 0.0f);
+    f2 prod[CPT][4];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
       if (RESID) {
-        const uint4 r = reinterpret_cast<const uint4*>(p.residual + row * p.cols)[c];
-        const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          hw[i] = pack_bf16x2(__fadd_rn(bf_lo(hw[i]), bf_lo(rw[i])),
-                              __fadd_rn(bf_hi(hw[i]), bf_hi(rw[i])));
-        h = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        reinterpret_cast<uint4*>(p.h + row * p.cols)[c] = h;
+        x[i] = add_bf16x8(x[i], r[RESID ? i : 0]);
+        if (t + i * per_row < chunks)
+          reinterpret_cast<uint4*>(p.h)[base + t + i * per_row] = x[i];
       }
-      rq_row[c] = h;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = bf_lo(hw[i]), b = bf_hi(hw[i]);
-        top = absmax3(top, a * bf_lo(ww[i]), b * bf_hi(ww[i]));
-        sum = fmaf(b, b, fmaf(a, a, sum));
-      }
+      sum2 = sum_squares8(sum2, x[i]);
+      rq_products8(prod[i], x[i], w[i], top);
     }
-    rq_block_reduce(top, sum, red, kRqThreads / 32);
+    if (MANY && row + stride < p.rows) load(row + stride);
+    float sum = f2_lo(sum2) + f2_hi(sum2);
+    rq_reduce<true>(top, sum, red[flip], warps);
     const float inv = rq_inverse<INT8>(top);
-    uint2* qv = reinterpret_cast<uint2*>(p.q + row * p.cols);
+    uint2* qv = reinterpret_cast<uint2*>(p.q) + base;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i)
+      if (t + i * per_row < chunks) qv[t + i * per_row] = rq_codes8<INT8>(prod[i], inv);
+    if (t == 0) rms_store_scale<INT8>(p, row, top, sum);
+    if (!MANY) break;
+  }
+}
+
+// Wide rows: the inputs, then the products in their place, in shared memory, where each thread
+// keeps what it alone uses; the CTAs of an SM overlap one another's loads and work.
+template <bool INT8, bool RESID>
+__global__ void __launch_bounds__(kRqThreads) rms_norm_quant_wide_kernel(RmsParams p) {
+  extern __shared__ uint4 rq_smem[];
+  float* red = reinterpret_cast<float*>(rq_smem);  // two buffers of 64
+  const int chunks = p.cols >> 3;
+  uint4 *lo = rq_smem + 32, *hi = lo + chunks;
+  allow_dependents();
+  const uint4* wv = reinterpret_cast<const uint4*>(p.weight);
+  wait_for_producers();
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 64) {
+    const int64_t base = row * chunks;
+    const uint4* xv = reinterpret_cast<const uint4*>(p.x) + base;
+    const uint4* rv = reinterpret_cast<const uint4*>(p.residual) + base;
     for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
-      const uint4 h = rq_row[c], w = wv[c];
-      uint2 o = make_uint2(0u, 0u);
-      if (inv != 0.0f) {
-        o.x = rq_codes4<INT8>(bf_lo(h.x) * bf_lo(w.x), bf_hi(h.x) * bf_hi(w.x),
-                              bf_lo(h.y) * bf_lo(w.y), bf_hi(h.y) * bf_hi(w.y), inv);
-        o.y = rq_codes4<INT8>(bf_lo(h.z) * bf_lo(w.z), bf_hi(h.z) * bf_hi(w.z),
-                              bf_lo(h.w) * bf_lo(w.w), bf_hi(h.w) * bf_hi(w.w), inv);
+      cp_async16(lo + c, xv + c);
+      if (RESID) cp_async16(hi + c, rv + c);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    float top = 0.0f;
+    f2 sum2 = f2_make(0.0f, 0.0f);
+#pragma unroll 2
+    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+      uint4 h = lo[c];
+      if (RESID) {
+        h = add_bf16x8(h, hi[c]);
+        reinterpret_cast<uint4*>(p.h)[base + c] = h;
       }
-      qv[c] = o;
+      sum2 = sum_squares8(sum2, h);
+      f2 prod[4];
+      rq_products8(prod, h, __ldg(wv + c), top);
+      rq_keep(lo + c, hi + c, prod);
     }
-    if (threadIdx.x == 0) {
-      const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(p.cols)), p.eps));
-      float s = 0.0f;
-      if (top >= kRqTiny) s = __fdiv_rn(__fmul_rn(top, rstd), rq_qmax<INT8>());
-      // NaN also where the squares leave fp32 (|h| from about 2^60)
-      if (!(top <= 3.402823466e38f) || !(sum <= 3.402823466e38f)) s = __uint_as_float(0x7FC00000u);
-      p.scale[row] = s;
+    float sum = f2_lo(sum2) + f2_hi(sum2);
+    rq_reduce<true>(top, sum, red + flip, kRqThreads / 32);
+    const float inv = rq_inverse<INT8>(top);
+    uint2* qv = reinterpret_cast<uint2*>(p.q) + base;
+#pragma unroll 2
+    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+      f2 prod[4];
+      rq_kept(prod, lo[c], hi[c]);
+      qv[c] = rq_codes8<INT8>(prod, inv);
     }
-    __syncthreads();
+    if (threadIdx.x == 0) rms_store_scale<INT8>(p, row, top, sum);
   }
 }
 
@@ -174,50 +302,96 @@ struct SiluParams {
   int cols;
 };
 
-// One CTA per row: max|p| first, then the codes from a second reading of the row.
 template <bool INT8>
-__global__ void __launch_bounds__(kRqThreads) silu_mul_quant_kernel(SiluParams p) {
-  __shared__ float red[64];
+__device__ __forceinline__ void silu_store_scale(const SiluParams& p, int64_t row, float top) {
+  float s = top >= kRqTiny ? __fdiv_rn(top, rq_qmax<INT8>()) : 0.0f;
+  if (!(top <= 3.402823466e38f)) s = __uint_as_float(0x7FC00000u);
+  p.scale[row] = s;
+}
+
+// As rms_norm_quant_kernel: a row in the registers of its threads.
+template <bool INT8, int CPT, bool MANY>
+__global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
+    silu_mul_quant_kernel(SiluParams p, int per_row) {
+  __shared__ float red[2][64];
   allow_dependents();
+  const int t = threadIdx.x % per_row, chunks = p.cols >> 3, warps = per_row >> 5;
+  const int rows_cta = blockDim.x / per_row;
   wait_for_producers();
-  const int chunks = p.cols >> 3;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+  uint4 g[CPT], u[CPT];
+  auto load = [&](int64_t row) {
     const uint4* gv = reinterpret_cast<const uint4*>(p.gate + row * p.ld);
     const uint4* uv = reinterpret_cast<const uint4*>(p.up + row * p.ld);
-    float top = 0.0f, sum = 0.0f;
-    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
-      const uint4 g = gv[c], u = uv[c];
-      const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t s = rq_silu2(gw[i]);
-        top = absmax3(top, bf_lo(s) * bf_lo(uw[i]), bf_hi(s) * bf_hi(uw[i]));
+    for (int i = 0; i < CPT; ++i) {
+      g[i] = u[i] = make_uint4(0, 0, 0, 0);
+      if (t + i * per_row < chunks) {
+        g[i] = ld_stream(gv + t + i * per_row);
+        u[i] = ld_stream(uv + t + i * per_row);
       }
     }
-    rq_block_reduce(top, sum, red, kRqThreads / 32);
+  };
+  int64_t row = int64_t(blockIdx.x) * rows_cta + threadIdx.x / per_row;
+  const int64_t stride = int64_t(gridDim.x) * rows_cta;
+  if (row < p.rows) load(row);
+  for (int flip = 0; row < p.rows; row += stride, flip ^= 1) {
+    float top = 0.0f, none = 0.0f;
+    f2 prod[CPT][4];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) rq_products8(prod[i], rq_silu8(g[i]), u[i], top);
+    if (MANY && row + stride < p.rows) load(row + stride);
+    rq_reduce<false>(top, none, red[flip], warps);
     const float inv = rq_inverse<INT8>(top);
-    uint2* qv = reinterpret_cast<uint2*>(p.q + row * p.cols);
-    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
-      uint32_t o[2] = {0u, 0u};
-      if (inv != 0.0f) {
-        const uint4 g = gv[c], u = uv[c];
-        const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+    uint2* qv = reinterpret_cast<uint2*>(p.q) + row * chunks;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t s = rq_silu2(gw[2 * i]), t = rq_silu2(gw[2 * i + 1]);
-          o[i] = rq_codes4<INT8>(bf_lo(s) * bf_lo(uw[2 * i]), bf_hi(s) * bf_hi(uw[2 * i]),
-                                 bf_lo(t) * bf_lo(uw[2 * i + 1]), bf_hi(t) * bf_hi(uw[2 * i + 1]),
-                                 inv);
-        }
+    for (int i = 0; i < CPT; ++i)
+      if (t + i * per_row < chunks) qv[t + i * per_row] = rq_codes8<INT8>(prod[i], inv);
+    if (t == 0) silu_store_scale<INT8>(p, row, top);
+    if (!MANY) break;
+  }
+}
+
+// Wide rows in shared memory (KEEP: gate and up, then the products in their place, each thread's
+// own); rows that do not fit are read twice.
+template <bool INT8, bool KEEP>
+__global__ void __launch_bounds__(kRqThreads) silu_mul_quant_wide_kernel(SiluParams p) {
+  extern __shared__ uint4 rq_smem[];
+  float* red = reinterpret_cast<float*>(rq_smem);  // two buffers of 64
+  const int chunks = p.cols >> 3;
+  uint4 *lo = rq_smem + 32, *hi = lo + chunks;
+  allow_dependents();
+  wait_for_producers();
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 64) {
+    const uint4* gv = reinterpret_cast<const uint4*>(p.gate + row * p.ld);
+    const uint4* uv = reinterpret_cast<const uint4*>(p.up + row * p.ld);
+    if (KEEP) {
+      for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+        cp_async16(lo + c, gv + c);
+        cp_async16(hi + c, uv + c);
       }
-      qv[c] = make_uint2(o[0], o[1]);
+      cp_async_commit();
+      cp_async_wait<0>();
     }
-    if (threadIdx.x == 0) {
-      float s = top >= kRqTiny ? __fdiv_rn(top, rq_qmax<INT8>()) : 0.0f;
-      if (!(top <= 3.402823466e38f)) s = __uint_as_float(0x7FC00000u);
-      p.scale[row] = s;
+    float top = 0.0f, none = 0.0f;
+#pragma unroll 2
+    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+      f2 prod[4];
+      rq_products8(prod, rq_silu8(KEEP ? lo[c] : gv[c]), KEEP ? hi[c] : uv[c], top);
+      if (KEEP) rq_keep(lo + c, hi + c, prod);
     }
-    __syncthreads();
+    rq_reduce<false>(top, none, red + flip, kRqThreads / 32);
+    const float inv = rq_inverse<INT8>(top);
+    uint2* qv = reinterpret_cast<uint2*>(p.q) + row * chunks;
+#pragma unroll 2
+    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+      f2 prod[4];
+      float again = 0.0f;
+      if (KEEP) rq_kept(prod, lo[c], hi[c]);
+      else rq_products8(prod, rq_silu8(gv[c]), uv[c], again);
+      qv[c] = rq_codes8<INT8>(prod, inv);
+    }
+    if (threadIdx.x == 0) silu_store_scale<INT8>(p, row, top);
   }
 }
 

@@ -92,7 +92,8 @@ def f32(n, seed):
 # ------------------------------------------------------------------------------------------
 
 NORM_SHAPES = [(1, 8), (3, 16), (2, 248), (5, 1000), (1, 6144), (127, 5120), (300, 2056),
-               (1000, 6144), (700, 8192), (9, 12288), (5, 24576), (3, 32768), (4000, 64)]
+               (1000, 6144), (700, 8192), (9, 12288), (5, 24576), (3, 32768), (4000, 64), (1000, 248),
+               (306, 8200), (400, 12288), (310, 32768), (3001, 1024)]
 
 
 @gpu
@@ -190,7 +191,8 @@ def test_silu_of_every_bf16_gate():
 
 
 SILU_SHAPES = [(1, 8), (3, 24), (5, 1000), (1, 18432), (333, 5640), (700, 2048), (40, 18432),
-               (9, 40000), (2, 1 << 20), (3000, 128)]
+               (9, 40000), (2, 1 << 20), (3000, 128), (400, 12288),
+               (310, 12160), (400, 8192), (1000, 520), (330, 58000), (306, 65536)]
 
 
 @gpu
