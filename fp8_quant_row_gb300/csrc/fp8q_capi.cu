@@ -314,34 +314,37 @@ RowShape row_shape(int64_t rows, int chunks, int most, int sms) {
   return s;
 }
 
-// No more CTAs than are resident at once, each with the same number of rows (one more or less by
-// the last): they share the memory evenly and end together. A CTA has one row where not `many`.
+// As many CTAs as are resident at once, each going from row to row; one row a CTA where not `many`.
 template <typename Params>
 fp8q_status launch_rows(void (*fn)(Params, int), const Params& p, const RowShape& s,
                         const DeviceInfo& dev, cudaStream_t stream) {
-  const int64_t ctas = (p.rows + s.threads / s.per_row - 1) / (s.threads / s.per_row);
-  int64_t rounds = 1;
+  int64_t ctas = (p.rows + s.threads / s.per_row - 1) / (s.threads / s.per_row);
   if (s.many) {
     int bps = 0;
     const fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), s.threads, 0, &bps);
     if (st != FP8Q_OK) return st;
-    const int64_t slots = int64_t(dev.sms) * std::max(bps, 1);
-    rounds = (ctas + slots - 1) / slots;
+    ctas = std::min(ctas, int64_t(dev.sms) * std::max(bps, 1));
   }
-  return launch(fn, dim3(unsigned((ctas + rounds - 1) / rounds)), dim3(s.threads), 0, stream, p,
-                s.per_row);
+  return launch(fn, dim3(unsigned(ctas)), dim3(s.threads), 0, stream, p, s.per_row);
+}
+
+// Threads of a row in shared memory. An SM wants over a thousand threads, and several rows, at
+// work: 256 threads a row where five rows and more fit (10240 columns, 4608 rows: 37.2 us against
+// 39.0 with 512), 512 where two to four do (18432 columns: 65.0 against 67.6 with 256), 1024 for
+// one.
+int wide_threads(size_t smem, const DeviceInfo& dev) {
+  const size_t fit = size_t(dev.smem_optin) / (smem + 1024);
+  return fit >= 5 ? 256 : fit >= 2 ? 512 : 1024;
 }
 
 template <typename Params>
-fp8q_status launch_wide(void (*fn)(Params), const Params& p, size_t smem, const DeviceInfo& dev,
-                        cudaStream_t stream) {
+fp8q_status launch_wide(void (*fn)(Params), int threads, size_t smem, const Params& p,
+                        const DeviceInfo& dev, cudaStream_t stream) {
   int bps = 0;
-  const fp8q_status st =
-      blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kRqThreads, smem, &bps);
+  const fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), threads, smem, &bps);
   if (st != FP8Q_OK) return st;
-  const int64_t slots = int64_t(dev.sms) * std::max(bps, 1), rounds = (p.rows + slots - 1) / slots;
-  return launch(fn, dim3(unsigned((p.rows + rounds - 1) / rounds)), dim3(fp8q::kRqThreads), smem,
-                stream, p);
+  const int64_t ctas = std::min<int64_t>(p.rows, int64_t(dev.sms) * std::max(bps, 1));
+  return launch(fn, dim3(unsigned(ctas)), dim3(threads), smem, stream, p);
 }
 
 template <bool INT8, bool RESID, int CPT>
@@ -359,9 +362,16 @@ fp8q_status launch_rms(const fp8q::RmsParams& p, const DeviceInfo& dev, cudaStre
     case 2: return launch_rms_rows<INT8, RESID, 2>(p, s, dev, stream);
     case 3: return launch_rms_rows<INT8, RESID, 3>(p, s, dev, stream);
     case 4: return launch_rms_rows<INT8, RESID, 4>(p, s, dev, stream);
+    default: break;
+  }
+  const size_t smem = size_t(p.cols) * 4 + fp8q::kRqRedBytes;
+  switch (wide_threads(smem, dev)) {
+    case 256:
+      return launch_wide(fp8q::rms_norm_quant_wide_kernel<INT8, RESID, 256>, 256, smem, p, dev, stream);
+    case 512:
+      return launch_wide(fp8q::rms_norm_quant_wide_kernel<INT8, RESID, 512>, 512, smem, p, dev, stream);
     default:
-      return launch_wide(fp8q::rms_norm_quant_wide_kernel<INT8, RESID>, p,
-                         size_t(p.cols) * 4 + fp8q::kRqRedBytes, dev, stream);
+      return launch_wide(fp8q::rms_norm_quant_wide_kernel<INT8, RESID, 1024>, 1024, smem, p, dev, stream);
   }
 }
 
@@ -383,9 +393,17 @@ fp8q_status launch_silu(const fp8q::SiluParams& p, const DeviceInfo& dev, cudaSt
     default: break;
   }
   const size_t smem = size_t(p.cols) * 4 + fp8q::kRqRedBytes;
-  if (smem <= size_t(dev.smem_optin))
-    return launch_wide(fp8q::silu_mul_quant_wide_kernel<INT8, true>, p, smem, dev, stream);
-  return launch_wide(fp8q::silu_mul_quant_wide_kernel<INT8, false>, p, fp8q::kRqRedBytes, dev, stream);
+  if (smem > size_t(dev.smem_optin))
+    return launch_wide(fp8q::silu_mul_quant_wide_kernel<INT8, false, 512>, 512,
+                       fp8q::kRqRedBytes, p, dev, stream);
+  switch (wide_threads(smem, dev)) {
+    case 256:
+      return launch_wide(fp8q::silu_mul_quant_wide_kernel<INT8, true, 256>, 256, smem, p, dev, stream);
+    case 512:
+      return launch_wide(fp8q::silu_mul_quant_wide_kernel<INT8, true, 512>, 512, smem, p, dev, stream);
+    default:
+      return launch_wide(fp8q::silu_mul_quant_wide_kernel<INT8, true, 1024>, 1024, smem, p, dev, stream);
+  }
 }
 
 // The driver's tensor-map encoder, through the runtime (the library links no libcuda).

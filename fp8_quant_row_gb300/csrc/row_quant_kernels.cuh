@@ -17,7 +17,6 @@
 
 namespace fp8q {
 
-constexpr int kRqThreads = 256;
 constexpr int kRqRedBytes = 512;  // two buffers of a CTA's partial results
 constexpr float kRqTiny = 0x1p-100f;
 
@@ -244,8 +243,8 @@ __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
 
 // Wide rows: the inputs, then the products in their place, in shared memory, where each thread
 // keeps what it alone uses; the CTAs of an SM overlap one another's loads and work.
-template <bool INT8, bool RESID>
-__global__ void __launch_bounds__(kRqThreads) rms_norm_quant_wide_kernel(RmsParams p) {
+template <bool INT8, bool RESID, int THREADS>
+__global__ void __launch_bounds__(THREADS) rms_norm_quant_wide_kernel(RmsParams p) {
   extern __shared__ uint4 rq_smem[];
   float* red = reinterpret_cast<float*>(rq_smem);  // two buffers of 64
   const int chunks = p.cols >> 3;
@@ -258,7 +257,7 @@ __global__ void __launch_bounds__(kRqThreads) rms_norm_quant_wide_kernel(RmsPara
     const int64_t base = row * chunks;
     const uint4* xv = reinterpret_cast<const uint4*>(p.x) + base;
     const uint4* rv = reinterpret_cast<const uint4*>(p.residual) + base;
-    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+    for (int c = threadIdx.x; c < chunks; c += THREADS) {
       cp_async16(lo + c, xv + c);
       if (RESID) cp_async16(hi + c, rv + c);
     }
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(kRqThreads) rms_norm_quant_wide_kernel(RmsPara
     float top = 0.0f;
     f2 sum2 = f2_make(0.0f, 0.0f);
 #pragma unroll 2
-    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+    for (int c = threadIdx.x; c < chunks; c += THREADS) {
       uint4 h = lo[c];
       if (RESID) {
         h = add_bf16x8(h, hi[c]);
@@ -279,11 +278,11 @@ __global__ void __launch_bounds__(kRqThreads) rms_norm_quant_wide_kernel(RmsPara
       rq_keep(lo + c, hi + c, prod);
     }
     float sum = f2_lo(sum2) + f2_hi(sum2);
-    rq_reduce<true>(top, sum, red + flip, kRqThreads / 32);
+    rq_reduce<true>(top, sum, red + flip, THREADS / 32);
     const float inv = rq_inverse<INT8>(top);
     uint2* qv = reinterpret_cast<uint2*>(p.q) + base;
 #pragma unroll 2
-    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+    for (int c = threadIdx.x; c < chunks; c += THREADS) {
       f2 prod[4];
       rq_kept(prod, lo[c], hi[c]);
       qv[c] = rq_codes8<INT8>(prod, inv);
@@ -353,8 +352,8 @@ __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
 
 // Wide rows in shared memory (KEEP: gate and up, then the products in their place, each thread's
 // own); rows that do not fit are read twice.
-template <bool INT8, bool KEEP>
-__global__ void __launch_bounds__(kRqThreads) silu_mul_quant_wide_kernel(SiluParams p) {
+template <bool INT8, bool KEEP, int THREADS>
+__global__ void __launch_bounds__(THREADS) silu_mul_quant_wide_kernel(SiluParams p) {
   extern __shared__ uint4 rq_smem[];
   float* red = reinterpret_cast<float*>(rq_smem);  // two buffers of 64
   const int chunks = p.cols >> 3;
@@ -366,7 +365,7 @@ __global__ void __launch_bounds__(kRqThreads) silu_mul_quant_wide_kernel(SiluPar
     const uint4* gv = reinterpret_cast<const uint4*>(p.gate + row * p.ld);
     const uint4* uv = reinterpret_cast<const uint4*>(p.up + row * p.ld);
     if (KEEP) {
-      for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+      for (int c = threadIdx.x; c < chunks; c += THREADS) {
         cp_async16(lo + c, gv + c);
         cp_async16(hi + c, uv + c);
       }
@@ -375,16 +374,16 @@ __global__ void __launch_bounds__(kRqThreads) silu_mul_quant_wide_kernel(SiluPar
     }
     float top = 0.0f, none = 0.0f;
 #pragma unroll 2
-    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+    for (int c = threadIdx.x; c < chunks; c += THREADS) {
       f2 prod[4];
       rq_products8(prod, rq_silu8(KEEP ? lo[c] : gv[c]), KEEP ? hi[c] : uv[c], top);
       if (KEEP) rq_keep(lo + c, hi + c, prod);
     }
-    rq_reduce<false>(top, none, red + flip, kRqThreads / 32);
+    rq_reduce<false>(top, none, red + flip, THREADS / 32);
     const float inv = rq_inverse<INT8>(top);
     uint2* qv = reinterpret_cast<uint2*>(p.q) + row * chunks;
 #pragma unroll 2
-    for (int c = threadIdx.x; c < chunks; c += kRqThreads) {
+    for (int c = threadIdx.x; c < chunks; c += THREADS) {
       f2 prod[4];
       float again = 0.0f;
       if (KEEP) rq_kept(prod, lo[c], hi[c]);
