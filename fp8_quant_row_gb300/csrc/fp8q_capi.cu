@@ -615,7 +615,7 @@ fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
   int which = 0;
   const double weights = double(p.n) * double(p.k);
   if (p.m <= 8) best = 3.0 + weights / 5.9e6, which = 8;
-  else if (p.m <= 16) best = 3.0 + weights / 3.6e6, which = 16;
+  else if (p.m <= 16) best = 3.0 + weights / 4.2e6, which = 16;
   fp8q_status st = FP8Q_OK;
   if (p.m <= 64) st = consider_tc<1, 32, F32>(p, dev, &best, &which);
   if (st == FP8Q_OK && p.m > 32 && p.m <= 128) st = consider_tc<1, 64, F32>(p, dev, &best, &which);

@@ -3,11 +3,10 @@
 //
 // A CTA of eight warps takes 16 output channels at a time; `split` of its warps share a channel
 // group's k, interleaved by 128 values, so that together they read a kilobyte of each row at
-// about one time (DRAM pages; a contiguous range for each warp reached 69% of the memory's rate
-// at 36864 x 6144 where this reaches more). Each lane copies its own 16-byte pieces of the
-// weights (cp.async) through a ring in shared memory that it alone writes and reads, three
-// groups of k ahead (6 KB a warp, 144 KB in flight on an SM of 24 warps), across channel groups,
-// in the layout of the fp16 matrix instruction m16n8k16: 16 consecutive bytes of a channel per
+// about one time (DRAM pages: at 36864 x 6144, 42.6 us against 48.8 with a contiguous range for
+// each warp). Each lane copies its own 16-byte pieces of the weights (cp.async) through a ring in
+// shared memory that it alone writes and reads, two groups of k ahead (4 KB a warp, 96 KB in
+// flight on an SM of 24 warps), across channel groups, in the layout of the fp16 matrix instruction m16n8k16: 16 consecutive bytes of a channel per
 // lane; which k a fragment's places stand for is free as long as both operands agree. It
 // converts (exact) and multiplies; tokens are read and converted the same way and come from the
 // L1 cache after the first use. (The integer instruction m16n8k32 runs at a quarter of the fp16
@@ -20,7 +19,7 @@
 namespace fp8q {
 
 constexpr int kFewWarps = 8;
-constexpr int kFewStages = 4;                     // groups of 128 values of k in the ring
+constexpr int kFewStages = 3;                     // groups of 128 values of k in the ring
 constexpr int kFewStageBytes = 4 * 512;           // per warp: 16 channels x 128 values
 constexpr int kFewFlush = 1024 / 128;             // groups between drains: sums stay exact
 constexpr int kFewRing = kFewWarps * kFewStages * kFewStageBytes;

@@ -57,14 +57,14 @@ struct TcLayout {
   static constexpr int kScaleBytes = 2 * BT * 4;  // the token scales of two tiles in turn
   static constexpr int kRawStages0 =
       (kTcSmemLimit - kBarBytes - kScaleBytes - kConvStages * kConvB) / kRaw;
-  static constexpr int kRawStages = kRawStages0 > 10 ? 10 : kRawStages0;
+  static constexpr int kRawStages = kRawStages0 > 9 ? 9 : kRawStages0;
   static constexpr int kBytes = kRawStages * kRaw + kConvStages * kConvB + kBarBytes + kScaleBytes;
   static constexpr int kColsA = BT;  // first column of the converted weights
   static constexpr int kCols = kColsA + kConvStages * 64 <= 256 ? 256 : 512;
   // partial sums, sent and got, over the stages (free by then)
   static_assert(CG == 2 || (2 * BT + 8) * 512 <= kRawStages * kRaw + kConvStages * kConvB, "");
   static_assert(kBytes <= kTcSmemLimit && kRawStages >= 2 && kColsA + kConvStages * 64 <= 512, "");
-  static_assert(8 * (2 * kRawStages + 2 * kConvStages + 6) <= kBarBytes, "");
+  static_assert(8 * (2 * kRawStages + 2 * kConvStages + 7) <= kBarBytes, "");
 };
 
 // ---- instructions -------------------------------------------------------------------------
@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* peers_ready = d_empty + 1;               // CG = 1: the others' stages are free
   uint64_t* sums_full = peers_ready + 1;             // CG = 1: the others' sums are here
   uint64_t* sums_laid = sums_full + 1;               // CG = 1: this CTA's sums are in its memory
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums_laid + 1);
+  uint64_t* idle = sums_laid + 1;                    // all matrix instructions are done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(idle + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -287,6 +288,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(peers_ready, CG == 1 && ctas > 1 ? ctas - 1 : 1);
     mbar_init(sums_full, 1);
     mbar_init(sums_laid, 8);
+    mbar_init(idle, 1);
     fence_mbar_init();
   }
   __syncwarp();
@@ -358,7 +360,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       // matrix instructions still in flight are done before tensor memory is freed
-      if (chunk > 0 && ok) tc_wait_warp(d_full, (chunk - 1) & 1);
+      if (leader) tc_commit<CG>(idle);
+      __syncwarp();
+      tc_wait_warp(idle, 0);
     }
   } else if (warp < kTcFirstDrain) {
     reg_dec<L::kRegsConvert>();

@@ -17,7 +17,7 @@
 
 namespace fp8q {
 
-constexpr int kRqRedBytes = 512;  // two buffers of a CTA's partial results
+constexpr int kRqRedBytes = 1024;  // two buffers of a CTA's partial results, of 96 floats each
 constexpr float kRqTiny = 0x1p-100f;
 
 // max(|a|, |b|, |c|), NaN if any is NaN.
@@ -104,27 +104,43 @@ __device__ __forceinline__ uint4 rq_silu8(uint4 g) {
   return make_uint4(rq_silu2(g.x), rq_silu2(g.y), rq_silu2(g.z), rq_silu2(g.w));
 }
 
-// Largest magnitude (NaN above infinity) and, with SUM, sum over the threads of a row: a warp, or
-// the whole CTA through `red` (64 floats), with one barrier after it before `red` is used again.
-template <bool SUM>
-__device__ __forceinline__ void rq_reduce(float& top, float& sum, float* red, int warps) {
+// A sum kept as an unevaluated pair: the additions' rounding errors (TwoSum) gather in lo, so that
+// the sum, rounded to fp32 at the end, does not depend on the order, that is on how many rows a
+// call has (but for sums within about 2^-44 of a rounding border).
+struct RowSum {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float h, float l) {
+    float s, e;
+    two_sum(hi, h, s, e);
+    hi = s;
+    lo = __fadd_rn(lo, __fadd_rn(l, e));
+  }
+  __device__ __forceinline__ void add_lanes() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      add(__shfl_xor_sync(0xffffffffu, hi, o), __shfl_xor_sync(0xffffffffu, lo, o));
+  }
+};
+
+// Largest magnitude (NaN above infinity) and, where `sum` is given, sum over the threads of a row: a
+// warp, or the whole CTA through `red` (kRqRed floats), with one barrier after it before `red` is
+// used again.
+constexpr int kRqRed = 96;
+__device__ __forceinline__ void rq_reduce(float& top, RowSum* sum, float* red, int warps) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t t = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7FFFFFFFu);
-  if (SUM) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
+  if (sum) sum->add_lanes();
   if (warps > 1) {
     if (lane == 0) {
       red[warp] = __uint_as_float(t);
-      if (SUM) red[32 + warp] = sum;
+      if (sum) red[32 + warp] = sum->hi, red[64 + warp] = sum->lo;
     }
     __syncthreads();
     t = __reduce_max_sync(0xffffffffu, __float_as_uint(lane < warps ? red[lane] : 0.0f));
-    if (SUM) {
-      sum = lane < warps ? red[32 + lane] : 0.0f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (sum) {
+      sum->hi = lane < warps ? red[32 + lane] : 0.0f;
+      sum->lo = lane < warps ? red[64 + lane] : 0.0f;
+      sum->add_lanes();
     }
   }
   top = __uint_as_float(t);
@@ -164,14 +180,15 @@ __device__ __forceinline__ uint4 add_bf16x8(uint4 a, uint4 b) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-__device__ __forceinline__ f2 sum_squares8(f2 sum, uint4 h) {
+__device__ __forceinline__ float sum_squares8(uint4 h) {
   const uint32_t x[4] = {h.x, h.y, h.z, h.w};
+  f2 sum = f2_make(0.0f, 0.0f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const f2 v = bf2_to_f2(x[i]);
     sum = fma2(v, v, sum);
   }
-  return sum;
+  return __fadd_rn(f2_lo(sum), f2_hi(sum));
 }
 
 // A row lives in the registers of its threads: `per_row` threads (a warp, several rows a CTA; or
@@ -182,7 +199,7 @@ __device__ __forceinline__ f2 sum_squares8(f2 sum, uint4 h) {
 template <bool INT8, bool RESID, int CPT, bool MANY>
 __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
     rms_norm_quant_kernel(RmsParams p, int per_row) {
-  __shared__ float red[2][64];
+  __shared__ float red[2][kRqRed];
   allow_dependents();
   const int t = threadIdx.x % per_row, chunks = p.cols >> 3, warps = per_row >> 5;
   const int rows_cta = blockDim.x / per_row;
@@ -216,7 +233,7 @@ __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
   for (int flip = 0; row < p.rows; row += stride, flip ^= 1) {
     const int64_t base = row * chunks;
     float top = 0.0f;
-    f2 sum2 = f2_make(0.0f, 0.0f);
+    RowSum sum;
     f2 prod[CPT][4];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
@@ -225,18 +242,17 @@ __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
         if (t + i * per_row < chunks)
           reinterpret_cast<uint4*>(p.h)[base + t + i * per_row] = x[i];
       }
-      sum2 = sum_squares8(sum2, x[i]);
+      sum.add(sum_squares8(x[i]), 0.0f);
       rq_products8(prod[i], x[i], w[i], top);
     }
     if (MANY && row + stride < p.rows) load(row + stride);
-    float sum = f2_lo(sum2) + f2_hi(sum2);
-    rq_reduce<true>(top, sum, red[flip], warps);
+    rq_reduce(top, &sum, red[flip], warps);
     const float inv = rq_inverse<INT8>(top);
     uint2* qv = reinterpret_cast<uint2*>(p.q) + base;
 #pragma unroll
     for (int i = 0; i < CPT; ++i)
       if (t + i * per_row < chunks) qv[t + i * per_row] = rq_codes8<INT8>(prod[i], inv);
-    if (t == 0) rms_store_scale<INT8>(p, row, top, sum);
+    if (t == 0) rms_store_scale<INT8>(p, row, top, __fadd_rn(sum.hi, sum.lo));
     if (!MANY) break;
   }
 }
@@ -246,14 +262,14 @@ __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
 template <bool INT8, bool RESID, int THREADS>
 __global__ void __launch_bounds__(THREADS) rms_norm_quant_wide_kernel(RmsParams p) {
   extern __shared__ uint4 rq_smem[];
-  float* red = reinterpret_cast<float*>(rq_smem);  // two buffers of 64
+  float* red = reinterpret_cast<float*>(rq_smem);  // two buffers
   const int chunks = p.cols >> 3;
-  uint4 *lo = rq_smem + 32, *hi = lo + chunks;
+  uint4 *lo = rq_smem + kRqRedBytes / 16, *hi = lo + chunks;
   allow_dependents();
   const uint4* wv = reinterpret_cast<const uint4*>(p.weight);
   wait_for_producers();
   int flip = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 64) {
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= kRqRed) {
     const int64_t base = row * chunks;
     const uint4* xv = reinterpret_cast<const uint4*>(p.x) + base;
     const uint4* rv = reinterpret_cast<const uint4*>(p.residual) + base;
@@ -264,7 +280,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_quant_wide_kernel(RmsParams 
     cp_async_commit();
     cp_async_wait<0>();
     float top = 0.0f;
-    f2 sum2 = f2_make(0.0f, 0.0f);
+    RowSum sum;
 #pragma unroll 2
     for (int c = threadIdx.x; c < chunks; c += THREADS) {
       uint4 h = lo[c];
@@ -272,13 +288,12 @@ __global__ void __launch_bounds__(THREADS) rms_norm_quant_wide_kernel(RmsParams 
         h = add_bf16x8(h, hi[c]);
         reinterpret_cast<uint4*>(p.h)[base + c] = h;
       }
-      sum2 = sum_squares8(sum2, h);
+      sum.add(sum_squares8(h), 0.0f);
       f2 prod[4];
       rq_products8(prod, h, __ldg(wv + c), top);
       rq_keep(lo + c, hi + c, prod);
     }
-    float sum = f2_lo(sum2) + f2_hi(sum2);
-    rq_reduce<true>(top, sum, red + flip, THREADS / 32);
+    rq_reduce(top, &sum, red + flip, THREADS / 32);
     const float inv = rq_inverse<INT8>(top);
     uint2* qv = reinterpret_cast<uint2*>(p.q) + base;
 #pragma unroll 2
@@ -287,7 +302,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_quant_wide_kernel(RmsParams 
       rq_kept(prod, lo[c], hi[c]);
       qv[c] = rq_codes8<INT8>(prod, inv);
     }
-    if (threadIdx.x == 0) rms_store_scale<INT8>(p, row, top, sum);
+    if (threadIdx.x == 0) rms_store_scale<INT8>(p, row, top, __fadd_rn(sum.hi, sum.lo));
   }
 }
 
@@ -312,7 +327,7 @@ __device__ __forceinline__ void silu_store_scale(const SiluParams& p, int64_t ro
 template <bool INT8, int CPT, bool MANY>
 __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
     silu_mul_quant_kernel(SiluParams p, int per_row) {
-  __shared__ float red[2][64];
+  __shared__ float red[2][kRqRed];
   allow_dependents();
   const int t = threadIdx.x % per_row, chunks = p.cols >> 3, warps = per_row >> 5;
   const int rows_cta = blockDim.x / per_row;
@@ -334,12 +349,12 @@ __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
   const int64_t stride = int64_t(gridDim.x) * rows_cta;
   if (row < p.rows) load(row);
   for (int flip = 0; row < p.rows; row += stride, flip ^= 1) {
-    float top = 0.0f, none = 0.0f;
+    float top = 0.0f;
     f2 prod[CPT][4];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) rq_products8(prod[i], rq_silu8(g[i]), u[i], top);
     if (MANY && row + stride < p.rows) load(row + stride);
-    rq_reduce<false>(top, none, red[flip], warps);
+    rq_reduce(top, nullptr, red[flip], warps);
     const float inv = rq_inverse<INT8>(top);
     uint2* qv = reinterpret_cast<uint2*>(p.q) + row * chunks;
 #pragma unroll
@@ -355,13 +370,13 @@ __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
 template <bool INT8, bool KEEP, int THREADS>
 __global__ void __launch_bounds__(THREADS) silu_mul_quant_wide_kernel(SiluParams p) {
   extern __shared__ uint4 rq_smem[];
-  float* red = reinterpret_cast<float*>(rq_smem);  // two buffers of 64
+  float* red = reinterpret_cast<float*>(rq_smem);  // two buffers
   const int chunks = p.cols >> 3;
-  uint4 *lo = rq_smem + 32, *hi = lo + chunks;
+  uint4 *lo = rq_smem + kRqRedBytes / 16, *hi = lo + chunks;
   allow_dependents();
   wait_for_producers();
   int flip = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 64) {
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= kRqRed) {
     const uint4* gv = reinterpret_cast<const uint4*>(p.gate + row * p.ld);
     const uint4* uv = reinterpret_cast<const uint4*>(p.up + row * p.ld);
     if (KEEP) {
@@ -372,14 +387,14 @@ __global__ void __launch_bounds__(THREADS) silu_mul_quant_wide_kernel(SiluParams
       cp_async_commit();
       cp_async_wait<0>();
     }
-    float top = 0.0f, none = 0.0f;
+    float top = 0.0f;
 #pragma unroll 2
     for (int c = threadIdx.x; c < chunks; c += THREADS) {
       f2 prod[4];
       rq_products8(prod, rq_silu8(KEEP ? lo[c] : gv[c]), KEEP ? hi[c] : uv[c], top);
       if (KEEP) rq_keep(lo + c, hi + c, prod);
     }
-    rq_reduce<false>(top, none, red + flip, THREADS / 32);
+    rq_reduce(top, nullptr, red + flip, THREADS / 32);
     const float inv = rq_inverse<INT8>(top);
     uint2* qv = reinterpret_cast<uint2*>(p.q) + row * chunks;
 #pragma unroll 2

@@ -263,7 +263,9 @@ MM_SHAPES = [(1, 1, 16), (1, 7, 16), (1, 64, 48), (2, 129, 64), (3, 1000, 4096),
              (17, 640, 512), (31, 1023, 272), (33, 257, 1056), (64, 6144, 2048), (65, 384, 640),
              (100, 1111, 3088), (128, 128, 64), (129, 255, 96), (200, 10007, 256), (256, 2048, 2064),
              (257, 513, 2096), (300, 4100, 1024), (511, 300, 4096), (1000, 1024, 1040),
-             (2049, 777, 528)]
+             (2049, 777, 528), (12, 64, 16), (40, 65, 16), (90, 64, 16), (300, 64, 16),
+             # several tiles a CTA, several drains a tile
+             (20, 30000, 1104), (60, 25000, 2064), (120, 41000, 1040), (2500, 9000, 2064)]
 
 
 @gpu
@@ -321,6 +323,78 @@ def test_int8_matmul_guards_and_nan_scales(m):
     assert not torch.isfinite(rest[:, 5]).any()
     rest[:, 5] = 0
     assert bool(torch.isfinite(rest).all())
+
+
+@gpu
+@pytest.mark.parametrize("m", [2, 12, 30, 70, 140])
+def test_int8_matmul_unaligned_vectors(m):
+    """The output, the scales and the bias start at any of their elements."""
+    n, k = 259, 144
+    a, w = int8((m, k), 1), int8((n, k), 2)
+    sa, sw, b = f32(m + 1, 3)[1:], f32(n + 3, 4)[3:], normal((n + 1,), 5)[1:]
+    buf = torch.zeros(m * n + 1, dtype=torch.bfloat16, device="cuda")
+    out = buf[1:].view(m, n)
+    fq.int8_matmul(a, sa, w, sw, bias=b, out=out)
+    assert torch.equal(out, fq.int8_matmul(a, sa.clone(), w, sw.clone(), bias=b.clone()))
+    assert buf[0] == 0
+
+
+@gpu
+def test_int8_matmul_batch_of_one_equals_rows():
+    """A token's result does not depend on which other tokens are there beyond the sums' order:
+    exact sums make it the same for every kernel."""
+    a, w = int8((300, 768), 1, -50, 51), int8((640, 768), 2, -50, 51)
+    sa, sw = f32(300, 3), f32(640, 4)
+    full = fq.int8_matmul(a, sa, w, sw, out_dtype=torch.float32)
+    for m in (1, 8, 9, 16, 17, 33, 65, 129, 200):
+        assert torch.equal(full[:m], fq.int8_matmul(a[:m], sa[:m], w, sw, out_dtype=torch.float32))
+
+
+# ------------------------------------------------------------------------------------------
+# offsets beyond 32 bits
+# ------------------------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("m", [1, 16, 40, 128, 300])
+def test_int8_matmul_large_weights(m):
+    n, k = 140000, 32768  # 4.6 GB
+    w = torch.zeros(n, k, dtype=torch.int8, device="cuda")
+    w[-40:] = int8((40, k), 1)
+    w[:24] = int8((24, k), 2)
+    a, sa, sw = int8((m, k), 3), f32(m, 4), f32(n, 5)
+    out = fq.int8_matmul(a, sa, w, sw)
+    for part in (slice(0, 24), slice(n - 40, n)):
+        ref = plain_matmul(a, sa, w[part], sw[part], None, None)
+        assert float(((out[:, part].double() - ref).abs() / ref.abs().clamp_min(1)).max()) < 2.0 ** -7
+    assert not out[:, 24:-40].any()
+
+
+@gpu
+def test_int8_matmul_large_output():
+    m, n, k = 70000, 32768, 64  # 2.3e9 values
+    a, w, sa, sw = int8((m, k), 1), int8((n, k), 2), f32(m, 3), f32(n, 4)
+    out = fq.int8_matmul(a, sa, w, sw)
+    for r in (slice(0, 3), slice(65534, 65540), slice(m - 3, m)):
+        ref = plain_matmul(a[r], sa[r], w, sw, None, None)
+        assert bool(((out[r].double() - ref).abs() <= 2.0 ** -8 * 1.001 * ref.abs()).all())
+
+
+@gpu
+def test_rows_beyond_four_gigabytes():
+    rows, cols = 300000, 8192  # 4.9 GB of bf16
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[:] = normal((1, cols), 1)
+    tail = normal((5, cols), 2)
+    x[-5:] = tail
+    w = normal((cols,), 3)
+    q, s = fq.rms_norm_quant(x, w)
+    want = fq.rms_norm_quant(tail, w)
+    assert torch.equal(q[-5:], want[0]) and torch.equal(s[-5:], want[1])
+    assert bool((q[:-5] == q[0]).all()) and bool((s[:-5] == s[0]).all())
+    q, s = fq.silu_mul_quant(x[:, :4096], x[:, 4096:])
+    want = fq.silu_mul_quant(tail[:, :4096], tail[:, 4096:])
+    assert torch.equal(q[-5:], want[0]) and torch.equal(s[-5:], want[1])
+    assert bool((q[:-5] == q[0]).all())
 
 
 # ------------------------------------------------------------------------------------------
@@ -392,6 +466,59 @@ def test_graph_capture_and_streams(rows):
     y = fq.int8_matmul(q2, s2, w["down"], w["down_s"], stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(h, want[0]) and torch.equal(y, want[1])
+    assert fq.device_error() == 0
+
+
+@gpu
+def test_first_calls_of_a_process_captured():
+    """Nothing has run before the capture: the launch caches fill during it."""
+    code = """
+import torch, fp8_quant_row_gb300 as fq
+torch.cuda.init()
+x = torch.randn(40, 1024, device="cuda").bfloat16(); w = torch.ones(1024, device="cuda").bfloat16()
+W = torch.randint(-127, 128, (2048, 1024), device="cuda", dtype=torch.int8); sw = torch.rand(2048, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    outs = []
+    for m in (1, 12, 40):
+        q, s = fq.rms_norm_quant(x[:m], w)
+        y = fq.int8_matmul(q, s, W, sw)
+        outs.append((m, y, *fq.silu_mul_quant(y[:, :1024], y[:, 1024:])))
+g.replay(); torch.cuda.synchronize()
+for m, y, q2, s2 in outs:
+    q, s = fq.rms_norm_quant(x[:m], w)
+    assert torch.equal(y, fq.int8_matmul(q, s, W, sw))
+    a, b = fq.silu_mul_quant(y[:, :1024], y[:, 1024:])
+    assert torch.equal(a, q2) and torch.equal(b, s2)
+print("fine")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0 and "fine" in out.stdout, out.stderr[-2000:]
+
+
+@gpu
+def test_two_streams_at_once():
+    w = block_weights(1024, 2048)
+    xs = [normal((m, 1024), 30 + m) for m in (1, 24, 150, 600)]
+    rs = [normal(x.shape, 60) for x in xs]
+    want = [mlp_block(x, r, w) for x, r in zip(xs, rs)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[] for _ in xs]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(mlp_block(xs[i], rs[i], w))
+    torch.cuda.synchronize()
+    for i, runs in enumerate(got):
+        for h, y in runs:
+            assert torch.equal(h, want[i][0]) and torch.equal(y, want[i][1])
     assert fq.device_error() == 0
 
 
