@@ -246,6 +246,17 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+_entry = {}
+
+
+def _function(name: str):
+    """The library's entry point, looked up once."""
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(_capi.lib(), name)
+    return f
+
+
 def _raw_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
@@ -288,9 +299,13 @@ def rms_norm_quant(x, weight, *, residual=None, dtype=torch.int8, eps: float = E
     if qt is None:
         raise TypeError(f"dtype: expected torch.int8 or torch.float8_e4m3fn, got {dtype}")
     dev = _check_device(x, "x", weight, residual, residual_out, q, scale)
-    _bf16(x, "x"), _bf16(weight, "weight")
+    if x.dtype is not _BF16 or not x.is_contiguous():
+        _bf16(x, "x")
+    if weight.dtype is not _BF16 or not weight.is_contiguous():
+        _bf16(weight, "weight")
     shape = x.shape
-    rows, cols = _rows_cols(x)
+    cols = shape[-1]
+    rows = x.numel() // cols if cols else 0
     if weight.numel() != cols:
         raise TypeError(f"weight: expected {cols} values, got {tuple(weight.shape)}")
     h = None
@@ -304,7 +319,7 @@ def rms_norm_quant(x, weight, *, residual=None, dtype=torch.int8, eps: float = E
     q = _new(shape, dtype, x, stream) if q is None else _given(q, shape, dtype, "q")
     scale = (_new(shape[:-1], _F32, x, stream) if scale is None
              else _given(scale, shape[:-1], _F32, "scale"))
-    st = _capi.lib().fp8q_rms_norm_quant(None if h is None else h.data_ptr(), q.data_ptr(),
+    st = _function("fp8q_rms_norm_quant")(None if h is None else h.data_ptr(), q.data_ptr(),
                                          scale.data_ptr(), x.data_ptr(),
                                          None if h is None else residual.data_ptr(),
                                          weight.data_ptr(), qt, rows, cols, eps,
@@ -329,7 +344,7 @@ def silu_mul_quant(gate, up, *, dtype=torch.int8, q=None, scale=None, stream=Non
     q = _new(shape, dtype, gate, stream) if q is None else _given(q, shape, dtype, "q")
     scale = (_new(shape[:-1], _F32, gate, stream) if scale is None
              else _given(scale, shape[:-1], _F32, "scale"))
-    st = _capi.lib().fp8q_silu_mul_quant(q.data_ptr(), scale.data_ptr(), gate.data_ptr(),
+    st = _function("fp8q_silu_mul_quant")(q.data_ptr(), scale.data_ptr(), gate.data_ptr(),
                                          up.data_ptr(), ld, qt, rows, cols,
                                          _raw_stream(stream, dev))
     if st:
@@ -355,7 +370,7 @@ def int8_matmul(a, a_scale, w, w_scale, *, bias=None, out_dtype=torch.bfloat16, 
         raise TypeError(f"bias: expected {n} values, got {tuple(bias.shape)}")
     shape = (*a.shape[:-1], n)
     out = _new(shape, out_dtype, a, stream) if out is None else _given(out, shape, out_dtype, "out")
-    st = _capi.lib().fp8q_int8_matmul(out.data_ptr(), a.data_ptr(), lda,
+    st = _function("fp8q_int8_matmul")(out.data_ptr(), a.data_ptr(), lda,
                                       _row_scale(a_scale, m, "a_scale"), w.data_ptr(),
                                       _row_scale(w_scale, n, "w_scale"),
                                       None if bias is None else bias.data_ptr(), ot, m, n, k,

@@ -490,7 +490,7 @@ fp8q_status clusters_resident(const void* fn, int threads, size_t smem, int size
 // Tiles of a CG x BT kernel for this product and an estimate of its time in us: rounds of tiles
 // times a tile's stages, plus a launch's fixed part (kTcStage and kTcFixed, fitted to 13 token counts
 // at five weight shapes; within about 10% of each measurement there).
-constexpr double kTcFixed = 4.0, kTcExchange = 4.0;  // the exchange and 0.03 a token column
+constexpr double kTcFixed = 4.0, kTcExchange = 0.8, kTcColumn = 0.02;  // sums' exchange
 
 template <int CG, int BT>
 constexpr double tc_stage_us() {
@@ -525,7 +525,7 @@ fp8q_status plan_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, fp8q::TcPar
   const int64_t slots = dev.sms / CG;
   const double rounds = p->split > 1 ? 1.0 : double((p->tiles + slots - 1) / slots);
   *cost = rounds * p->steps_per * tc_stage_us<CG, BT>() + kTcFixed +
-          (p->split > 1 ? kTcExchange + 0.03 * double(std::min<int64_t>(mm.m, BT)) : 0.0);
+          (p->split > 1 ? kTcExchange + kTcColumn * double(std::min<int64_t>(mm.m, BT)) : 0.0);
   return FP8Q_OK;
 }
 
@@ -596,30 +596,33 @@ fp8q_status consider_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, double*
   return st;
 }
 
-// The kernel with the least estimated time. Measured at 6144 x 6144 weights (us; 8 and 16: the
-// kernel for few tokens, CGxBT: the tensor-memory kernel):
+// The kernel with the least estimated time. Measured (us; 8 and 16: the kernel for few tokens,
+// CGxBT: the tensor-memory kernel), at 6144 x 6144 weights:
 //   tokens      8     16   1x32   1x64  1x128  2x128  2x256
-//        8   10.5   14.6   13.6   15.0   18.0   23.1   35.2
-//       32                 14.4   15.8   17.4   23.4   35.9
-//       64                 20.3   16.9   18.5   23.8   36.0
-//      128                 37.0   23.0   21.0   24.0   36.1
-//      256                 53.9   41.6   25.9   24.4   36.3
-//     1024                186.3  115.9   69.9   63.2   67.3
-//     4608                769.9  438.4  266.9  238.8  196.3
-// and with 36864 x 6144 weights 8 tokens take 43.7 / 51.6 / 39.8 us (8, 16, 1x32), 128 tokens
-// 52.0 / 47.7 / 70.1 us (1x128, 2x128, 2x256).
+//        8    9.6   11.9   13.6   15.0   17.4   23.7   35.2
+//       32                 14.0   15.2   16.9   23.6   35.9
+//       64                 20.5   16.0   17.4   24.3   36.1
+//      128                 37.3   23.1   18.9   24.4   36.1
+//      256                 54.2   42.1   26.5   24.9   36.4
+//     1024                       116.6   70.8   64.7   67.8
+//     4608                       443.0  269.2  243.1  193.1
+// at 36864 x 6144, 8 tokens: 42.1 / 55.1 / 39.7 / 46.7 / 67.1 / 45.0 / 66.9, 128 tokens: 1x128 51.9,
+// 2x128 46.9, 2x256 69.5; at 2048 x 2048, 8 tokens: 3.5 / 4.3 / 5.9, 192 tokens: 1x64 8.9, 2x128 10.8.
 template <bool F32>
 fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
                                cudaStream_t stream) {
   double best = 1e30;
   int which = 0;
-  const double weights = double(p.n) * double(p.k);
+  // bytes at the rate that many channel groups reach, and how unevenly few groups fall on the SMs
+  const int64_t groups = (p.n + 15) / 16, per_sm = (groups + dev.sms - 1) / dev.sms;
+  const double uneven = per_sm <= 3 ? double(per_sm * dev.sms) / double(groups) : 1.0;
+  const double weights = double(p.n) * double(p.k) * std::min(uneven, 2.0);
   if (p.m <= 8) best = 3.0 + weights / 5.9e6, which = 8;
   else if (p.m <= 16) best = 3.0 + weights / 4.2e6, which = 16;
   fp8q_status st = FP8Q_OK;
-  if (p.m <= 64) st = consider_tc<1, 32, F32>(p, dev, &best, &which);
-  if (st == FP8Q_OK && p.m > 32 && p.m <= 128) st = consider_tc<1, 64, F32>(p, dev, &best, &which);
-  if (st == FP8Q_OK && p.m > 64 && p.m <= 512) st = consider_tc<1, 128, F32>(p, dev, &best, &which);
+  if (p.m <= 128) st = consider_tc<1, 32, F32>(p, dev, &best, &which);
+  if (st == FP8Q_OK && p.m > 32 && p.m <= 512) st = consider_tc<1, 64, F32>(p, dev, &best, &which);
+  if (st == FP8Q_OK && p.m > 64 && p.m <= 1024) st = consider_tc<1, 128, F32>(p, dev, &best, &which);
   if (st == FP8Q_OK && p.m > 64) st = consider_tc<2, 128, F32>(p, dev, &best, &which);
   if (st == FP8Q_OK && p.m > 128) st = consider_tc<2, 256, F32>(p, dev, &best, &which);
   if (st != FP8Q_OK) return st;

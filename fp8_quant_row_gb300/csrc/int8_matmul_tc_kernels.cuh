@@ -274,6 +274,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int steps = CG == 2 ? p.steps : min(p.steps_per, p.steps - s0);
 
   allow_dependents();
+  if (threadIdx.x == 64) {  // the copies' descriptions, ahead of their first use
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kRawStages; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -479,6 +483,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = tc_wait_warp(d_full, chunk & 1);
         if (!ok) break;
         tc_fence_after();
+        // the last products are in: this CTA's stages are free, which the other CTAs of the
+        // tile wait to hear
+        if (CG == 1 && ctas > 1 && warp == kTcFirstDrain && s + kTcChunk / kTcStep >= steps &&
+            lane < ctas && lane != int(rank))
+          mbar_arrive_cluster(map_rank(smem_addr(peers_ready), lane));
         if (s == 0) {
           // The four warps of a side store the same values. Their buffer is free: this tile's
           // first products were issued after every warp had drained the tile before, which is
@@ -525,8 +534,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive(sums_laid);
         ok = tc_wait_warp(sums_laid, 0);
         if (warp == kTcFirstDrain) {
-          if (lane < ctas && lane != int(rank))
-            mbar_arrive_cluster(map_rank(smem_addr(peers_ready), lane));
           ok = tc_wait_warp(peers_ready, 0) && ok;
           const int to0 = min(lane * per, cols), to1 = min(to0 + per, cols);
           if (ok && lane < ctas && lane != int(rank) && to1 > to0)
@@ -539,14 +546,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (n < p.mm.n) {
           uint8_t* o = o0 + (own0 + side - side * kAcc) * step;
 #pragma unroll 1
-          for (int col = own0 + side; col < own1; col += 2, o += 2 * step) {
-            float v = 0.0f;  // in the order of k
-#pragma unroll 4
-            for (int r = 0; r < ctas; ++r)
-              v += lds_f32((r == int(rank) ? send + uint32_t(col * 512)
-                                           : get + uint32_t((r * per + col - own0) * 512)) + at);
-            const float as = scales[col];
-            mm_store<F32>(o, mm_value(v, ws, as, bias));
+          for (int col = own0 + side; col < own1; col += 8) {  // four columns at a time
+            float v[4] = {};
+#pragma unroll 1
+            for (int r = 0; r < ctas; ++r) {  // in the order of k
+              const uint32_t from = (r == int(rank) ? send + uint32_t(col * 512)
+                                                    : get + uint32_t((r * per + col - own0) * 512)) + at;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (col + 2 * i < own1) v[i] += lds_f32(from + i * 1024);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i, o += 2 * step)
+              if (col + 2 * i < own1) mm_store<F32>(o, mm_value(v[i], ws, scales[col + 2 * i], bias));
           }
         }
       } else if (n < p.mm.n) {
