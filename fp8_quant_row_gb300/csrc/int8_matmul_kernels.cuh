@@ -1,5 +1,6 @@
 // int8_matmul_kernels.cuh -- out[m, n] = (sum_k a[m, k] w[n, k]) * w_scale[n] * a_scale[m]
-// (+ bias[n]) for int8 a and w, sm_103a.
+// (+ bias[n]) for int8 a and w, sm_103a: what its two kernels share (few tokens, and tiles on
+// the 5th-generation tensor cores).
 #pragma once
 
 #include "fp8q_device.cuh"

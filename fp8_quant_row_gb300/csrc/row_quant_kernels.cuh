@@ -9,6 +9,13 @@
 //   e4m3   E4M3(RN(p * inv))
 // The norm's 1/rms is common to a row, cancels in p / P and only enters the row's scale, so
 // the codes do not depend on the order of any sum.
+// Bound: HBM. Measured on one GB300 (CUDA-graph replay, inputs larger than the L2 cache; share of
+// the 6690 GB/s of a plain copy): norm with residual 16384 x 8192 143 us (98%), 4608 x 6144 32.5
+// (91%), without residual 18.5 (68%: three bytes a value leave 7.6 values a clock and SM to form
+// and encode); silu 4608 x 18432 64.9 us (98%), 4608 x 10240 37.4 (94%); one row of 6144 2.1 us,
+// of 18432 3.0 us. What carried them: the products kept between the two passes as fp32 pairs (no
+// second unpacking), all loads of a row issued at once, the next row's before the reduction.
+//
 // A row with a NaN or infinite product gets the scale NaN and codes 0; one whose products are
 // all below 2^-100 in magnitude gets the scale 0 and codes 0.
 #pragma once

@@ -261,7 +261,8 @@ fp8q_status fp8q_qkv_epilogue(void* joint_q, void* joint_k, void* joint_v,
  *           E4M3(RN_fp32(p_j * inv))                         FP8Q_E4M3
  *   scale = P / sqrt(mean_j(h_j^2) + eps) / QMAX             in fp32
  * so q_j * scale approximates the normalised h_j * w_j / rms. 1/rms cancels in q: the codes
- * are those of exact products whatever the order of the sum.
+ * are those of exact products whatever the order of the sum. The sum of squares carries its
+ * rounding errors along, so that a row's scale does not depend on the call's row count either.
  *
  *   residual_out  out [rows, cols] bf16; NULL exactly when residual_bf16 is; may be exactly
  *                     the residual buffer (in-place update)
@@ -304,7 +305,10 @@ fp8q_status fp8q_silu_mul_quant(void* q, float* q_scale, const void* gate_bf16,
 /*
  * Product of 8-bit integers with scales for each row and output channel:
  *   out[i, j] = RN(RN_fp32(acc * w_scale[j]) * a_scale[i] + bias[j]),
- *   acc = sum_k a[i, k] * w[j, k]
+ *   acc = sum_k a[i, k] * w[j, k], exact while sums of the products' magnitudes stay within
+ *         2^24 (always for k <= 1024); else sums of 1024 products are exact and are added
+ *         in fp32
+ * A row's result does not depend on the other rows, nor, where acc is exact, on m.
  *
  *   out       out [m, n] bf16 (FP8Q_OUT_BF16) or fp32 (FP8Q_OUT_FP32), contiguous, aligned to
  *                 its element
@@ -347,7 +351,8 @@ int fp8q_last_cuda_error(void);
 const char* fp8q_last_error_detail(void);
 
 /* Library ABI version: 0x00MMmmpp (0.2.0: token_cat_nvfp4 and qkv_epilogue added; 0.3.0:
- * fp8q_device_error added). */
+ * fp8q_device_error added, later rms_norm_quant, silu_mul_quant and int8_matmul: new entry
+ * points beside unchanged ones keep the number). */
 int fp8q_version(void);
 
 #ifdef __cplusplus
