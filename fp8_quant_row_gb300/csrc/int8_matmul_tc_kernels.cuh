@@ -59,6 +59,9 @@ struct TcLayout {
   static constexpr int kRegsDrain = BT > 128 ? 152 : 104;
   static_assert(kRegsIssue + 4 * kRegsConvert + 2 * kRegsDrain <= 7 * 72, "");
   static constexpr int kRowsB = BT / CG;
+  // A pair's accumulators are two halves, of the tokens' first and second halves in each CTA, so
+  // that one is drained while the other's products run.
+  static constexpr int kHalves = CG;
   static constexpr int kRawA = 128 * kTcStep, kRawB = kRowsB * kTcStep, kRaw = kRawA + kRawB;
   static constexpr int kConvB = kRowsB * kTcStep * 2;
   static constexpr int kConvStages = 3;
@@ -66,14 +69,14 @@ struct TcLayout {
   static constexpr int kScaleBytes = 2 * BT * 4;  // the token scales of two tiles in turn
   static constexpr int kRawStages0 =
       (kTcSmemLimit - kBarBytes - kScaleBytes - kConvStages * kConvB) / kRaw;
-  static constexpr int kRawStages = kRawStages0 > 9 ? 9 : kRawStages0;
+  static constexpr int kRawStages = kRawStages0 > 8 ? 8 : kRawStages0;
   static constexpr int kBytes = kRawStages * kRaw + kConvStages * kConvB + kBarBytes + kScaleBytes;
   static constexpr int kColsA = BT;  // first column of the converted weights
   static constexpr int kCols = kColsA + kConvStages * 64 <= 256 ? 256 : 512;
   // partial sums, sent and got, over the stages (free by then)
   static_assert(CG == 2 || (2 * BT + 8) * 512 <= kRawStages * kRaw + kConvStages * kConvB, "");
   static_assert(kBytes <= kTcSmemLimit && kRawStages >= 2 && kColsA + kConvStages * 64 <= 512, "");
-  static_assert(8 * (2 * kRawStages + 2 * kConvStages + 7) <= kBarBytes, "");
+  static_assert(8 * (2 * kRawStages + 2 * kConvStages + 9) <= kBarBytes, "");
 };
 
 // ---- instructions -------------------------------------------------------------------------
@@ -266,9 +269,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* raw_empty = raw_full + L::kRawStages;
   uint64_t* conv_full = raw_empty + L::kRawStages;   // first CTA's counts for the pair
   uint64_t* conv_empty = conv_full + L::kConvStages;
-  uint64_t* d_full = conv_empty + L::kConvStages;
-  uint64_t* d_empty = d_full + 1;                    // first CTA's counts for the pair
-  uint64_t* peers_ready = d_empty + 1;               // CG = 1: the others' stages are free
+  uint64_t* d_full = conv_empty + L::kConvStages;    // one for each half
+  uint64_t* d_empty = d_full + 2;                    // the same; first CTA's counts for the pair
+  uint64_t* peers_ready = d_empty + 2;               // CG = 1: the others' stages are free
   uint64_t* sums_full = peers_ready + 1;             // CG = 1: the others' sums are here
   uint64_t* sums_laid = sums_full + 1;               // CG = 1: this CTA's sums are in its memory
   uint64_t* idle = sums_laid + 1;                    // all matrix instructions are done
@@ -296,8 +299,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&conv_full[i], 8 * CG);
       mbar_init(&conv_empty[i], 1);
     }
-    mbar_init(d_full, 1);
-    mbar_init(d_empty, 8 * CG);
+    for (int h = 0; h < L::kHalves; ++h) {
+      mbar_init(&d_full[h], 1);
+      mbar_init(&d_empty[h], 8 * CG / L::kHalves);
+    }
     mbar_init(peers_ready, CG == 1 && ctas > 1 ? ctas - 1 : 1);
     mbar_init(sums_full, 1);
     mbar_init(sums_laid, 8);
@@ -338,8 +343,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp == 1 && half == 0) {
       // The whole warp goes through the loop and one lane issues: values that the warp shares
       // stay in uniform registers, where the instructions want them.
-      // fp32 accumulators, fp16 operands, K-major, N = BT, M = CG * 128
-      constexpr uint32_t idesc = (1u << 4) | (uint32_t(BT / 8) << 17) | (uint32_t(CG * 8) << 24);
+      // fp32 accumulators, fp16 operands, K-major, N = BT or half of it, M = CG * 128
+      constexpr uint32_t idesc = (1u << 4) | (uint32_t(BT / L::kHalves / 8) << 17) | (uint32_t(CG * 8) << 24);
       // 128-byte swizzle, 1024 bytes between groups of eight rows
       constexpr uint32_t desc_hi = (2u << 29) | (1u << 14) | 64u;
       const uint32_t desc_lo = (1u << 16) | ((smem_addr(conv) & 0x3FFFFu) >> 4);
@@ -350,25 +355,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int64_t t = first; t < p.tiles && ok; t += stride) {
         for (int s = 0; s < steps; ++s) {
           const bool fresh = s % (kTcChunk / kTcStep) == 0;
-          if (fresh) {
-            ok = tc_wait_warp(d_empty, (chunk & 1) ^ 1);
-            ++chunk;
-            if (!ok) break;
-          }
+          const bool last = s % (kTcChunk / kTcStep) == kTcChunk / kTcStep - 1 || s == steps - 1;
           ok = tc_wait_warp(&conv_full[st], use);
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = d + L::kColsA + st * 64, b = desc_lo + st * (L::kConvB >> 4);
-          if (leader) {
-            tc_mma<CG, false>(d, a, b, desc_hi, idesc, !fresh);
+          const uint32_t a = d + L::kColsA + st * 64;
 #pragma unroll
-            for (int j = 1; j < kTcStep / 16; ++j)
-              tc_mma<CG, true>(d, a + j * 8, b + (j / 4) * (L::kRowsB * 8) + (j % 4) * 2, desc_hi,
-                               idesc, 1);
-            tc_commit<CG>(&conv_empty[st]);
-            if (s % (kTcChunk / kTcStep) == kTcChunk / kTcStep - 1 || s == steps - 1)
-              tc_commit<CG>(d_full);
+          for (int h = 0; h < L::kHalves; ++h) {
+            if (fresh) ok = tc_wait_warp(&d_empty[h], (chunk & 1) ^ 1) && ok;
+            tc_fence_after();
+            const uint32_t dh = d + h * (BT / 2);
+            const uint32_t b = desc_lo + st * (L::kConvB >> 4) + h * (L::kRowsB / 2 * 8);
+            if (leader && ok) {
+              tc_mma<CG, false>(dh, a, b, desc_hi, idesc, !fresh);
+#pragma unroll
+              for (int j = 1; j < kTcStep / 16; ++j)
+                tc_mma<CG, true>(dh, a + j * 8, b + (j / 4) * (L::kRowsB * 8) + (j % 4) * 2,
+                                 desc_hi, idesc, 1);
+              if (last) tc_commit<CG>(&d_full[h]);
+            }
           }
+          if (!ok) break;
+          if (leader) tc_commit<CG>(&conv_empty[st]);
+          if (last) ++chunk;
           if (++st == L::kConvStages) st = 0, use ^= 1;
         }
       }
@@ -462,7 +470,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int kAcc = BT / 2;  // token columns of this warp
     const int side = (warp - kTcFirstDrain) >> 2, quarter = warp & 3;
     const uint32_t src = tmem + side * kAcc + (uint32_t(quarter) << 21);
-    const uint32_t empty0 = map_rank(smem_addr(d_empty), rank - half);
+    const uint32_t empty0 = map_rank(smem_addr(&d_empty[side % L::kHalves]), rank - half);
     uint32_t chunk = 0;
     bool ok = true;
     float* scales = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + L::kBarBytes);
@@ -471,14 +479,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int64_t tn, tm;
       tc_tile(p, t, tn, tm);
       const int64_t n = tn * (128 * CG) + half * 128 + quarter * 32 + lane;
-      const int64_t m0 = tm * BT + side * kAcc, left = p.mm.m - m0;
+      // the tokens of this warp's columns: two runs of half of them
+      const int64_t m0 = tm * BT + side * (CG == 2 ? kAcc / 2 : kAcc);
+      constexpr int kRun = CG == 2 ? kAcc : kAcc / 2;  // from the first run to the second
       // the scales while the products run
       constexpr int kMine = (kAcc + 31) / 32;
       float as[kMine];
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int c = i * 32 + lane;
-        as[i] = c < kAcc && c < left ? p.mm.a_scale[m0 + c] : 0.0f;
+        const int64_t m = m0 + c % (kAcc / 2) + (c >= kAcc / 2 ? kRun : 0);
+        as[i] = c < kAcc && m < p.mm.m ? p.mm.a_scale[m] : 0.0f;
       }
       float ws = 0.0f, bias = 0.0f;
       if (n < p.mm.n) {
@@ -489,7 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) acc[i] = 0.0f;
       for (int s = 0; s < steps; s += kTcChunk / kTcStep, ++chunk) {
-        ok = tc_wait_warp(d_full, chunk & 1);
+        ok = tc_wait_warp(&d_full[side % L::kHalves], chunk & 1);
         if (!ok) break;
         tc_fence_after();
         // the last products are in: this CTA's stages are free, which the other CTAs of the
@@ -517,7 +528,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if (CG == 2) mbar_arrive_cluster(empty0);
-          else mbar_arrive(d_empty);
+          else mbar_arrive(&d_empty[0]);
         }
       }
       if (!ok) break;
@@ -571,16 +582,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       } else if (n < p.mm.n) {
-        uint8_t* o = o0;
-        const int cols = left < kAcc ? int(left) : kAcc;
 #pragma unroll
-        for (int c = 0; c < kAcc; c += 4) {
-          const float4 sc = lds128(reinterpret_cast<const float4*>(scales + side * kAcc + c));
+        for (int run = 0; run < 2; ++run) {
+          uint8_t* o = o0 + run * kRun * step;
+          const int64_t left = p.mm.m - m0 - run * kRun;
+          const int cols = left < kAcc / 2 ? int(left) : kAcc / 2;
 #pragma unroll
-          for (int i = 0; i < 4; ++i, o += step)
-            if (c + i < cols)
-              mm_store<F32>(o, mm_value(acc[c + i], ws,
-                                        i == 0 ? sc.x : i == 1 ? sc.y : i == 2 ? sc.z : sc.w, bias));
+          for (int c = 0; c < kAcc / 2; c += 4) {
+            const float4 sc = lds128(
+                reinterpret_cast<const float4*>(scales + side * kAcc + run * (kAcc / 2) + c));
+#pragma unroll
+            for (int i = 0; i < 4; ++i, o += step)
+              if (c + i < cols)
+                mm_store<F32>(o, mm_value(acc[run * (kAcc / 2) + c + i], ws,
+                                          i == 0 ? sc.x : i == 1 ? sc.y : i == 2 ? sc.z : sc.w,
+                                          bias));
+          }
         }
       }
       scales = parity ? scales - BT : scales + BT;
