@@ -494,7 +494,7 @@ constexpr double kTcFixed = 4.0, kTcExchange = 0.8, kTcColumn = 0.02;  // sums' 
 
 template <int CG, int BT>
 constexpr double tc_stage_us() {
-  return CG == 2 ? (BT == 256 ? 0.66 : 0.43) : BT == 128 ? 0.50 : BT == 64 ? 0.41 : 0.37;
+  return CG == 2 ? (BT == 256 ? 0.64 : 0.43) : BT == 128 ? 0.50 : BT == 64 ? 0.41 : 0.37;
 }
 
 template <int CG, int BT, bool F32>
