@@ -231,11 +231,11 @@ fp8q_status launch_ws(const fp8q::NssParams& p, const DeviceInfo& dev, int64_t n
   if (n_mod > grid) return FP8Q_OK;  // every CTA must sit inside one modulation group
   if (L::kSmemBytes > size_t(dev.smem_optin)) return FP8Q_OK;
   int bps = 0;
-  fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kTcThreads, L::kSmemBytes, &bps);
+  fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), L::kThreads, L::kSmemBytes, &bps);
   if (st != FP8Q_OK) return st;
   if (bps <= 0) return FP8Q_OK;
   *launched = true;
-  return launch(fn, dim3(unsigned(grid)), dim3(fp8q::kTcThreads), L::kSmemBytes, stream, p, n_mod,
+  return launch(fn, dim3(unsigned(grid)), dim3(L::kThreads), L::kSmemBytes, stream, p, n_mod,
                 kWsDepth);
 }
 
