@@ -446,50 +446,50 @@ fp8q_status int8_map(CUtensorMap* map, const int8_t* p, int64_t rows, int64_t k,
   return FP8Q_OK;
 }
 
-// Clusters of `size` CTAs that are resident at one time, cached per device.
-struct ClusterEntry {
-  int dev;
-  const void* fn;
-  int size, clusters;
+// Clusters of 2 to 8 CTAs that are resident at one time with one CTA an SM, asked once per device.
+// (A cluster stays within one GPC, so larger ones do not fill all SMs: 46 of three CTAs, 36 of
+// four, 15 of eight.)
+struct ClusterFit {
+  std::once_flag once;
+  int fit[9] = {};
+  fp8q_status status = FP8Q_OK;
 };
-ClusterEntry g_cluster[256];
-int g_cluster_n = 0;
+ClusterFit g_cluster[kMaxDevices];
 
-fp8q_status clusters_resident(const void* fn, int threads, size_t smem, int size, int* clusters) {
+fp8q_status cluster_fit(const int** fit) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  int bps = 0;
-  const fp8q_status st = blocks_per_sm(fn, threads, smem, &bps);  // raises the smem limit
-  if (st != FP8Q_OK) return st;
-  std::lock_guard<std::mutex> lock(g_occ_mu);
-  for (int i = 0; i < g_cluster_n; ++i)
-    if (g_cluster[i].dev == dev && g_cluster[i].fn == fn && g_cluster[i].size == size) {
-      *clusters = g_cluster[i].clusters;
-      return FP8Q_OK;
+  if (dev < 0 || dev >= kMaxDevices) return FP8Q_ERR_UNSUPPORTED;
+  ClusterFit& c = g_cluster[dev];
+  std::call_once(c.once, [&c] {
+    using L = fp8q::TcLayout<1, 128>;
+    auto* fn = fp8q::int8_matmul_tc_kernel<1, 128, false>;
+    int bps = 0;
+    c.status = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kTcThreads, L::kBytes, &bps);
+    for (int size = 2; size <= 8 && c.status == FP8Q_OK; ++size) {
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = unsigned(size);
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(unsigned(size));
+      cfg.blockDim = dim3(fp8q::kTcThreads);
+      cfg.dynamicSmemBytes = L::kBytes;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      const cudaError_t err = cudaOccupancyMaxActiveClusters(&c.fit[size], fn, &cfg);
+      if (err != cudaSuccess) c.status = cuda_fail(err, "cudaOccupancyMaxActiveClusters", size);
     }
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = unsigned(size);
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(size));
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters", size);
-  if (g_cluster_n < 256) g_cluster[g_cluster_n++] = ClusterEntry{dev, fn, size, n};
-  *clusters = n;
-  return FP8Q_OK;
+  });
+  *fit = c.fit;
+  return c.status;
 }
 
 // Tiles of a CG x BT kernel for this product and an estimate of its time in us: rounds of tiles
-// times a tile's stages, plus a launch's fixed part (kTcStage and kTcFixed, fitted to 13 token counts
-// at five weight shapes; within about 10% of each measurement there).
+// times a tile's stages, plus a launch's fixed part (fitted to 13 token counts at six weight
+// shapes; the choice is within 10% of the best measured at nearly all of them).
 constexpr double kTcFixed = 4.0, kTcExchange = 0.8, kTcColumn = 0.02;  // sums' exchange
 
 template <int CG, int BT>
@@ -497,50 +497,46 @@ constexpr double tc_stage_us() {
   return CG == 2 ? (BT == 256 ? 0.64 : 0.43) : BT == 128 ? 0.50 : BT == 64 ? 0.41 : 0.37;
 }
 
-template <int CG, int BT, bool F32>
-fp8q_status plan_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, fp8q::TcParams* p,
-                    double* cost) {
-  using L = fp8q::TcLayout<CG, BT>;
-  p->tiles_n = (mm.n + 128 * CG - 1) / (128 * CG);
-  p->tiles_m = (mm.m + BT - 1) / BT;
-  p->tiles = p->tiles_n * p->tiles_m;
-  p->steps = int((mm.k + fp8q::kTcStep - 1) / fp8q::kTcStep);
-  p->split = 1;
-  p->steps_per = p->steps;
+template <int CG, int BT>
+fp8q::TcParams plan_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, const int* fit,
+                       double* cost) {
+  fp8q::TcParams p;
+  p.mm = mm;
+  p.tiles_n = (mm.n + 128 * CG - 1) / (128 * CG);
+  p.tiles_m = (mm.m + BT - 1) / BT;
+  p.tiles = p.tiles_n * p.tiles_m;
+  p.steps = int((mm.k + fp8q::kTcStep - 1) / fp8q::kTcStep);
+  p.split = 1;
+  p.steps_per = p.steps;
   // Fewer tiles than SMs: CTAs of a cluster share a tile's k, each with two stages at least, as
-  // many as leave all clusters resident at once (a cluster stays within one GPC, so larger ones
-  // do not fill all SMs: 46 of three CTAs, 36 of four, 15 of eight).
+  // many as leave all clusters resident at once.
   if (CG == 1) {
-    const void* fn = reinterpret_cast<const void*>(fp8q::int8_matmul_tc_kernel<CG, BT, F32>);
-    for (int s = int(std::min<int64_t>({8, dev.sms / p->tiles, p->steps / 2})); s > 1; --s) {
-      int fit = 0;
-      const fp8q_status st = clusters_resident(fn, fp8q::kTcThreads, L::kBytes, s, &fit);
-      if (st != FP8Q_OK) return st;
-      if (fit < p->tiles) continue;
-      p->steps_per = (p->steps + s - 1) / s;
-      p->split = (p->steps + p->steps_per - 1) / p->steps_per;
-      break;
+    int s = int(std::min<int64_t>({8, dev.sms / p.tiles, p.steps / 2}));
+    while (s > 1 && fit[s] < p.tiles) --s;
+    if (s > 1) {
+      p.steps_per = (p.steps + s - 1) / s;
+      p.split = (p.steps + p.steps_per - 1) / p.steps_per;
     }
   }
   const int64_t slots = dev.sms / CG;
-  const double rounds = p->split > 1 ? 1.0 : double((p->tiles + slots - 1) / slots);
-  *cost = rounds * p->steps_per * tc_stage_us<CG, BT>() + kTcFixed +
-          (p->split > 1 ? kTcExchange + kTcColumn * double(std::min<int64_t>(mm.m, BT)) : 0.0);
-  return FP8Q_OK;
+  const double rounds = p.split > 1 ? 1.0 : double((p.tiles + slots - 1) / slots);
+  *cost = rounds * p.steps_per * tc_stage_us<CG, BT>() + kTcFixed +
+          (p.split > 1 ? kTcExchange + kTcColumn * double(std::min<int64_t>(mm.m, BT)) : 0.0);
+  return p;
 }
 
 template <int CG, int BT, bool F32>
 fp8q_status launch_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, cudaStream_t stream) {
   using L = fp8q::TcLayout<CG, BT>;
   auto* fn = fp8q::int8_matmul_tc_kernel<CG, BT, F32>;
-  fp8q::TcParams p;
-  double cost = 0.0;
-  fp8q_status st = plan_tc<CG, BT, F32>(mm, dev, &p, &cost);
+  const int* fit = nullptr;
+  fp8q_status st = cluster_fit(&fit);
   if (st != FP8Q_OK) return st;
+  double cost = 0.0;
+  const fp8q::TcParams p = plan_tc<CG, BT>(mm, dev, fit, &cost);
   int bps = 0;
   st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kTcThreads, L::kBytes, &bps);
   if (st != FP8Q_OK) return st;
-  p.mm = mm;
   const int ctas = CG == 2 ? 2 : p.split;
   CUtensorMap map_w, map_a;
   st = int8_map(&map_w, mm.w, mm.n, mm.k, mm.k, 128);
@@ -581,19 +577,18 @@ fp8q_status launch_few(const fp8q::MmParams& p, const DeviceInfo& dev, cudaStrea
   // no more CTAs than are resident at once, each with the same number of groups (one more or less
   // by the last): they draw on the memory evenly and end together
   const int64_t per_cta = fp8q::kFewWarps / split;
-  const int64_t rounds = (groups + dev.sms * bps * per_cta - 1) / (dev.sms * bps * per_cta);
+  const int64_t slots = dev.sms * std::max(bps, 1) * per_cta, rounds = (groups + slots - 1) / slots;
   const int64_t grid = (groups + rounds * per_cta - 1) / (rounds * per_cta);
   return launch(fn, dim3(unsigned(grid)), dim3(fp8q::kFewWarps * 32), smem, stream, p, split,
                 int(rounds));
 }
 
-template <int CG, int BT, bool F32>
-fp8q_status consider_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, double* best, int* which) {
-  fp8q::TcParams p;
+template <int CG, int BT>
+void consider_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, const int* fit, double* best,
+                 int* which) {
   double cost = 0.0;
-  const fp8q_status st = plan_tc<CG, BT, F32>(mm, dev, &p, &cost);
-  if (st == FP8Q_OK && cost < *best) *best = cost, *which = CG * 1000 + BT;
-  return st;
+  plan_tc<CG, BT>(mm, dev, fit, &cost);
+  if (cost < *best) *best = cost, *which = CG * 1000 + BT;
 }
 
 // The kernel with the least estimated time. Measured (us; 8 and 16: the kernel for few tokens,
@@ -619,13 +614,14 @@ fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
   const double weights = double(p.n) * double(p.k) * std::min(uneven, 2.0);
   if (p.m <= 8) best = 3.0 + weights / 5.9e6, which = 8;
   else if (p.m <= 16) best = 3.0 + weights / 4.2e6, which = 16;
-  fp8q_status st = FP8Q_OK;
-  if (p.m <= 128) st = consider_tc<1, 32, F32>(p, dev, &best, &which);
-  if (st == FP8Q_OK && p.m > 32 && p.m <= 512) st = consider_tc<1, 64, F32>(p, dev, &best, &which);
-  if (st == FP8Q_OK && p.m > 64 && p.m <= 1024) st = consider_tc<1, 128, F32>(p, dev, &best, &which);
-  if (st == FP8Q_OK && p.m > 64) st = consider_tc<2, 128, F32>(p, dev, &best, &which);
-  if (st == FP8Q_OK && p.m > 128) st = consider_tc<2, 256, F32>(p, dev, &best, &which);
+  const int* fit = nullptr;
+  const fp8q_status st = cluster_fit(&fit);
   if (st != FP8Q_OK) return st;
+  if (p.m <= 128) consider_tc<1, 32>(p, dev, fit, &best, &which);
+  if (p.m > 32 && p.m <= 512) consider_tc<1, 64>(p, dev, fit, &best, &which);
+  if (p.m > 64 && p.m <= 1024) consider_tc<1, 128>(p, dev, fit, &best, &which);
+  if (p.m > 64) consider_tc<2, 128>(p, dev, fit, &best, &which);
+  if (p.m > 128) consider_tc<2, 256>(p, dev, fit, &best, &which);
   switch (which) {
     case 8: return launch_few<1, F32>(p, dev, stream);
     case 16: return launch_few<2, F32>(p, dev, stream);

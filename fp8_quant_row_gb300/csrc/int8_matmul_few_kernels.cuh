@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3)
 #pragma unroll
   for (int i = 0; i < kFewStages - 1; ++i) fetch();
 
-  // This lane's tokens of group i, loaded one group ahead (past k the weights are zero).
+  // This lane's tokens of group i, loaded one group ahead (past k the weights are zero; no
+  // read-only loads: the kernel before may write the tokens while this one has begun).
   uint4 an[2][NT];
   auto tokens = [&](int i) {
 #pragma unroll
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3)
       const int off = k0 + i * step + h * 64;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        an[h][j] = __ldg(reinterpret_cast<const uint4*>(a[j] + (off < k ? off : 0)));
+        an[h][j] = *reinterpret_cast<const uint4*>(a[j] + (off < k ? off : 0));
     }
   };
   tokens(0);

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
   for (int i = 0; i < CPT; ++i) {
     w[i] = make_uint4(0, 0, 0, 0);
     if (t + i * per_row < chunks)
-      w[i] = __ldg(reinterpret_cast<const uint4*>(p.weight) + t + i * per_row);
+      w[i] = reinterpret_cast<const uint4*>(p.weight)[t + i * per_row];
   }
   auto load = [&](int64_t row) {
     const uint4* xv = reinterpret_cast<const uint4*>(p.x) + row * chunks;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_quant_wide_kernel(RmsParams 
       }
       sum.add(sum_squares8(h), 0.0f);
       f2 prod[4];
-      rq_products8(prod, h, __ldg(wv + c), top);
+      rq_products8(prod, h, wv[c], top);
       rq_keep(lo + c, hi + c, prod);
     }
     rq_reduce(top, &sum, red + flip, THREADS / 32);

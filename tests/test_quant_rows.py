@@ -503,6 +503,27 @@ print("fine")
 
 
 @gpu
+@pytest.mark.parametrize("m", [1, 8, 16, 40, 200])
+def test_reused_buffers_back_to_back(m):
+    """Each product reads rows that the call just before it wrote over others, on kernels that may
+    begin while the one before still runs."""
+    d = 1024
+    w, wq, sw = normal((d,), 1), int8((512, d), 2), f32(512, 3)
+    xs = [normal((m, d), 100 + i) for i in range(40)]
+    q, s = torch.empty(m, d, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    torch.cuda.synchronize()
+    outs = []
+    for x in xs:
+        fq.rms_norm_quant(x, w, q=q, scale=s)
+        outs.append(fq.int8_matmul(q, s, wq, sw))
+    torch.cuda.synchronize()
+    for x, out in zip(xs, outs):
+        q, s = fq.rms_norm_quant(x, w)
+        torch.cuda.synchronize()
+        assert torch.equal(out, fq.int8_matmul(q, s, wq, sw))
+
+
+@gpu
 def test_two_streams_at_once():
     w = block_weights(1024, 2048)
     xs = [normal((m, 1024), 30 + m) for m in (1, 24, 150, 600)]
