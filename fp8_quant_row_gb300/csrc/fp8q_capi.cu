@@ -384,12 +384,16 @@ fp8q_status launch_silu_rows(const fp8q::SiluParams& p, const RowShape& s, const
 
 template <bool INT8>
 fp8q_status launch_silu(const fp8q::SiluParams& p, const DeviceInfo& dev, cudaStream_t stream) {
-  const RowShape s = row_shape(p.rows, p.cols / 8, 4, dev.sms);
+  // Four chunks a thread leave room for two CTAs an SM: with many rows shared memory is faster from
+  // there (8192 columns, 4608 rows: 30.8 us against 32.1).
+  const RowShape s = row_shape(p.rows, p.cols / 8, 3, dev.sms);
   switch (s.cpt) {
     case 1: return launch_silu_rows<INT8, 1>(p, s, dev, stream);
     case 2: return launch_silu_rows<INT8, 2>(p, s, dev, stream);
     case 3: return launch_silu_rows<INT8, 3>(p, s, dev, stream);
-    case 4: return launch_silu_rows<INT8, 4>(p, s, dev, stream);
+    case 4:
+      if (s.many) break;
+      return launch_rows(fp8q::silu_mul_quant_kernel<INT8, 4, false>, p, s, dev, stream);
     default: break;
   }
   const size_t smem = size_t(p.cols) * 4 + fp8q::kRqRedBytes;

@@ -330,9 +330,10 @@ __device__ __forceinline__ void silu_store_scale(const SiluParams& p, int64_t ro
   p.scale[row] = s;
 }
 
-// As rms_norm_quant_kernel: a row in the registers of its threads.
+// As rms_norm_quant_kernel: a row in the registers of its threads (three CTAs an SM: 23.0 us at
+// 4608 x 6144 against 25.0 with two; the norm, with its weights and residual, is faster with two).
 template <bool INT8, int CPT, bool MANY>
-__global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
+__global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 3 : 1)
     silu_mul_quant_kernel(SiluParams p, int per_row) {
   __shared__ float red[2][kRqRed];
   allow_dependents();
