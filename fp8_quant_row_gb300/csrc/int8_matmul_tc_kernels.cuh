@@ -27,14 +27,14 @@
 // Conversion of four int8: flip the sign bits (value + 128), place each byte under the fp16
 // exponent of 1024 (1024 + 128 + value, exact), subtract 1152.
 //
-// Measured on one GB300 (graph replay): 4608 x 36864 x 6144 1163 us, 1795 TFLOP/s, 93% of what
-// cuBLAS reaches in bf16 there (1925); 4608 x 6144 x 18432 592 us (1762); tensor pipe active 74%
-// of the elapsed clocks. For a CTA of a pair one stage is 1024 clocks of the tensor cores, and of
-// shared memory too (32 KB each of copies in, reads for conversion, converted tokens, and reads by
-// the tensor cores): weights go to tensor memory so that this is not more. 16 x 36864 x 6144 40 us
-// (85% of HBM), 64 x 6144 x 6144 16 us. What it took, at 4608 x 6144 x 18432: waits and arrivals
-// without cluster-scope fences 993 -> 630 us; issue from uniform registers and two groups of
-// converting warps for either operand 630 -> 560.
+// Measured on one GB300 (graph replay): 4608 x 36864 x 6144 1079 us, 1935 TFLOP/s (cuBLAS in bf16
+// there: 1925 as a burst, 1743 sustained); 4608 x 6144 x 18432 586 us (1781). For a CTA of a pair one
+// stage is 1024 clocks of the tensor cores, and of shared memory too (32 KB each of copies in,
+// reads for conversion, converted tokens, and reads by the tensor cores): weights go to tensor
+// memory so that this is not more; about 1200 are reached. 16 x 36864 x 6144 40 us (86% of HBM),
+// 64 x 6144 x 6144 16 us. What it took, at 4608 x 6144 x 18432: waits and arrivals without
+// cluster-scope fences 993 -> 630 us; issue from uniform registers and two groups of converting
+// warps for either operand 630 -> 560; the accumulators in two halves -> 537.
 //
 // Every wait is bounded; a wait that runs out records the device error bit, the role stops, and
 // the CTA pair meets at the end, where tensor memory is freed.

@@ -12,7 +12,7 @@
 // Bound: HBM. Measured on one GB300 (CUDA-graph replay, inputs larger than the L2 cache; share of
 // the 6690 GB/s of a plain copy): norm with residual 16384 x 8192 143 us (98%), 4608 x 6144 32.5
 // (91%), without residual 18.5 (68%: three bytes a value leave 7.6 values a clock and SM to form
-// and encode); silu 4608 x 18432 64.9 us (98%), 4608 x 10240 37.4 (94%); one row of 6144 2.1 us,
+// and encode); silu 4608 x 18432 65.3 us (97%), 4608 x 10240 37.8 (93%); one row of 6144 2.1 us,
 // of 18432 3.0 us. What carried them: the products kept between the two passes as fp32 pairs (no
 // second unpacking), all loads of a row issued at once, the next row's before the reduction.
 //
