@@ -123,9 +123,17 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity) {
     }
   return true;
 }
-// The same for a whole warp: one answer for all lanes.
+// The same for a whole warp, whose lanes stay together (what follows are warp-wide instructions):
+// every branch is on a vote.
 __device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, tc_wait(bar, parity));
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) {
+      report_device_error(kDevErrWaitTimeout);
+      return false;
+    }
+  return true;
 }
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
@@ -397,12 +405,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int row = weights ? tid : tid % L::kRowsB;
     const int part = weights ? 0 : tid / L::kRowsB * kParts;  // its first chunk
     const uint32_t chunks = weights ? 8 : kParts;
-    uint32_t it = 0;
+    // its next stage of either ring and the phases that it waits for
+    uint32_t rs = turn, cs = turn, raw_phase = 0, conv_phase = 1;
+    int s = int(turn);
     for (int64_t t = first; t < p.tiles && ok; t += stride) {
-      for (int s = 0; s < steps; ++s, ++it) {
-        if ((it & 1) != turn) continue;
-        const uint32_t rs = it % L::kRawStages, cs = it % L::kConvStages;
-        ok = tc_wait_warp(&raw_full[rs], (it / L::kRawStages) & 1);
+      for (; s < steps; s += 2) {
+        ok = tc_wait_warp(&raw_full[rs], raw_phase);
         if (!ok) break;
         const uint8_t* src = raw + rs * L::kRaw + (weights ? 0 : L::kRawA) + row * 128;
         uint8_t* dst = conv + cs * L::kConvB + row * 128;
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (h * 4 + i < chunks)
               v[i] = *reinterpret_cast<const uint4*>(src + (((part + h * 4 + i) ^ (row & 7)) << 4));
           if (h == 0) {
-            ok = tc_wait_warp(&conv_empty[cs], ((it / L::kConvStages) & 1) ^ 1);
+            ok = tc_wait_warp(&conv_empty[cs], conv_phase);
             if (!ok) break;
             tc_fence_after();
           } else {
@@ -464,7 +472,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (CG == 2) mbar_arrive_cluster(full0 + cs * 8);
           else mbar_arrive(&conv_full[cs]);
         }
+        rs += 2;
+        if (rs >= L::kRawStages) rs -= L::kRawStages, raw_phase ^= 1;
+        cs += 2;
+        if (cs >= L::kConvStages) cs -= L::kConvStages, conv_phase ^= 1;
       }
+      s -= steps;
     }
   } else {
     reg_inc<L::kRegsDrain>();
