@@ -498,7 +498,7 @@ constexpr double kTcFixed = 4.0, kTcExchange = 0.8, kTcColumn = 0.02;  // sums' 
 
 template <int CG, int BT>
 constexpr double tc_stage_us() {
-  return CG == 2 ? (BT == 256 ? 0.64 : 0.43) : BT == 128 ? 0.50 : BT == 64 ? 0.41 : 0.37;
+  return CG == 2 ? (BT == 256 ? 0.637 : 0.395) : BT == 128 ? 0.44 : BT == 64 ? 0.38 : 0.35;
 }
 
 template <int CG, int BT>
@@ -598,15 +598,16 @@ void consider_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, const int* fit
 // The kernel with the least estimated time. Measured (us; 8 and 16: the kernel for few tokens,
 // CGxBT: the tensor-memory kernel), at 6144 x 6144 weights:
 //   tokens      8     16   1x32   1x64  1x128  2x128  2x256
-//        8    9.6   11.9   13.6   15.0   17.4   23.7   35.2
-//       32                 14.0   15.2   16.9   23.6   35.9
-//       64                 20.5   16.0   17.4   24.3   36.1
-//      128                 37.3   23.1   18.9   24.4   36.1
-//      256                 54.2   42.1   26.5   24.9   36.4
-//     1024                       116.6   70.8   64.7   67.8
-//     4608                       443.0  269.2  243.1  193.1
-// at 36864 x 6144, 8 tokens: 42.1 / 55.1 / 39.7 / 46.7 / 67.1 / 45.0 / 66.9, 128 tokens: 1x128 51.9,
-// 2x128 46.9, 2x256 69.5; at 2048 x 2048, 8 tokens: 3.5 / 4.3 / 5.9, 192 tokens: 1x64 8.9, 2x128 10.8.
+//        8    9.7   12.0   12.9   13.7   16.9   22.3   34.5
+//       16          12.3   12.9   13.6   17.8   22.3   34.6
+//       32                 13.3   13.9   16.1   22.4   34.6
+//       64                 18.7   14.4   16.8   22.5   34.8
+//      128                 34.1   20.6   18.2   22.6   34.9
+//      256                 49.6   37.2   25.1   23.2   35.1
+//     1024                171.3  103.6   67.6   60.2   65.1
+//     4608                706.6  389.6  258.1  230.0  191.0
+// at 36864 x 6144, 8 tokens: 42.2 / 55.2 / 39.5 / 45.6 / 65.1 / 42.7 / 64.5, 128 tokens: 1x128 51.0,
+// 2x128 46.2, 2x256 67.1; at 2048 x 2048, 8 tokens: 3.6 / 4.4 / 6.1, 200 tokens: 1x64 8.9, 2x128 10.6.
 template <bool F32>
 fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
                                cudaStream_t stream) {
