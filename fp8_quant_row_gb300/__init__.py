@@ -22,7 +22,7 @@ from __future__ import annotations
 import torch
 
 from . import _capi
-from ._build import build
+from ._build import NATIVE, build
 from ._capi import Fp8qError
 
 __all__ = ["nss_fp8", "scale_residual_nss_fp8", "bias_mul_add", "token_cat_fp8",
@@ -213,80 +213,27 @@ def qkv_epilogue(txt: dict, img: dict, heads: int, *, out=None, stream=None):
 
 _QTYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
 _OUT_TYPES = {torch.bfloat16: 0, torch.float32: 1}
-_BF16, _F32, _I8 = torch.bfloat16, torch.float32, torch.int8
+_native_module = None
 
 
-def _check_device(x: torch.Tensor, name: str, *others) -> int:
-    """The library launches on the current device: x and the other tensors have to be there.
-    (Calls for one token take the device a few microseconds: the checks of these functions go by
-    plain attributes, and the raw stream handle.)"""
-    dev = x.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise TypeError(f"tensors on {x.device} and on {t.device}: expected one device")
-    if dev < 0:
-        raise TypeError(f"{name}: expected a CUDA tensor, got {x.device}")
-    if dev != torch._C._cuda_getDevice():
-        raise TypeError(f"{name} is on {x.device}, but the current device is "
-                        f"cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _given(out: torch.Tensor, shape, dtype, name: str) -> torch.Tensor:
-    if out.dtype is not dtype or out.shape != shape or not out.is_contiguous():
-        raise TypeError(f"{name}: expected contiguous {dtype} {tuple(shape)}")
-    return out
-
-
-def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
-    """An output that belongs to the stream it is written on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-_entry = {}
-
-
-def _function(name: str):
-    """The library's entry point, looked up once."""
-    f = _entry.get(name)
-    if f is None:
-        f = _entry[name] = getattr(_capi.lib(), name)
-    return f
-
-
-def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _strided_rows(t: torch.Tensor, dtype, name: str):
-    """(rows, cols, row stride) of a tensor whose rows lie at one stride, columns adjacent."""
-    shape = t.shape
-    if t.dtype is not dtype or not shape:
-        raise TypeError(f"{name}: expected a {dtype} tensor [..., cols], got {t.dtype} "
-                        f"{tuple(shape)}")
-    cols = shape[-1]
-    if t.is_contiguous():
-        return (t.numel() // cols if cols else 0), cols, cols
-    if len(shape) == 2 and t.stride(1) == 1:
-        return shape[0], cols, (t.stride(0) if shape[0] > 1 else cols)
-    try:
-        v = t.view(-1, cols)
-    except RuntimeError:
-        v = None
-    if v is None or v.stride(1) != 1:
-        raise TypeError(f"{name}: rows of shape {tuple(shape)} and strides {t.stride()} do "
-                        "not lie at one row stride with adjacent columns")
-    return v.shape[0], cols, (v.stride(0) if v.shape[0] > 1 else cols)
-
-
-def _row_scale(t: torch.Tensor, n: int, name: str) -> int:
-    if t.dtype is not _F32 or t.numel() != n or not t.is_contiguous():
-        raise TypeError(f"{name}: expected {n} contiguous float32 values, got {t.dtype} "
-                        f"{tuple(t.shape)}")
-    return t.data_ptr()
+def _native():
+    """The native marshalling of the functions below, with the library's entry points."""
+    global _native_module
+    if _native_module is None:
+        import ctypes
+        import importlib.machinery
+        import importlib.util
+        import os
+        if not os.path.exists(NATIVE):
+            raise RuntimeError(f"{NATIVE} is missing: build it with __graft_entry__.build()")
+        name = "_native"
+        loader = importlib.machinery.ExtensionFileLoader(name, NATIVE)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+        loader.exec_module(m)
+        m.init(*(ctypes.cast(getattr(_capi.lib(), f), ctypes.c_void_p).value for f in
+                 ("fp8q_rms_norm_quant", "fp8q_silu_mul_quant", "fp8q_int8_matmul")), _capi.check)
+        _native_module = m
+    return _native_module
 
 
 def rms_norm_quant(x, weight, *, residual=None, dtype=torch.int8, eps: float = EPS,
@@ -298,35 +245,12 @@ def rms_norm_quant(x, weight, *, residual=None, dtype=torch.int8, eps: float = E
     qt = _QTYPES.get(dtype)
     if qt is None:
         raise TypeError(f"dtype: expected torch.int8 or torch.float8_e4m3fn, got {dtype}")
-    dev = _check_device(x, "x", weight, residual, residual_out, q, scale)
-    if x.dtype is not _BF16 or not x.is_contiguous():
-        _bf16(x, "x")
-    if weight.dtype is not _BF16 or not weight.is_contiguous():
-        _bf16(weight, "weight")
-    shape = x.shape
-    cols = shape[-1]
-    rows = x.numel() // cols if cols else 0
-    if weight.numel() != cols:
-        raise TypeError(f"weight: expected {cols} values, got {tuple(weight.shape)}")
-    h = None
-    if residual is not None:
-        if _bf16(residual, "residual").shape != shape:
-            raise TypeError(f"residual: expected {tuple(shape)}, got {tuple(residual.shape)}")
-        h = (_new(shape, _BF16, x, stream) if residual_out is None
-             else _given(residual_out, shape, _BF16, "residual_out"))
-    elif residual_out is not None:
-        raise TypeError("residual_out: given without a residual")
-    q = _new(shape, dtype, x, stream) if q is None else _given(q, shape, dtype, "q")
-    scale = (_new(shape[:-1], _F32, x, stream) if scale is None
-             else _given(scale, shape[:-1], _F32, "scale"))
-    st = _function("fp8q_rms_norm_quant")(None if h is None else h.data_ptr(), q.data_ptr(),
-                                         scale.data_ptr(), x.data_ptr(),
-                                         None if h is None else residual.data_ptr(),
-                                         weight.data_ptr(), qt, rows, cols, eps,
-                                         _raw_stream(stream, dev))
-    if st:
-        _capi.check(st, "fp8q_rms_norm_quant")
-    return (q, scale) if h is None else (h, q, scale)
+    if stream is not None:
+        with torch.cuda.stream(stream):  # new outputs belong to the stream they are written on
+            return rms_norm_quant(x, weight, residual=residual, dtype=dtype, eps=eps,
+                                  residual_out=residual_out, q=q, scale=scale)
+    m = _native_module or _native()
+    return m.rms_norm_quant(x, weight, residual, qt, eps, residual_out, q, scale)
 
 
 def silu_mul_quant(gate, up, *, dtype=torch.int8, q=None, scale=None, stream=None):
@@ -335,21 +259,11 @@ def silu_mul_quant(gate, up, *, dtype=torch.int8, q=None, scale=None, stream=Non
     qt = _QTYPES.get(dtype)
     if qt is None:
         raise TypeError(f"dtype: expected torch.int8 or torch.float8_e4m3fn, got {dtype}")
-    dev = _check_device(gate, "gate", up, q, scale)
-    rows, cols, ld = _strided_rows(gate, _BF16, "gate")
-    shape = gate.shape
-    if up.shape != shape or _strided_rows(up, _BF16, "up")[2] != ld:
-        raise TypeError(f"gate {tuple(shape)} {gate.stride()} and up {tuple(up.shape)} "
-                        f"{up.stride()}: expected one shape and one row stride")
-    q = _new(shape, dtype, gate, stream) if q is None else _given(q, shape, dtype, "q")
-    scale = (_new(shape[:-1], _F32, gate, stream) if scale is None
-             else _given(scale, shape[:-1], _F32, "scale"))
-    st = _function("fp8q_silu_mul_quant")(q.data_ptr(), scale.data_ptr(), gate.data_ptr(),
-                                         up.data_ptr(), ld, qt, rows, cols,
-                                         _raw_stream(stream, dev))
-    if st:
-        _capi.check(st, "fp8q_silu_mul_quant")
-    return q, scale
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return silu_mul_quant(gate, up, dtype=dtype, q=q, scale=scale)
+    m = _native_module or _native()
+    return m.silu_mul_quant(gate, up, qt, q, scale)
 
 
 def int8_matmul(a, a_scale, w, w_scale, *, bias=None, out_dtype=torch.bfloat16, out=None,
@@ -360,24 +274,11 @@ def int8_matmul(a, a_scale, w, w_scale, *, bias=None, out_dtype=torch.bfloat16, 
     ot = _OUT_TYPES.get(out_dtype)
     if ot is None:
         raise TypeError(f"out_dtype: expected torch.bfloat16 or torch.float32, got {out_dtype}")
-    dev = _check_device(a, "a", a_scale, w, w_scale, bias, out)
-    m, k, lda = _strided_rows(a, _I8, "a")
-    wshape = w.shape
-    if w.dtype is not _I8 or len(wshape) != 2 or wshape[1] != k or not w.is_contiguous():
-        raise TypeError(f"w: expected a contiguous int8 [n, {k}], got {w.dtype} {tuple(wshape)}")
-    n = wshape[0]
-    if bias is not None and _bf16(bias, "bias").numel() != n:
-        raise TypeError(f"bias: expected {n} values, got {tuple(bias.shape)}")
-    shape = (*a.shape[:-1], n)
-    out = _new(shape, out_dtype, a, stream) if out is None else _given(out, shape, out_dtype, "out")
-    st = _function("fp8q_int8_matmul")(out.data_ptr(), a.data_ptr(), lda,
-                                      _row_scale(a_scale, m, "a_scale"), w.data_ptr(),
-                                      _row_scale(w_scale, n, "w_scale"),
-                                      None if bias is None else bias.data_ptr(), ot, m, n, k,
-                                      _raw_stream(stream, dev))
-    if st:
-        _capi.check(st, "fp8q_int8_matmul")
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return int8_matmul(a, a_scale, w, w_scale, bias=bias, out_dtype=out_dtype, out=out)
+    m = _native_module or _native()
+    return m.int8_matmul(a, a_scale, w, w_scale, bias, ot, out)
 
 
 def device_error() -> int:

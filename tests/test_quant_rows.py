@@ -650,7 +650,43 @@ def test_matmul_argument_checks(L):
         assert call(o=v) == ALIAS
 
 
+def test_binding_fails_loudly_without_the_native_module(monkeypatch, tmp_path):
+    monkeypatch.setattr(fq, "NATIVE", str(tmp_path / "missing.so"))
+    monkeypatch.setattr(fq, "_native_module", None)
+    with pytest.raises(RuntimeError, match="missing"):
+        fq.rms_norm_quant(None, None)
+
+
+def test_native_module_is_rebuilt_for_a_change(monkeypatch):
+    import os
+    from fp8_quant_row_gb300 import _build
+    _build.build()
+    assert _build.native_up_to_date()
+    built, real = os.path.getmtime(_build.NATIVE), os.path.getmtime
+    monkeypatch.setattr(os.path, "getmtime",
+                        lambda p: built + 1.0 if p == _build.NATIVE_SOURCE else real(p))
+    assert not _build.native_up_to_date()
+    monkeypatch.setattr(os.path, "getmtime", real)
+    monkeypatch.setattr(_build, "_native_stamp", lambda: "another torch")
+    assert not _build.native_up_to_date()
+
+
+def test_binding_refuses_what_is_no_tensor():
+    fq.build()
+    x = torch.zeros(4, 512, dtype=torch.bfloat16)
+    for bad in (None, 3, "x", [1.0]):
+        with pytest.raises(TypeError):
+            fq.rms_norm_quant(bad, x)
+        with pytest.raises(TypeError):
+            fq.silu_mul_quant(x, bad)
+        with pytest.raises(TypeError):
+            fq.int8_matmul(x, bad, x, x)
+    with pytest.raises(TypeError):
+        fq.rms_norm_quant(x, x, eps="small")
+
+
 def test_binding_refuses_cpu_tensors_and_types():
+    fq.build()
     x = torch.zeros(4, 512, dtype=torch.bfloat16)
     with pytest.raises(TypeError):
         fq.rms_norm_quant(x, x[0])
