@@ -84,7 +84,7 @@ def build_native(force: bool = False) -> str:
                     f"-I{sysconfig.get_paths()['include']}", f"-I{home}/include",
                     f"-I{home}/include/torch/csrc/api/include", f"-I{CUDA_HOME}/include",
                     NATIVE_SOURCE, "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
-                    "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"], check=True)
+                    "-ltorch_cuda", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"], check=True)
     os.replace(tmp, NATIVE)
     with open(NATIVE + ".stamp", "w") as f:
         f.write(_native_stamp())

@@ -11,7 +11,7 @@
 #include <optional>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -118,7 +118,7 @@ struct Out {
       data = given->data_ptr();
       return;
     }
-    at::Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    at::Tensor t = at::detail::empty_cuda(shape, type, dev, std::nullopt);
     data = t.data_ptr();
     object = THPVariable_Wrap(std::move(t));
     if (!object) throw Refused{};

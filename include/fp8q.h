@@ -284,7 +284,7 @@ fp8q_status fp8q_rms_norm_quant(void* residual_out, void* q, float* q_scale, con
 /*
  * Gated activation -> 8-bit rows with one scale each:
  *   s_j = RN_bf16(RN_fp32(silu(gate_j))), silu(g) = g / (1 + exp(-g)); 0 for
- *         finite g < -87, NaN for -infinity
+ *         (of either sign) for finite g < -87, NaN for -infinity
  *   p_j = s_j * up_j (exact in fp32), P, inv, q_j as above,  scale = P / QMAX
  * The gate's activation is rounded to bf16 (as where it is a tensor of its own), so that the
  * products are exact and the codes do not depend on how the exponential is computed.
