@@ -498,7 +498,7 @@ constexpr double kTcFixed = 4.0, kTcExchange = 0.8, kTcColumn = 0.02;  // sums' 
 
 template <int CG, int BT>
 constexpr double tc_stage_us() {
-  return CG == 2 ? (BT == 256 ? 0.637 : 0.395) : BT == 128 ? 0.44 : BT == 64 ? 0.38 : 0.35;
+  return CG == 2 ? (BT == 256 ? 0.617 : 0.395) : BT == 128 ? 0.44 : BT == 64 ? 0.38 : 0.35;
 }
 
 template <int CG, int BT>
