@@ -66,18 +66,24 @@ struct TcLayout {
   static constexpr int kRawA = 128 * kTcStep, kRawB = kRowsB * kTcStep, kRaw = kRawA + kRawB;
   static constexpr int kConvB = kRowsB * kTcStep * 2;
   static constexpr int kConvStages = BT == 256 ? 4 : 3;
-  static constexpr int kBarBytes = 256;
+  static constexpr int kBarBytes = 320;
   static constexpr int kScaleBytes = 2 * BT * 4;  // the token scales of two tiles in turn
   static constexpr int kRawStages0 =
       (kTcSmemLimit - kBarBytes - kScaleBytes - kConvStages * kConvB) / kRaw;
   static constexpr int kRawStages = kRawStages0 > 8 ? 8 : kRawStages0;
+  // "Copied in" barriers. The two groups of converting warps take stages in turn, and a wait tells
+  // phases apart by parity alone: over an odd ring a group would see only every second phase of a
+  // barrier, and pass on the one before when that copy is late. So their ring is even. (Converted
+  // stages are freed in order: who waits for one has seen the one two before it freed, so no
+  // phase of a ring of three or four goes unseen.)
+  static constexpr int kFullBars = kRawStages % 2 ? 2 * kRawStages : kRawStages;
   static constexpr int kBytes = kRawStages * kRaw + kConvStages * kConvB + kBarBytes + kScaleBytes;
   static constexpr int kColsA = BT;  // first column of the converted weights
   static constexpr int kCols = kColsA + kConvStages * 64 <= 256 ? 256 : 512;
   // partial sums, sent and got, over the stages (free by then)
   static_assert(CG == 2 || (2 * BT + 8) * 512 <= kRawStages * kRaw + kConvStages * kConvB, "");
   static_assert(kBytes <= kTcSmemLimit && kRawStages >= 2 && kColsA + kConvStages * 64 <= 512, "");
-  static_assert(8 * (2 * kRawStages + 2 * kConvStages + 9) <= kBarBytes, "");
+  static_assert(8 * (kFullBars + kRawStages + 2 * kConvStages + 9) <= kBarBytes, "");
 };
 
 // ---- instructions -------------------------------------------------------------------------
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint8_t* conv = smem + L::kRawStages * L::kRaw;
   uint64_t* bars = reinterpret_cast<uint64_t*>(conv + L::kConvStages * L::kConvB);
   uint64_t* raw_full = bars;
-  uint64_t* raw_empty = raw_full + L::kRawStages;
+  uint64_t* raw_empty = raw_full + L::kFullBars;
   uint64_t* conv_full = raw_empty + L::kRawStages;   // first CTA's counts for the pair
   uint64_t* conv_empty = conv_full + L::kConvStages;
   uint64_t* d_full = conv_empty + L::kConvStages;    // one for each half
@@ -300,10 +306,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kRawStages; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 8);
-    }
+    for (int i = 0; i < L::kFullBars; ++i) mbar_init(&raw_full[i], 1);
+    for (int i = 0; i < L::kRawStages; ++i) mbar_init(&raw_empty[i], 8);
     for (int i = 0; i < L::kConvStages; ++i) {
       mbar_init(&conv_full[i], 8 * CG);
       mbar_init(&conv_empty[i], 1);
@@ -341,14 +345,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ok = tc_wait(&raw_empty[st], (use & 1) ^ 1);
           if (!ok) break;
           uint8_t* dst = raw + st * L::kRaw;
-          mbar_arrive_expect_tx(&raw_full[st], L::kRaw);
-          tma_load_2d(dst, &map_w, (s0 + s) * kTcStep, yw, &raw_full[st]);
-          tma_load_2d(dst + L::kRawA, &map_a, (s0 + s) * kTcStep, ya, &raw_full[st]);
+          uint64_t* full = &raw_full[it % L::kFullBars];
+          mbar_arrive_expect_tx(full, L::kRaw);
+          tma_load_2d(dst, &map_w, (s0 + s) * kTcStep, yw, full);
+          tma_load_2d(dst + L::kRawA, &map_a, (s0 + s) * kTcStep, ya, full);
         }
       }
       // copies still in flight land before the CTA ends
       for (uint32_t i = it > L::kRawStages ? it - L::kRawStages : 0; i < it; ++i)
-        tc_wait(&raw_full[i % L::kRawStages], (i / L::kRawStages) & 1);
+        tc_wait(&raw_full[i % L::kFullBars], (i / L::kFullBars) & 1);
     } else if (warp == 1 && half == 0) {
       // The whole warp goes through the loop and one lane issues: values that the warp shares
       // stay in uniform registers, where the instructions want them.
@@ -429,12 +434,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int row = weights ? tid : tid % L::kRowsB;
     const int part = weights ? 0 : tid / L::kRowsB * kParts;  // its first chunk
     const uint32_t chunks = weights ? 8 : kParts;
-    // its next stage of either ring and the phases that it waits for
-    uint32_t rs = turn, cs = turn, raw_phase = 0, conv_phase = 1;
+    // its next stage of either ring, its next "copied in" barrier, and the phases that it waits for
+    uint32_t rs = turn, cs = turn, full = turn, raw_phase = 0, conv_phase = 1;
     int s = int(turn);
     for (int64_t t = first; t < p.tiles && ok; t += stride) {
       for (; s < steps; s += 2) {
-        ok = tc_wait_warp(&raw_full[rs], raw_phase);
+        ok = tc_wait_warp(&raw_full[full], raw_phase);
         if (!ok) break;
         const uint8_t* src = raw + rs * L::kRaw + (weights ? 0 : L::kRawA) + row * 128;
         uint8_t* dst = conv + cs * L::kConvB + row * 128;
@@ -497,7 +502,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           else mbar_arrive(&conv_full[cs]);
         }
         rs += 2;
-        if (rs >= L::kRawStages) rs -= L::kRawStages, raw_phase ^= 1;
+        if (rs >= L::kRawStages) rs -= L::kRawStages;
+        full += 2;
+        if (full >= L::kFullBars) full -= L::kFullBars, raw_phase ^= 1;
         cs += 2;
         if (cs >= L::kConvStages) cs -= L::kConvStages, conv_phase ^= 1;
       }
