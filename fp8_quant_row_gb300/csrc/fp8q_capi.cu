@@ -498,7 +498,7 @@ constexpr double kTcFixed = 4.0, kTcExchange = 0.8, kTcColumn = 0.02;  // sums' 
 
 template <int CG, int BT>
 constexpr double tc_stage_us() {
-  return CG == 2 ? (BT == 256 ? 0.617 : 0.395) : BT == 128 ? 0.44 : BT == 64 ? 0.38 : 0.35;
+  return CG == 2 ? (BT == 256 ? 0.617 : 0.375) : BT == 128 ? 0.44 : BT == 64 ? 0.37 : 0.35;
 }
 
 template <int CG, int BT>
@@ -598,16 +598,17 @@ void consider_tc(const fp8q::MmParams& mm, const DeviceInfo& dev, const int* fit
 // The kernel with the least estimated time. Measured (us; 8 and 16: the kernel for few tokens,
 // CGxBT: the tensor-memory kernel), at 6144 x 6144 weights:
 //   tokens      8     16   1x32   1x64  1x128  2x128  2x256
-//        8    9.7   12.0   12.9   13.7   16.9   22.3   34.5
-//       16          12.3   12.9   13.6   17.8   22.3   34.6
-//       32                 13.3   13.9   16.1   22.4   34.6
-//       64                 18.7   14.4   16.8   22.5   34.8
-//      128                 34.1   20.6   18.2   22.6   34.9
-//      256                 49.6   37.2   25.1   23.2   35.1
-//     1024                171.3  103.6   67.6   60.2   65.1
-//     4608                706.6  389.6  258.1  230.0  191.0
+//        8    9.5   11.9   12.9   13.8   17.4   21.8   33.2
+//       16          12.1   13.0   14.0   17.4   21.9   33.2
+//       32                 13.3   14.2   16.2   21.9   33.5
+//       64                 18.8   14.8   17.1   22.2   33.7
+//      128                 34.4   21.6   18.3   22.1   34.0
+//      256                 49.6   39.0   25.6   22.8   34.1
+//      450                 80.4   56.6   46.9   40.7   35.1
+//     1024                171.9  108.3   67.8   58.3   63.2
+//     4608                709.5  407.2  258.7  221.4  183.4
 // at 36864 x 6144, 8 tokens: 42.2 / 55.2 / 39.5 / 45.6 / 65.1 / 42.7 / 64.5, 128 tokens: 1x128 51.0,
-// 2x128 46.2, 2x256 67.1; at 2048 x 2048, 8 tokens: 3.6 / 4.4 / 6.1, 200 tokens: 1x64 8.9, 2x128 10.6.
+// 2x128 44.5, 2x256 66.0; at 2048 x 2048, 8 tokens: 3.6 / 4.4 / 6.1, 200 tokens: 1x64 8.9, 2x128 10.6.
 template <bool F32>
 fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
                                cudaStream_t stream) {
@@ -615,14 +616,14 @@ fp8q_status launch_int8_matmul(const fp8q::MmParams& p, const DeviceInfo& dev,
   int which = 0;
   // bytes at the rate that many channel groups reach, and how unevenly few groups fall on the SMs
   const int64_t groups = (p.n + 15) / 16, per_sm = (groups + dev.sms - 1) / dev.sms;
-  const double uneven = per_sm <= 3 ? double(per_sm * dev.sms) / double(groups) : 1.0;
+  const double uneven = per_sm <= 2 ? double(per_sm * dev.sms) / double(groups) : 1.0;
   const double weights = double(p.n) * double(p.k) * std::min(uneven, 2.0);
   if (p.m <= 8) best = 3.0 + weights / 5.9e6, which = 8;
   else if (p.m <= 16) best = 3.0 + weights / 4.2e6, which = 16;
   const int* fit = nullptr;
   const fp8q_status st = cluster_fit(&fit);
   if (st != FP8Q_OK) return st;
-  if (p.m <= 128) consider_tc<1, 32>(p, dev, fit, &best, &which);
+  if (p.m <= 512) consider_tc<1, 32>(p, dev, fit, &best, &which);
   if (p.m > 32 && p.m <= 512) consider_tc<1, 64>(p, dev, fit, &best, &which);
   if (p.m > 64 && p.m <= 1024) consider_tc<1, 128>(p, dev, fit, &best, &which);
   if (p.m > 64) consider_tc<2, 128>(p, dev, fit, &best, &which);
