@@ -544,6 +544,30 @@ def test_two_streams_at_once():
 
 
 @gpu
+@pytest.mark.parametrize("m", [8, 24, 64, 128, 300, 2000])
+def test_int8_matmul_beside_copies(m):
+    """Its tiles come late and out of order while another stream copies. Sums of small integers are
+    exact, so every run gives the same values."""
+    n, k = 6144, 6144
+    a, w = int8((m, k), 1, -4, 5), int8((n, k), 2, -4, 5)
+    sa, sw = torch.ones(m, device="cuda"), torch.ones(n, device="cuda")
+    want = (a.double() @ w.double().t()).float()
+    src = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    dst, side = torch.empty_like(src), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(12):
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                dst.copy_(src)
+        for _ in range(4):
+            outs.append(fq.int8_matmul(a, sa, w, sw, out_dtype=torch.float32))
+    torch.cuda.synchronize()
+    assert fq.device_error() == 0
+    assert all(torch.equal(out, want) for out in outs)
+
+
+@gpu
 def test_empty_calls():
     x = torch.empty(0, 512, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(512, dtype=torch.bfloat16, device="cuda")
