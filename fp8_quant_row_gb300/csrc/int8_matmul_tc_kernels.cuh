@@ -649,6 +649,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       scales = parity ? scales - BT : scales + BT;
       parity = !parity;
     }
+    if (warp == kTcFirstDrain) {
+      // The commits' arrivals, which the first CTA of a pair sends to both, land in either before
+      // its shared memory goes to another CTA: the last of each converted stage, and `idle` (those
+      // on d_full the draining warps have seen). Here, since only after the last drain are they
+      // at most a few stages away, whatever the product's length: the waits are bounded.
+      bool landed = tc_wait_warp(idle, 0) && ok;
+      const uint32_t uses = uint32_t((p.tiles - first + stride - 1) / stride) * uint32_t(steps);
+      for (uint32_t i = uses > L::kConvStages ? uses - L::kConvStages : 0; i < uses && landed; ++i)
+        landed = tc_wait_warp(&conv_empty[i % L::kConvStages], (i / L::kConvStages) & 1);
+    }
   }
   __syncwarp();
   tc_fence_before();

@@ -568,6 +568,26 @@ def test_int8_matmul_beside_copies(m):
 
 
 @gpu
+@pytest.mark.parametrize("m", [1025, 1200, 2049])
+@pytest.mark.parametrize("n,k", [(200, 16), (256, 128), (300, 400), (700, 640), (513, 1040)])
+def test_int8_matmul_short_pairs_back_to_back(m, n, k):
+    """Products of a few stages on pairs of CTAs, each followed at once by the next and by one on
+    single CTAs: the last arrivals of one lie close to the first barriers of the next, whose shared
+    memory is the same. Sums of small integers are exact."""
+    a, w = int8((m, k), 1, -4, 5), int8((n, k), 2, -4, 5)
+    one = torch.ones(max(m, n), device="cuda")
+    want = (a.double() @ w.double().t()).float()
+    outs = []
+    torch.cuda.synchronize()
+    for _ in range(40):
+        outs.append(fq.int8_matmul(a, one[:m], w, one[:n], out_dtype=torch.float32))
+        outs.append(fq.int8_matmul(a[:40], one[:40], w, one[:n], out_dtype=torch.float32))
+    torch.cuda.synchronize()
+    assert fq.device_error() == 0
+    assert all(torch.equal(out, want[:len(out)]) for out in outs)
+
+
+@gpu
 def test_empty_calls():
     x = torch.empty(0, 512, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(512, dtype=torch.bfloat16, device="cuda")
