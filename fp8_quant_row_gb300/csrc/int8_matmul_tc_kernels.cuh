@@ -461,6 +461,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&raw_empty[rs]);
           }
+          __syncwarp();  // the stores to tensor memory below are warp-wide
           if (weights) {
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
@@ -554,6 +555,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (CG == 1 && ctas > 1 && warp == kTcFirstDrain && s + kTcChunk / kTcStep >= steps &&
             lane < ctas && lane != int(rank))
           mbar_arrive_cluster(map_rank(smem_addr(peers_ready), lane));
+        __syncwarp();  // the loads from tensor memory below are warp-wide
         if (s == 0) {
           // The four warps of a side store the same values. Their buffer is free: this tile's
           // first products were issued after every warp had drained the tile before, which is

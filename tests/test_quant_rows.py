@@ -588,6 +588,20 @@ def test_int8_matmul_short_pairs_back_to_back(m, n, k):
 
 
 @gpu
+@pytest.mark.parametrize("m,n", [(24, 640), (64, 640), (128, 640), (1030, 300), (2050, 1000)])
+@pytest.mark.parametrize("k", [1024, 1152, 4112, 18432])
+def test_int8_matmul_many_drains(m, n, k):
+    """Several drains of a tile, one of them of a single stage, in every tile shape. Sums of small
+    integers are exact."""
+    a, w = int8((m, k), 1, -4, 5), int8((n, k), 2, -4, 5)
+    one = torch.ones(max(m, n), device="cuda")
+    want = (a.double() @ w.double().t()).float()
+    outs = [fq.int8_matmul(a, one[:m], w, one[:n], out_dtype=torch.float32) for _ in range(10)]
+    assert fq.device_error() == 0
+    assert all(torch.equal(out, want) for out in outs)
+
+
+@gpu
 def test_empty_calls():
     x = torch.empty(0, 512, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(512, dtype=torch.bfloat16, device="cuda")
