@@ -73,9 +73,10 @@ fp8q_status current_device(const DeviceInfo** out) {
   return FP8Q_OK;
 }
 
-// Resident CTAs per SM of a kernel at a dynamic shared-memory size, cached per device.
+// Resident CTAs per SM of a kernel at a block size and a dynamic shared-memory size, cached per
+// device. (The row kernels are launched with several block sizes.)
 struct OccEntry {
-  int dev;
+  int dev, threads;
   const void* fn;
   size_t smem;
   int blocks;
@@ -120,14 +121,15 @@ fp8q_status blocks_per_sm(const void* fn, int threads, size_t smem, int* blocks)
     if (st != FP8Q_OK) return st;
   }
   for (int i = 0; i < g_occ_n; ++i)
-    if (g_occ[i].dev == dev && g_occ[i].fn == fn && g_occ[i].smem == smem) {
+    if (g_occ[i].dev == dev && g_occ[i].fn == fn && g_occ[i].threads == threads &&
+        g_occ[i].smem == smem) {
       *blocks = g_occ[i].blocks;
       return FP8Q_OK;
     }
   int b = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, fn, threads, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor", (long long)smem);
-  if (g_occ_n < 256) g_occ[g_occ_n++] = OccEntry{dev, fn, smem, b};
+  if (g_occ_n < 256) g_occ[g_occ_n++] = OccEntry{dev, threads, fn, smem, b};
   *blocks = b;
   return FP8Q_OK;
 }
