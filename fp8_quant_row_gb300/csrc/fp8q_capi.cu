@@ -74,15 +74,29 @@ fp8q_status current_device(const DeviceInfo** out) {
 }
 
 // Resident CTAs per SM of a kernel at a block size and a dynamic shared-memory size, cached per
-// device. (The row kernels are launched with several block sizes.)
+// device. (The row kernels are launched with several block sizes, and wide rows with a
+// shared-memory size for each width: a table of 512 sets of eight, in which the next entry of a full
+// set is replaced, so that what a process calls stays known however many widths it has seen.)
 struct OccEntry {
   int dev, threads;
   const void* fn;
   size_t smem;
   int blocks;
 };
-OccEntry g_occ[256];
-int g_occ_n = 0;
+constexpr int kOccSets = 512, kOccWays = 8;
+struct OccSet {
+  OccEntry entry[kOccWays];  // fn null where free
+  int next;
+};
+OccSet g_occ[kOccSets];
+
+OccSet& occ_set(int dev, const void* fn, int threads, size_t smem) {
+  uint64_t h = uint64_t(reinterpret_cast<uintptr_t>(fn));
+  for (uint64_t v : {uint64_t(smem), uint64_t(threads), uint64_t(dev)})
+    h = (h ^ (h >> 29) ^ v) * 0x9E3779B97F4A7C15u;  // odd, 2^64 / golden ratio
+  return g_occ[(h >> 40) % kOccSets];
+}
+
 // Dynamic shared-memory limit set on each (device, function): the limit is a property of the
 // function, not of a launch, so it only ever grows to the largest size launched (a launch
 // above the current limit is rejected; a smaller size seen later must not lower it).
@@ -120,16 +134,17 @@ fp8q_status blocks_per_sm(const void* fn, int threads, size_t smem, int* blocks)
     const fp8q_status st = raise_smem_limit(dev, fn, smem);
     if (st != FP8Q_OK) return st;
   }
-  for (int i = 0; i < g_occ_n; ++i)
-    if (g_occ[i].dev == dev && g_occ[i].fn == fn && g_occ[i].threads == threads &&
-        g_occ[i].smem == smem) {
-      *blocks = g_occ[i].blocks;
+  OccSet& set = occ_set(dev, fn, threads, smem);
+  for (const OccEntry& o : set.entry)
+    if (o.fn == fn && o.dev == dev && o.threads == threads && o.smem == smem) {
+      *blocks = o.blocks;
       return FP8Q_OK;
     }
   int b = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, fn, threads, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor", (long long)smem);
-  if (g_occ_n < 256) g_occ[g_occ_n++] = OccEntry{dev, threads, fn, smem, b};
+  set.entry[set.next] = OccEntry{dev, threads, fn, smem, b};
+  set.next = (set.next + 1) % kOccWays;
   *blocks = b;
   return FP8Q_OK;
 }

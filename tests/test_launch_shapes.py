@@ -73,3 +73,25 @@ def test_a_grid_does_not_depend_on_earlier_widths(fake, op):
         rows_cta = 4 if block == 128 and int(cols) <= (1024 if op == "rms" else 768) else 1
         resident = min(2048 // block, 65536 // (128 * block), 32)
         assert grid == min(-(-4608 // rows_cta), 152 * resident), (cols, grid, block)
+
+
+def test_launch_cache_holds_many_widths(fake):
+    """Wide rows have an entry for each width. However many a process has seen, calls that it has
+    made before ask the runtime nothing."""
+    got = fake("""
+    widths = [8200 + 8 * i for i in range(600)]
+    def calls():
+        for cols in widths:
+            assert rms(400, cols) == 0 and silu(400, cols + 8192) == 0
+        before = F.fake_queries()
+        for _ in range(50):
+            assert rms(4608, 2048) == 0 and silu(4608, 12288) == 0
+        return before
+    calls()
+    first = F.fake_queries()
+    again = calls()
+    print(json.dumps([first, again - first, F.fake_queries() - again]))
+    """)
+    assert 1200 <= got[0] <= 1210
+    assert got[1] <= 12  # (of 1200: the table is a hash of the kernels' addresses)
+    assert got[2] == 0
