@@ -75,15 +75,16 @@ fp8q_status current_device(const DeviceInfo** out) {
 
 // Resident CTAs per SM of a kernel at a block size and a dynamic shared-memory size, cached per
 // device. (The row kernels are launched with several block sizes, and wide rows with a
-// shared-memory size for each width: a table of 512 sets of eight, in which the next entry of a full
-// set is replaced, so that what a process calls stays known however many widths it has seen.)
+// shared-memory size for each width: a table of 2048 sets of eight, in which the next entry of a
+// full set is replaced, so that what a process calls stays known however many widths it has seen.
+// With 1200 entries spread evenly, some set has nine with a probability of 3e-5.)
 struct OccEntry {
   int dev, threads;
   const void* fn;
   size_t smem;
   int blocks;
 };
-constexpr int kOccSets = 512, kOccWays = 8;
+constexpr int kOccSets = 2048, kOccWays = 8;
 struct OccSet {
   OccEntry entry[kOccWays];  // fn null where free
   int next;
