@@ -102,26 +102,28 @@ OccSet& occ_set(int dev, const void* fn, int threads, size_t smem) {
 // function, not of a launch, so it only ever grows to the largest size launched (a launch
 // above the current limit is rejected; a smaller size seen later must not lower it).
 struct SmemLimit {
-  int dev;
   const void* fn;
   size_t limit;
 };
-SmemLimit g_lim[256];
-int g_lim_n = 0;
+constexpr int kMaxLimits = 256;  // more than the library has kernels
+struct SmemLimits {
+  SmemLimit entry[kMaxLimits];
+  int n;
+};
+SmemLimits g_lim[kMaxDevices];
 std::mutex g_occ_mu;
 
 fp8q_status raise_smem_limit(int dev, const void* fn, size_t smem) {
+  SmemLimits& lim = g_lim[dev];
   SmemLimit* entry = nullptr;
-  for (int i = 0; i < g_lim_n; ++i)
-    if (g_lim[i].dev == dev && g_lim[i].fn == fn) entry = &g_lim[i];
+  for (int i = 0; i < lim.n; ++i)
+    if (lim.entry[i].fn == fn) entry = &lim.entry[i];
   if (entry && entry->limit >= smem) return FP8Q_OK;
+  if (!entry && lim.n == kMaxLimits) return FP8Q_ERR_UNSUPPORTED;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)", (long long)smem);
-  if (entry) {
-    entry->limit = smem;
-  } else if (g_lim_n < 256) {
-    g_lim[g_lim_n++] = SmemLimit{dev, fn, smem};
-  }
+  if (!entry) entry = &lim.entry[lim.n++];
+  *entry = SmemLimit{fn, smem};
   return FP8Q_OK;
 }
 
@@ -129,6 +131,7 @@ fp8q_status blocks_per_sm(const void* fn, int threads, size_t smem, int* blocks)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev < 0 || dev >= kMaxDevices) return FP8Q_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lock(g_occ_mu);
   // Checked on every call: the cached occupancy below says nothing about the current limit.
   if (smem > 48 * 1024) {

@@ -11,7 +11,7 @@ struct fake_launch {
 
 #define LAUNCHES 65536
 static struct fake_launch launches[LAUNCHES];
-static int n_launches, n_queries, n_refused, device;
+static int n_launches, n_queries, n_refused, n_falls, device;
 
 /* dynamic shared-memory limits of (device, function) pairs, as the runtime keeps them */
 static struct { int dev; const void *fn; int limit; } limits[65536];
@@ -29,6 +29,7 @@ static int *limit_of(const void *fn) {
 int fake_launches(void) { return n_launches; }
 int fake_queries(void) { return n_queries; }
 int fake_refused(void) { return n_refused; }
+int fake_limit_falls(void) { return n_falls; }
 void fake_device(int d) { device = d; }
 struct fake_launch fake_launch_at(int i) { return launches[i]; }
 
@@ -53,7 +54,10 @@ cudaError_t cudaDeviceGetAttribute(int *v, enum cudaDeviceAttr a, int d) {
   return cudaSuccess;
 }
 cudaError_t cudaFuncSetAttribute(const void *fn, enum cudaFuncAttribute a, int v) {
-  if (a == cudaFuncAttributeMaxDynamicSharedMemorySize) *limit_of(fn) = v;
+  if (a == cudaFuncAttributeMaxDynamicSharedMemorySize) {
+    if (v < *limit_of(fn)) ++n_falls;
+    *limit_of(fn) = v;
+  }
   return cudaSuccess;
 }
 cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessor(int *n, const void *fn, int threads,

@@ -93,3 +93,22 @@ def test_launch_cache_holds_many_widths(fake):
     print(json.dumps([first, again - first, F.fake_queries() - again]))
     """)
     assert got == [1202, 0, 0]
+
+
+def test_shared_memory_limits_of_many_devices(fake):
+    """A function's limit only ever grows, on each of the 64 devices that the library knows: a small
+    launch after a large one must not lower it, since another thread may be launching the large one."""
+    got = fake("""
+    F.fake_limit_falls.restype = ctypes.c_int
+    wide = [12296, 24584, 16392]
+    for sweep in (wide, wide[::-1]):
+        for dev in range(64):
+            F.fake_device(dev)
+            for cols in sweep:
+                for e4m3 in (0, 1):
+                    for residual in (False, True):
+                        assert rms(400, cols, residual, e4m3) == 0
+                    assert silu(400, cols, e4m3) == 0
+    print(json.dumps([F.fake_refused(), F.fake_limit_falls()]))
+    """)
+    assert got == [0, 0]
