@@ -103,34 +103,62 @@ Rows strided_rows(const at::Tensor& t, at::ScalarType type, const char* name) {
   return r;
 }
 
-// An output: the given tensor, checked, or a new one. Returns the Python object (a new reference).
-struct Out {
-  PyObject* object = nullptr;
-  void* data = nullptr;
+// An output: the given tensor, checked, or a new one, made by data().
+class Out {
+ public:
   Out(const at::Tensor* given, PyObject* given_object, at::IntArrayRef shape, at::ScalarType type,
-      at::Device dev, const char* name) {
-    if (given) {
-      if (given->scalar_type() != type || given->sizes() != shape || !given->is_contiguous())
-        refuse("%s: expected a contiguous %s tensor of the result's shape", name,
-               c10::toString(type));
-      Py_INCREF(given_object);
-      object = given_object;
-      data = given->data_ptr();
-      return;
+      const char* name)
+      : given_(given), given_object_(given_object), shape_(shape.begin(), shape.end()), type_(type) {
+    if (given && (given->scalar_type() != type || given->sizes() != shape || !given->is_contiguous()))
+      refuse("%s: expected a contiguous %s tensor of the result's shape", name,
+             c10::toString(type));
+  }
+  void* data(at::Device dev) {
+    if (given_) return given_->data_ptr();
+    made_ = at::detail::empty_cuda(shape_, type_, dev, std::nullopt);
+    return made_.data_ptr();
+  }
+  // The Python object, a new reference.
+  PyObject* object() {
+    if (!given_) {
+      PyObject* o = THPVariable_Wrap(std::move(made_));
+      if (!o) throw Refused{};
+      return o;
     }
-    at::Tensor t = at::detail::empty_cuda(shape, type, dev, std::nullopt);
-    data = t.data_ptr();
-    object = THPVariable_Wrap(std::move(t));
-    if (!object) throw Refused{};
+    Py_INCREF(given_object_);
+    return given_object_;
   }
-  Out(const Out&) = delete;
-  ~Out() { Py_XDECREF(object); }
-  PyObject* release() {
-    PyObject* o = object;
-    object = nullptr;
-    return o;
-  }
+
+ private:
+  const at::Tensor* given_;
+  PyObject* given_object_;
+  at::Tensor made_;
+  c10::SmallVector<int64_t, 5> shape_;
+  at::ScalarType type_;
 };
+
+// Other Python threads run during an allocation, which may wait for the device, and a launch, which
+// waits while the stream's queue is full. (No Python object is touched meanwhile.)
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// A tuple of the outputs.
+PyObject* results(std::initializer_list<Out*> outs) {
+  PyObject* tuple = PyTuple_New(Py_ssize_t(outs.size()));
+  if (!tuple) throw Refused{};
+  Py_ssize_t i = 0;
+  try {
+    for (Out* o : outs) PyTuple_SET_ITEM(tuple, i++, o->object());
+  } catch (...) {
+    Py_DECREF(tuple);
+    throw;
+  }
+  return tuple;
+}
 
 at::ScalarType row_type(long code) { return code == 0 ? at::kChar : at::kFloat8_e4m3fn; }
 
@@ -173,23 +201,23 @@ PyObject* rms_norm_quant(PyObject* const* arg, Py_ssize_t n) {
   if (residual) {
     contiguous(*residual, at::kBFloat16, "residual");
     if (residual->sizes() != shape) refuse("residual: expected x's shape");
-    h.emplace(residual_out, arg[5], shape, at::kBFloat16, dev, "residual_out");
+    h.emplace(residual_out, arg[5], shape, at::kBFloat16, "residual_out");
   } else if (residual_out) {
     refuse("residual_out: given without a residual");
   }
-  Out qo(q, arg[6], shape, row_type(type), dev, "q");
-  Out so(scale, arg[7], shape.slice(0, shape.size() - 1), at::kFloat, dev, "scale");
-  check(g_rms(h ? h->data : nullptr, qo.data, static_cast<float*>(so.data), x.data_ptr(),
-              residual ? residual->data_ptr() : nullptr, weight.data_ptr(), int(type), rows, cols,
-              float(eps), c10::cuda::getCurrentCUDAStream(dev.index()).stream()),
-        "fp8q_rms_norm_quant");
-  PyObject* result = PyTuple_New(h ? 3 : 2);
-  if (!result) throw Refused{};
-  Py_ssize_t i = 0;
-  if (h) PyTuple_SET_ITEM(result, i++, h->release());
-  PyTuple_SET_ITEM(result, i++, qo.release());
-  PyTuple_SET_ITEM(result, i, so.release());
-  return result;
+  Out qo(q, arg[6], shape, row_type(type), "q");
+  Out so(scale, arg[7], shape.slice(0, shape.size() - 1), at::kFloat, "scale");
+  int status = 0;
+  {
+    Unlocked unlocked;
+    void* hp = h ? h->data(dev) : nullptr;
+    void* qp = qo.data(dev);
+    status = g_rms(hp, qp, static_cast<float*>(so.data(dev)), x.data_ptr(),
+                   residual ? residual->data_ptr() : nullptr, weight.data_ptr(), int(type), rows,
+                   cols, float(eps), c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+  }
+  check(status, "fp8q_rms_norm_quant");
+  return h ? results({&*h, &qo, &so}) : results({&qo, &so});
 }
 
 // silu_mul_quant(gate, up, q_type, q, scale)
@@ -207,17 +235,18 @@ PyObject* silu_mul_quant(PyObject* const* arg, Py_ssize_t n) {
   const at::IntArrayRef shape = gate.sizes();
   if (up.sizes() != shape || (g.rows > 1 && u.ld != g.ld))
     refuse("gate and up: expected one shape and one row stride");
-  Out qo(q, arg[3], shape, row_type(type), dev, "q");
-  Out so(scale, arg[4], shape.slice(0, shape.size() - 1), at::kFloat, dev, "scale");
-  check(g_silu(qo.data, static_cast<float*>(so.data), gate.data_ptr(), up.data_ptr(),
-               g.rows > 1 ? g.ld : g.cols, int(type), g.rows, g.cols,
-               c10::cuda::getCurrentCUDAStream(dev.index()).stream()),
-        "fp8q_silu_mul_quant");
-  PyObject* result = PyTuple_New(2);
-  if (!result) throw Refused{};
-  PyTuple_SET_ITEM(result, 0, qo.release());
-  PyTuple_SET_ITEM(result, 1, so.release());
-  return result;
+  Out qo(q, arg[3], shape, row_type(type), "q");
+  Out so(scale, arg[4], shape.slice(0, shape.size() - 1), at::kFloat, "scale");
+  int status = 0;
+  {
+    Unlocked unlocked;
+    void* qp = qo.data(dev);
+    status = g_silu(qp, static_cast<float*>(so.data(dev)), gate.data_ptr(), up.data_ptr(),
+                    g.rows > 1 ? g.ld : g.cols, int(type), g.rows, g.cols,
+                    c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+  }
+  check(status, "fp8q_silu_mul_quant");
+  return results({&qo, &so});
 }
 
 // int8_matmul(a, a_scale, w, w_scale, bias, out_type, out)
@@ -245,13 +274,17 @@ PyObject* int8_matmul(PyObject* const* arg, Py_ssize_t n) {
   }
   c10::SmallVector<int64_t, 8> shape(a.sizes().begin(), a.sizes().end());
   shape.back() = channels;
-  Out o(out, arg[6], shape, type == 0 ? at::kBFloat16 : at::kFloat, dev, "out");
-  check(g_matmul(o.data, static_cast<const int8_t*>(a.data_ptr()), r.rows > 1 ? r.ld : r.cols, as,
-                 static_cast<const int8_t*>(w.data_ptr()), ws, bias ? bias->data_ptr() : nullptr,
-                 int(type), r.rows, channels, r.cols,
-                 c10::cuda::getCurrentCUDAStream(dev.index()).stream()),
-        "fp8q_int8_matmul");
-  return o.release();
+  Out o(out, arg[6], shape, type == 0 ? at::kBFloat16 : at::kFloat, "out");
+  int status = 0;
+  {
+    Unlocked unlocked;
+    status = g_matmul(o.data(dev), static_cast<const int8_t*>(a.data_ptr()),
+                      r.rows > 1 ? r.ld : r.cols, as, static_cast<const int8_t*>(w.data_ptr()), ws,
+                      bias ? bias->data_ptr() : nullptr, int(type), r.rows, channels, r.cols,
+                      c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+  }
+  check(status, "fp8q_int8_matmul");
+  return o.object();
 }
 
 // init(rms, silu, matmul, check): the C entry points' addresses and the error raiser

@@ -602,6 +602,47 @@ def test_int8_matmul_many_drains(m, n, k):
 
 
 @gpu
+def test_other_threads_run_during_a_call(tmp_path):
+    """A launch waits on the host while the stream's queue is full, an allocation for the device:
+    other Python threads go on. Stood in for by entry points that sleep and launch nothing."""
+    import ctypes
+    import subprocess
+    import threading
+    import time
+    src, so = tmp_path / "slow.c", str(tmp_path / "slow.so")
+    src.write_text("#include <unistd.h>\nint slow(void) { return usleep(300000); }\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", so], check=True)
+    slow = ctypes.cast(ctypes.CDLL(so).slow, ctypes.c_void_p).value
+    native, lib = fq._native(), fq._capi.lib()
+    real = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
+            ("fp8q_rms_norm_quant", "fp8q_silu_mul_quant", "fp8q_int8_matmul")]
+    x, w = normal((4, 512), 1), torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    q, s4, s1 = int8((4, 512), 2), f32(4, 3), f32(4, 4)
+    turns, done = [0], threading.Event()
+
+    def other():
+        while not done.wait(0.002):
+            turns[0] += 1
+
+    native.init(slow, slow, slow, fq._capi.check)
+    thread = threading.Thread(target=other)
+    try:
+        thread.start()
+        for call in (lambda: fq.rms_norm_quant(x, w), lambda: fq.silu_mul_quant(x, x),
+                     lambda: fq.int8_matmul(q, s4, q, s1)):
+            before, t0 = turns[0], time.monotonic()
+            call()
+            after = turns[0]
+            assert time.monotonic() - t0 >= 0.29
+            assert after - before >= 10  # of about 140
+    finally:
+        done.set()
+        thread.join()
+        native.init(*real, fq._capi.check)
+    assert fq.rms_norm_quant(x, w)[0].abs().max() == 127
+
+
+@gpu
 def test_empty_calls():
     x = torch.empty(0, 512, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(512, dtype=torch.bfloat16, device="cuda")
