@@ -165,6 +165,73 @@ def test_rms_norm_quant_in_place_and_guards():
     assert gh.intact() and gq.intact() and gs.intact()
 
 
+def scatter(x, kinds):
+    """Puts each kind of row at several places among normal ones: the first and last rows, and
+    rows far apart, so that the same threads go from a special row to a normal one and back. kinds:
+    functions that change a row in place. Returns the kind of each row, -1 for normal ones."""
+    rows, kind = x.shape[0], torch.full((x.shape[0],), -1, device="cuda")
+    g = torch.Generator().manual_seed(rows)
+    places = torch.randperm(rows, generator=g)[:8 * len(kinds)].tolist()
+    for i, r in enumerate(places + [0, rows - 1]):
+        kinds[i % len(kinds)](x[r])
+        kind[r] = i % len(kinds)
+    return kind
+
+
+# widths and row counts of each kernel that goes from row to row: rows of a warp, of a CTA in
+# registers, in shared memory (with 256, 512 and 1024 threads)
+@gpu
+@pytest.mark.parametrize("rows,cols", [(5000, 64), (5000, 1000), (2000, 2056), (1500, 8192),
+                                       (1600, 8200), (1500, 12288), (700, 32768)])
+@pytest.mark.parametrize("dtype", [torch.int8, E4M3])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rms_norm_quant_special_rows_among_many(rows, cols, dtype, residual):
+    x, w = normal((rows, cols), 5), torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    r = normal((rows, cols), 6) if residual else None
+
+    def put(value, at=slice(None)):
+        def change(row):
+            row[at] = value
+        return change
+
+    kind = scatter(x, [put(0.0), put(float("nan"), 3), put(float("inf"), cols - 1), put(-0.0),
+                       put(2.0 ** -110), put(2.0 ** 70, 7), put(2.0 ** -90),
+                       put(float("-inf"), 0)])
+    if residual:
+        r[kind >= 0] = 0
+    got = fq.rms_norm_quant(x, w, residual=r, dtype=dtype)
+    h, q, s = got if residual else (x, *got)
+    hr, qr, sr = plain_rms(x, w, r, dtype, 1e-6)
+    assert torch.equal(h.nan_to_num(7.0), hr.nan_to_num(7.0))
+    assert torch.equal(q.float(), qr.float())
+    close_scale(s, sr, cols)
+    nan = torch.isnan(s)
+    assert torch.equal(nan, (kind == 1) | (kind == 2) | (kind == 5) | (kind == 7))
+    assert not s[(kind == 0) | (kind == 3) | (kind == 4)].any()
+
+
+@gpu
+@pytest.mark.parametrize("cols", [64, 248, 2056, 6144, 8192, 12288, 32768])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rms_norm_quant_scales_close(cols, residual):
+    """A chunk's eight squares go through four roundings at most, and the carried sum of the chunks
+    is rounded once, as are the mean and the addition of eps: 7 * 2^-24, halved by the square root.
+    The root, its product with the maximum and the quotient are rounded once each: 6.5 * 2^-24 in
+    all, and 7 covers the products of these and the carried errors' own roundings (2^-44)."""
+    rows = 700
+    x, w = normal((rows, cols), 1, 2.0), (1 + 0.2 * normal((cols,), 2).float()).bfloat16()
+    x[:, cols // 2] *= 20
+    r = normal((rows, cols), 3) if residual else None
+    few = [fq.rms_norm_quant(x[i:i + 7], w, residual=None if r is None else r[i:i + 7])[-1]
+           for i in range(0, rows, 7)]
+    many = fq.rms_norm_quant(x, w, residual=r)[-1]
+    _, _, ref = plain_rms(x, w, r, torch.int8, 1e-6)
+    for s in (torch.cat(few), many):
+        assert bool(((s.double() - ref).abs() <= 7 * 2.0 ** -24 * ref).all())
+    # A sum within about 2^-44 of a border of fp32 may go either way, one row in 2^19.
+    assert torch.equal(torch.cat(few), many)
+
+
 # ------------------------------------------------------------------------------------------
 # silu_mul_quant
 # ------------------------------------------------------------------------------------------
@@ -226,6 +293,33 @@ def test_silu_mul_quant_special_rows(cols, dtype):
     assert torch.equal(q.float(), qr.float())
     close_scale(s, sr, 8)
     assert torch.isnan(s).tolist() == [False, True, True, False, False, False, False]
+
+
+# the same kernels, and rows wider than shared memory, read twice
+@gpu
+@pytest.mark.parametrize("rows,cols", [(5000, 64), (5000, 760), (2000, 2056), (1500, 6144),
+                                       (1600, 8200), (1500, 18432), (700, 40000), (700, 57856),
+                                       (700, 57864)])
+@pytest.mark.parametrize("dtype", [torch.int8, E4M3])
+def test_silu_mul_quant_special_rows_among_many(rows, cols, dtype):
+    gu = normal((rows, 2 * cols), 5)
+
+    def put(half, value, at=slice(None)):
+        def change(row):
+            row[half * cols:(half + 1) * cols][at] = value
+        return change
+
+    kind = scatter(gu, [put(0, 0.0), put(0, float("nan"), 3), put(1, float("inf"), cols - 1),
+                        put(0, -1000.0), put(1, 0.0), put(0, 1000.0, 5), put(1, 2.0 ** -120),
+                        put(0, float("inf"), 9)])
+    gu[kind == 7, cols + 9] = 0.0  # infinity times zero
+    g, u = gu[:, :cols], gu[:, cols:]
+    q, s = fq.silu_mul_quant(g, u, dtype=dtype)
+    qr, sr = plain_silu(g, u, dtype)
+    assert torch.equal(q.float(), qr.float())
+    close_scale(s, sr, 8)
+    assert torch.equal(torch.isnan(s), (kind == 1) | (kind == 2) | (kind == 7))
+    assert not s[(kind == 0) | (kind == 3) | (kind == 4) | (kind == 6)].any()
 
 
 # ------------------------------------------------------------------------------------------
@@ -640,6 +734,53 @@ def test_other_threads_run_during_a_call(tmp_path):
         thread.join()
         native.init(*real, fq._capi.check)
     assert fq.rms_norm_quant(x, w)[0].abs().max() == 127
+
+
+@gpu
+def test_calls_from_several_threads():
+    """Each thread on its own stream, all through the same launch caches."""
+    import threading
+    w = block_weights(512, 1376)
+    xs = [normal((m, 512), 40 + m) for m in (2, 20, 90, 330, 1100)]
+    want = [mlp_block(x, x, w) for x in xs]
+    torch.cuda.synchronize()
+    got, failed = [[] for _ in xs], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got[i].append(mlp_block(xs[i], xs[i], w))
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for i, runs in enumerate(got):
+        assert len(runs) == 30
+        for h, y in runs:
+            assert torch.equal(h, want[i][0]) and torch.equal(y, want[i][1])
+    assert fq.device_error() == 0
+
+
+@gpu
+def test_single_rows_without_a_row_dimension():
+    d, f = 512, 1376
+    w = block_weights(d, f)
+    x, r = normal((d,), 6), normal((d,), 7)
+    h, q, s = fq.rms_norm_quant(x, w["norm"], residual=r)
+    assert h.shape == q.shape == (d,) and s.shape == ()
+    gu = fq.int8_matmul(q, s, w["gu"], w["gu_s"])
+    q2, s2 = fq.silu_mul_quant(gu[:f], gu[f:])
+    assert gu.shape == (2 * f,) and q2.shape == (f,) and s2.shape == ()
+    hr, y = mlp_block(x[None], r[None], w)
+    assert torch.equal(h, hr[0])
+    assert torch.equal(fq.int8_matmul(q2, s2, w["down"], w["down_s"]), y[0])
 
 
 @gpu
