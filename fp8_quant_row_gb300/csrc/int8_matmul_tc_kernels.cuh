@@ -27,17 +27,19 @@
 // Conversion of four int8: flip the sign bits (value + 128), place each byte under the fp16
 // exponent of 1024 (1024 + 128 + value, exact), subtract 1152.
 //
-// Measured on one GB300 (graph replay): 4608 x 36864 x 6144 1079 us, 1935 TFLOP/s (cuBLAS in bf16
-// there: 1925 as a burst, 1743 sustained); 4608 x 6144 x 18432 586 us (1781). For a CTA of a pair one
-// stage is 1024 clocks of the tensor cores, and of shared memory too (32 KB each of copies in,
-// reads for conversion, converted tokens, and reads by the tensor cores): weights go to tensor
-// memory so that this is not more; about 1200 are reached. 16 x 36864 x 6144 40 us (86% of HBM),
-// 64 x 6144 x 6144 16 us. What it took, at 4608 x 6144 x 18432: waits and arrivals without
-// cluster-scope fences 993 -> 630 us; issue from uniform registers and two groups of converting
-// warps for either operand 630 -> 560; the accumulators in two halves -> 537.
+// Measured on one GB300 (four calls in a CUDA graph, median of five replays, below the power limit):
+// 4608 x 36864 x 6144 1043 us, 2002 TFLOP/s (cuBLAS in bf16 at that shape, the same way: 1046);
+// 4608 x 6144 x 18432 528 us, 1978 (cuBLAS 537). Called for seconds on end, at the power limit, 1150
+// to 1180 and 580 to 600. For a CTA of a pair one stage is 1024 clocks of the tensor cores, and of
+// shared memory too (32 KB each of copies in, reads for conversion, converted tokens, and reads by
+// the tensor cores): weights go to tensor memory so that this is not more; about 1200 are reached.
+// 16 x 36864 x 6144 40 us (85% of HBM), 64 x 6144 x 6144 15 us. What it took, at 4608 x 6144 x 18432
+// (here and below both sides of a change are from one session; sessions differ by some percent):
+// waits and arrivals without cluster-scope fences 993 -> 630 us; issue from uniform registers and two
+// groups of converting warps for either operand 630 -> 560; the accumulators in two halves -> 537.
 //
 // Every wait is bounded; a wait that runs out records the device error bit, the role stops, and
-// the CTA pair meets at the end, where tensor memory is freed.
+// the CTA pair meets at the end, where tensor memory is freed and every arrival on its way has landed.
 #pragma once
 
 #include <cuda.h>

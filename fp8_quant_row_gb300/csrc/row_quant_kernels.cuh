@@ -11,9 +11,9 @@
 // the codes do not depend on the order of any sum.
 // Bound: HBM. Measured on one GB300 (CUDA-graph replay, inputs larger than the L2 cache; share of
 // the 6690 GB/s of a plain copy): norm with residual 16384 x 8192 143 us (98%), 4608 x 6144 32.5
-// (91%), without residual 18.5 (68%: three bytes a value leave 7.6 values a clock and SM to form
-// and encode); silu 4608 x 18432 65.3 us (97%), 4608 x 10240 37.8 (93%); one row of 6144 2.1 us,
-// of 18432 3.0 us. What carried them: the products kept between the two passes as fp32 pairs (no
+// (91%); without residual 16384 x 8192 72 us (84%), 4608 x 6144 18.7 (68%: there its 16 warps an SM
+// are at work on instructions, 64% of the issue slots, and wait for loads in 5% of their time); silu
+// 4608 x 18432 65.7 us (97%), 4608 x 10240 37.8 (93%); one row of 6144 2.3 us, of 18432 3.0 us. What carried them: the products kept between the two passes as fp32 pairs (no
 // second unpacking), all loads of a row issued at once, the next row's before the reduction.
 //
 // A row with a NaN or infinite product gets the scale NaN and codes 0; one whose products are
@@ -201,8 +201,8 @@ __device__ __forceinline__ float sum_squares8(uint4 h) {
 // A row lives in the registers of its threads: `per_row` threads (a warp, several rows a CTA; or
 // the whole CTA), CPT chunks of eight values each. With MANY rows a thread keeps its weights and
 // goes from row to row, one grid apart, with the next row's loads issued before the current
-// row's reduction (two CTAs of 256 threads an SM keep 50 KB and more in flight); without, a CTA
-// has one row.
+// row's reduction (at 6144 columns two CTAs of 256 threads an SM keep 49 KB in flight with the
+// residual, 25 KB without it). With few rows a CTA has one.
 template <bool INT8, bool RESID, int CPT, bool MANY>
 __global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 2 : 1)
     rms_norm_quant_kernel(RmsParams p, int per_row) {

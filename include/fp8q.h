@@ -262,7 +262,8 @@ fp8q_status fp8q_qkv_epilogue(void* joint_q, void* joint_k, void* joint_v,
  *   scale = P / sqrt(mean_j(h_j^2) + eps) / QMAX             in fp32
  * so q_j * scale approximates the normalised h_j * w_j / rms. 1/rms cancels in q: the codes
  * are those of exact products whatever the order of the sum. The sum of squares carries its
- * rounding errors along, so that a row's scale does not depend on the call's row count either.
+ * rounding errors along, so that a row's scale does not depend on the call's row count either
+ * (but for a sum within about 2^-44 of a border between two fp32 values).
  *
  *   residual_out  out [rows, cols] bf16; NULL exactly when residual_bf16 is; may be exactly
  *                     the residual buffer (in-place update)
@@ -283,8 +284,8 @@ fp8q_status fp8q_rms_norm_quant(void* residual_out, void* q, float* q_scale, con
 
 /*
  * Gated activation -> 8-bit rows with one scale each:
- *   s_j = RN_bf16(RN_fp32(silu(gate_j))), silu(g) = g / (1 + exp(-g)); 0 for
- *         (of either sign) for finite g < -87, NaN for -infinity
+ *   s_j = RN_bf16(RN_fp32(silu(gate_j))), silu(g) = g / (1 + exp(-g)); 0 (of either
+ *         sign) for finite g < -87, NaN for -infinity
  *   p_j = s_j * up_j (exact in fp32), P, inv, q_j as above,  scale = P / QMAX
  * The gate's activation is rounded to bf16 (as where it is a tensor of its own), so that the
  * products are exact and the codes do not depend on how the exponential is computed.
