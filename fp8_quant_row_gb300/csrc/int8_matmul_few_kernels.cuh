@@ -13,7 +13,7 @@
 // rate: 258 against 1020 products a clock and SM; eight tokens at the memory's rate need 183.)
 // The warps' sums are added through shared memory in a fixed order.
 //
-// Measured on one GB300 (graph replay over weights larger than the L2 cache): 1 x 6144 x 6144 9.4
+// Measured on one GB300 (graph replay over weights larger than the L2 cache): 1 x 6144 x 6144 9.6
 // us, 1 x 6144 x 18432 22.0 us, 1 x 2048 x 2048 3.5 us: about 6 TB/s of weights after 3.5 us of
 // launch, first loads and last sums. Issue slots are half used (ncu), so the memory bounds it.
 #pragma once
