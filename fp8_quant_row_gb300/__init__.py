@@ -15,9 +15,16 @@ library's sm_103a kernels; there is no CPU or eager fallback.
     h, q, s = rms_norm_quant(x, weight, residual=r, dtype=torch.float8_e4m3fn)
     q, s = silu_mul_quant(gate, up)                 # SiLU(gate) * up -> 8-bit rows
     y = int8_matmul(q, s, w, w_scale, bias=b)       # int8 rows x int8 weights, scaled
+    q, k = qk_norm_rope(q, k, inv_freq, positions, q_weight=wq, k_weight=wk)
+    cache = paged_cache(pages, 64, kv_heads, 128)   # int8, float8_e4m3fn or bfloat16 pages
+    q = cache_write(k, v, cache, slots, q=q, inv_freq=f, positions=p)   # k and v to their pages
+    k, v = cache_read(cache, page_table, offsets, rows)                 # sequences back as bf16
+    o = paged_attention(q, cache, page_table, lengths)                  # one new token each
     bits = device_error()                           # 0 unless a bounded kernel wait ran out
 """
 from __future__ import annotations
+
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -27,7 +34,8 @@ from ._capi import Fp8qError
 
 __all__ = ["nss_fp8", "scale_residual_nss_fp8", "bias_mul_add", "token_cat_fp8",
            "token_cat_nvfp4", "nvfp4_scale_bytes", "qkv_epilogue", "rms_norm_quant", "silu_mul_quant",
-           "int8_matmul", "device_error",
+           "int8_matmul", "rotary_axes", "qk_norm_rope", "PagedCache", "paged_cache", "cache_write",
+           "cache_read", "paged_attention", "device_error",
            "row_pieces", "build",
            "Fp8qError", "library_path"]
 
@@ -231,7 +239,9 @@ def _native():
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
         loader.exec_module(m)
         m.init(*(ctypes.cast(getattr(_capi.lib(), f), ctypes.c_void_p).value for f in
-                 ("fp8q_rms_norm_quant", "fp8q_silu_mul_quant", "fp8q_int8_matmul")), _capi.check)
+                 ("fp8q_rms_norm_quant", "fp8q_silu_mul_quant", "fp8q_int8_matmul",
+                  "fp8q_qk_norm_rope", "fp8q_cache_write", "fp8q_cache_read",
+                  "fp8q_paged_attention", "fp8q_paged_attention_workspace")), _capi.check)
         _native_module = m
     return _native_module
 
@@ -281,9 +291,112 @@ def int8_matmul(a, a_scale, w, w_scale, *, bias=None, out_dtype=torch.bfloat16, 
     return m.int8_matmul(a, a_scale, w, w_scale, bias, ot, out)
 
 
+def rotary_axes(dims, *, theta: float = 10000.0, device="cuda"):
+    """(inv_freq, axis) of a rotation over several axes, for qk_norm_rope and cache_write: axis a
+    turns dims[a] values of a head, the j-th of its dims[a] / 2 pairs by theta^(-2j / dims[a])
+    radians a position. One axis: rotary_axes((head_dim,))."""
+    if not dims or any(d < 2 or d % 2 for d in dims):
+        raise ValueError("dims: expected positive even numbers")
+    freq = [theta ** (-2.0 * j / d) for d in dims for j in range(d // 2)]
+    axis = [a for a, d in enumerate(dims) for _ in range(d // 2)]
+    return (torch.tensor(freq, dtype=torch.float64, device=device),
+            torch.tensor(axis, dtype=torch.int32, device=device))
+
+
+def qk_norm_rope(q, k, inv_freq=None, positions=None, *, axis=None, q_weight=None, k_weight=None,
+                 eps: float = EPS, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Per-head RMSNorm of q and k (with the weights that are given) and rotation of each head's
+    first 2 * len(inv_freq) values, in fp32 and rounded once: (q, k). q: [tokens, heads, head_dim],
+    k: [tokens, kv_heads, head_dim] bfloat16, a token's heads adjacent (column slices of one packed
+    product will do); head_dim 64, 128 or 256. inv_freq: float64 radians a position, positions:
+    int32 or int64 [tokens], or [axes, tokens] with axis (int32) the axis of each pair.
+    interleaved: pairs (2i, 2i + 1), else (i, i + len(inv_freq)). q_out and k_out may be q and k."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_norm_rope(q, k, inv_freq, positions, axis=axis, q_weight=q_weight,
+                                k_weight=k_weight, eps=eps, interleaved=interleaved, q_out=q_out,
+                                k_out=k_out)
+    m = _native_module or _native()
+    return m.qk_norm_rope(q, k, inv_freq, positions, axis, interleaved, q_weight, k_weight, eps,
+                          q_out, k_out)
+
+
+class PagedCache(NamedTuple):
+    """Pages of keys and values: k, v [pages, heads, page_size, head_dim] int8, float8_e4m3fn or
+    bfloat16 (pages contiguous, at any one stride), k_scale, v_scale float32 [pages, heads,
+    page_size] (None for bfloat16). Token t of a sequence lies in the page that its page table
+    names at t // page_size, at t % page_size; that row's slot is page * page_size + t % page_size."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+
+
+def paged_cache(pages: int, page_size: int, heads: int, head_dim: int, *, dtype=torch.int8,
+                device="cuda") -> PagedCache:
+    """A zeroed PagedCache. page_size: a multiple of 16 up to 1024; head_dim 64, 128 or 256."""
+    if dtype not in (torch.int8, torch.float8_e4m3fn, torch.bfloat16):
+        raise TypeError(f"dtype: expected int8, float8_e4m3fn or bfloat16, got {dtype}")
+    if page_size < 16 or page_size > 1024 or page_size % 16 or head_dim not in (64, 128, 256):
+        raise ValueError(f"no cache of pages of {page_size} tokens and heads of {head_dim} values")
+    shape = (pages, heads, page_size, head_dim)
+    k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+    if dtype == torch.bfloat16:
+        return PagedCache(k, v)
+    return PagedCache(k, v, *(torch.zeros(shape[:3], dtype=torch.float32, device=device)
+                              for _ in range(2)))
+
+
+def cache_write(k, v, cache, slots, *, q=None, inv_freq=None, positions=None, axis=None,
+                q_weight=None, k_weight=None, eps: float = EPS, interleaved: bool = False,
+                q_out=None, stream=None):
+    """Writes k (normed and rotated as by qk_norm_rope) and v of each token to the cache's row
+    slots[token] (int64; negative: not stored; no two alike), in 8 bits with a scale for each token
+    and head or as bfloat16. With q, also returns q normed and rotated, from the same pass."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_write(k, v, cache, slots, q=q, inv_freq=inv_freq, positions=positions,
+                               axis=axis, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                               interleaved=interleaved, q_out=q_out)
+    m = _native_module or _native()
+    ck, cv, sk, sv = cache
+    return m.cache_write(k, v, ck, cv, sk, sv, slots, q, inv_freq, positions, axis, interleaved,
+                         q_weight, k_weight, eps, q_out)
+
+
+def cache_read(cache, page_table, offsets, rows: int, *, k=None, v=None, stream=None):
+    """Sequences read back as bfloat16 (k, v), each [rows, heads, head_dim]: row offsets[b] + t is
+    token t of the sequence with pages page_table[b]. page_table: int32 [batch, width]; offsets:
+    int64 [batch + 1], not falling; rows from offsets[-1] on are left as they were."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_read(cache, page_table, offsets, rows, k=k, v=v)
+    m = _native_module or _native()
+    ck, cv, sk, sv = cache
+    return m.cache_read(ck, cv, sk, sv, page_table, offsets, rows, k, v)
+
+
+def paged_attention(q, cache, page_table, lengths, *, scale=None, window: int = 0,
+                    return_lse: bool = False, out=None, lse=None, stream=None):
+    """Attention of one new token per sequence over its cached tokens (its own among them): out
+    [batch, heads, head_dim] bfloat16, with return_lse (out, lse), lse float32 [batch, heads] the
+    logarithm of the exponentials' sum. q: [batch, heads, head_dim] bfloat16, heads a multiple of
+    the cache's; page_table int32 [batch, width]; lengths int32 [batch]; scale: head_dim^-0.5 unless
+    given; window: only the last so many tokens (0: all). A sequence of length 0 gets zeros."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return paged_attention(q, cache, page_table, lengths, scale=scale, window=window,
+                                   return_lse=return_lse, out=out, lse=lse)
+    m = _native_module or _native()
+    ck, cv, sk, sv = cache
+    return m.paged_attention(q, ck, cv, sk, sv, page_table, lengths, scale, window, return_lse, out,
+                             lse)
+
+
 def device_error() -> int:
-    """Reads and clears the current device's error word (fp8q_device_error): 0 unless a
-    bounded wait inside a kernel ran out since the last call. Synchronises with the device."""
+    """Reads and clears the current device's error word (fp8q_device_error): 0 unless, since the
+    last call, a bounded wait inside a kernel ran out (1) or a slot or page lay outside its cache
+    (2). Synchronises with the device."""
     import ctypes
     bits = ctypes.c_uint(0)
     _capi.check(_capi.lib().fp8q_device_error(ctypes.byref(bits)), "fp8q_device_error")

@@ -12,7 +12,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8q.so")
-SOURCES = [os.path.join(CSRC, "fp8q_capi.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fp8q_capi.cu", "cache_capi.cu")]
 
 
 def deps() -> list:
@@ -31,9 +31,10 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 # The CUDA runtime is linked shared (soname libcudart.so.13): inside a process that already
 # loaded torch, the library binds to the same runtime instance torch uses.
-NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-              "-Xcompiler", "-Wall", "-cudart", "shared",
-              "-Xlinker", f"-rpath,{os.path.join(CUDA_HOME, 'lib64')}", f"-I{INCLUDE}"]
+NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
+              "-Xcompiler", "-Wall", f"-I{INCLUDE}"]
+LINK_FLAGS = ["-shared", "-cudart", "shared",
+              "-Xlinker", f"-rpath,{os.path.join(CUDA_HOME, 'lib64')}"]
 
 
 NATIVE_SOURCE = os.path.join(PKG, "native", "binding.cpp")
@@ -68,7 +69,8 @@ def native_up_to_date() -> bool:
         return False
     with open(stamp) as f:
         same = f.read() == _native_stamp()
-    return same and os.path.getmtime(NATIVE_SOURCE) <= os.path.getmtime(NATIVE)
+    return same and all(os.path.getmtime(f) <= os.path.getmtime(NATIVE)
+                        for f in (NATIVE_SOURCE, os.path.join(INCLUDE, "fp8q.h")))
 
 
 def build_native(force: bool = False) -> str:
@@ -83,6 +85,7 @@ def build_native(force: bool = False) -> str:
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
                     f"-I{sysconfig.get_paths()['include']}", f"-I{home}/include",
                     f"-I{home}/include/torch/csrc/api/include", f"-I{CUDA_HOME}/include",
+                    f"-I{INCLUDE}",
                     NATIVE_SOURCE, "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
                     "-ltorch_cuda", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"], check=True)
     os.replace(tmp, NATIVE)
@@ -94,13 +97,30 @@ def build_native(force: bool = False) -> str:
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the CUDA sources into fp8_quant_row_gb300/libfp8q.so (sm_103a only), and the native
     argument marshalling beside it."""
-    build_native(force)
     if not force and up_to_date():
+        build_native(force)
         return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc_path(), *ARCH, *NVCC_FLAGS, "-o", tmp, *SOURCES]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    tmp = f"{LIB}.tmp{os.getpid()}"
+    objects = [f"{tmp}.{i}.o" for i in range(len(SOURCES))]
+    try:
+        # the sources at once, each by a compiler of its own, and g++ beside them
+        jobs = []
+        for source, obj in zip(SOURCES, objects):
+            cmd = [nvcc_path(), *ARCH, *NVCC_FLAGS, "-c", "-o", obj, source]
+            if verbose:
+                cmd.insert(1, "-Xptxas=-v")
+            jobs.append(subprocess.Popen(cmd))
+        try:
+            build_native(force)
+        finally:
+            codes = [job.wait() for job in jobs]
+        for job, code in zip(jobs, codes):
+            if code:
+                raise subprocess.CalledProcessError(code, job.args)
+        subprocess.run([nvcc_path(), *ARCH, *LINK_FLAGS, "-o", tmp, *objects], check=True)
+        os.replace(tmp, LIB)
+    finally:
+        for obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
     return LIB

@@ -363,9 +363,10 @@ namespace fp8q {
 
 // Bits set by a kernel that gave up on a wait (a wait only runs out when a phase it depends
 // on never completes, i.e. on a defect): the kernel records the bit, stops taking work and
-// returns. The host reads and clears the word with fp8q_device_error().
+// returns. The host reads and clears the word with fp8q_device_error(). Each translation unit of the
+// library has a word of its own.
 constexpr unsigned kDevErrWaitTimeout = 1u;
-__device__ unsigned int g_device_error = 0u;
+static __device__ unsigned int g_device_error = 0u;
 
 __device__ __forceinline__ void report_device_error(unsigned bits) {
   atomicOr(&g_device_error, bits);

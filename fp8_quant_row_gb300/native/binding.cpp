@@ -1,4 +1,5 @@
-// binding.cpp -- native argument marshalling of the 8-bit row operators and their product.
+// binding.cpp -- native argument marshalling of the 8-bit row operators, their product and the paged
+// cache.
 //
 // A call for one token takes the device two or three microseconds; checks and allocations from
 // Python took ten and more. These functions check the tensors, allocate the outputs that are not
@@ -6,6 +7,9 @@
 // results. Refusals are TypeErrors, statuses of the library go to the Python check().
 #include <Python.h>
 
+#include <algorithm>
+#include <array>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <optional>
@@ -17,6 +21,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "fp8q.h"
+
 namespace {
 
 using RmsFn = int (*)(void*, void*, float*, const void*, const void*, const void*, int, int64_t,
@@ -25,9 +31,19 @@ using SiluFn = int (*)(void*, float*, const void*, const void*, int64_t, int, in
                        cudaStream_t);
 using MatmulFn = int (*)(void*, const int8_t*, int64_t, const float*, const int8_t*, const float*,
                          const void*, int, int64_t, int64_t, int64_t, cudaStream_t);
+using RopeFn = decltype(&fp8q_qk_norm_rope);
+using WriteFn = decltype(&fp8q_cache_write);
+using ReadFn = decltype(&fp8q_cache_read);
+using AttnFn = decltype(&fp8q_paged_attention);
+using AttnSizeFn = decltype(&fp8q_paged_attention_workspace);
 RmsFn g_rms = nullptr;
 SiluFn g_silu = nullptr;
 MatmulFn g_matmul = nullptr;
+RopeFn g_rope = nullptr;
+WriteFn g_write = nullptr;
+ReadFn g_read = nullptr;
+AttnFn g_attn = nullptr;
+AttnSizeFn g_attn_size = nullptr;
 PyObject* g_check = nullptr;  // raises the library's error of a status
 
 // Thrown once a Python error is set.
@@ -287,18 +303,365 @@ PyObject* int8_matmul(PyObject* const* arg, Py_ssize_t n) {
   return o.object();
 }
 
-// init(rms, silu, matmul, check): the C entry points' addresses and the error raiser
+// ------------------------------------------------------------------------------------------
+// the paged cache
+// ------------------------------------------------------------------------------------------
+
+// Heads of tokens: [tokens, heads, dim] bf16, a token's heads adjacent; ld: values between tokens.
+struct Heads {
+  int64_t tokens, heads, dim, ld;
+};
+
+Heads head_rows(const at::Tensor& t, const char* name) {
+  if (t.scalar_type() != at::kBFloat16 || t.dim() != 3)
+    refuse("%s: expected a bfloat16 tensor [tokens, heads, head_dim], got %s of %lld dimensions", name,
+           c10::toString(t.scalar_type()), (long long)t.dim());
+  Heads h{t.size(0), t.size(1), t.size(2), 0};
+  const bool fine = (t.stride(2) == 1 || h.dim <= 1) && (t.stride(1) == h.dim || h.heads <= 1);
+  if (!fine && t.numel() > 0)
+    refuse("%s: a token's heads have to be adjacent (strides %lld, %lld)", name,
+           (long long)t.stride(1), (long long)t.stride(2));
+  h.ld = h.tokens > 1 ? t.stride(0) : h.heads * h.dim;
+  return h;
+}
+
+// An output of heads: the given tensor, strided as inputs may be, or a new contiguous one.
+class HeadsOut {
+ public:
+  HeadsOut(const at::Tensor* given, PyObject* object, const Heads& like, const char* name)
+      : given_(given), object_(object), shape_{like.tokens, like.heads, like.dim},
+        ld_(like.heads * like.dim) {
+    if (!given) return;
+    const Heads h = head_rows(*given, name);
+    if (h.tokens != like.tokens || h.heads != like.heads || h.dim != like.dim)
+      refuse("%s: expected the shape [%lld, %lld, %lld]", name, (long long)like.tokens,
+             (long long)like.heads, (long long)like.dim);
+    ld_ = h.ld;
+  }
+  int64_t ld() const { return ld_; }
+  void* data(at::Device dev) {
+    if (given_) return given_->data_ptr();
+    made_ = at::detail::empty_cuda(shape_, at::kBFloat16, dev, std::nullopt);
+    return made_.data_ptr();
+  }
+  PyObject* object() {
+    if (given_) {
+      Py_INCREF(object_);
+      return object_;
+    }
+    PyObject* o = THPVariable_Wrap(std::move(made_));
+    if (!o) throw Refused{};
+    return o;
+  }
+
+ private:
+  const at::Tensor* given_;
+  PyObject* object_;
+  at::Tensor made_;
+  std::array<int64_t, 3> shape_;
+  int64_t ld_;
+};
+
+// A head's norm weight.
+const void* head_weight(const at::Tensor* w, int64_t dim, const char* name) {
+  if (!w) return nullptr;
+  contiguous(*w, at::kBFloat16, name);
+  if (w->numel() != dim)
+    refuse("%s: expected %lld values, got %lld", name, (long long)dim, (long long)w->numel());
+  return w->data_ptr();
+}
+
+// inv_freq, positions, axis, interleaved: arg[0 .. 3]; false without a rotation.
+bool rotary_of(fp8q_rotary* r, PyObject* const* arg, int64_t tokens, const at::Tensor* const t[3]) {
+  const at::Tensor *freq = t[0], *pos = t[1], *axis = t[2];
+  const int interleaved = PyObject_IsTrue(arg[3]);
+  if (interleaved < 0) throw Refused{};
+  if (!freq) {
+    if (pos || axis) refuse("positions and axis: given without inv_freq");
+    return false;
+  }
+  if (!pos) refuse("positions: needed with inv_freq");
+  if (freq->scalar_type() != at::kDouble || freq->dim() != 1 || !freq->is_contiguous())
+    refuse("inv_freq: expected contiguous float64 values, got %s of %lld dimensions",
+           c10::toString(freq->scalar_type()), (long long)freq->dim());
+  if (freq->size(0) > INT32_MAX) refuse("inv_freq: too many values");
+  const bool wide = pos->scalar_type() == at::kLong;
+  if ((!wide && pos->scalar_type() != at::kInt) || pos->dim() < 1 || pos->dim() > 2 ||
+      pos->size(-1) != tokens || (pos->stride(-1) != 1 && tokens > 1))
+    refuse("positions: expected int32 or int64 [tokens] or [axes, tokens] with %lld adjacent tokens",
+           (long long)tokens);
+  r->axes = pos->dim() == 2 ? int(std::min<int64_t>(pos->size(0), INT32_MAX)) : 1;
+  if (axis) {
+    if (axis->scalar_type() != at::kInt || axis->numel() != freq->size(0) || !axis->is_contiguous())
+      refuse("axis: expected %lld contiguous int32 values", (long long)freq->size(0));
+  } else if (r->axes != 1) {
+    refuse("axis: needed for positions on %d axes", r->axes);
+  }
+  r->inv_freq = static_cast<const double*>(freq->data_ptr());
+  r->axis = axis ? static_cast<const int32_t*>(axis->data_ptr()) : nullptr;
+  r->positions = pos->data_ptr();
+  r->position_stride = pos->dim() == 2 ? pos->stride(0) : tokens;
+  r->position_bytes = wide ? 8 : 4;
+  r->pairs = int(freq->size(0));
+  r->interleaved = interleaved;
+  return true;
+}
+
+// k, v, k_scale, v_scale: arg[0 .. 3].
+fp8q_paged_cache cache_of(const at::Tensor* const t[4]) {
+  const at::Tensor &k = *t[0], &v = *t[1];
+  fp8q_paged_cache c{};
+  const at::ScalarType type = k.scalar_type();
+  if (type == at::kChar) c.type = FP8Q_INT8;
+  else if (type == at::kFloat8_e4m3fn) c.type = FP8Q_E4M3;
+  else if (type == at::kBFloat16) c.type = FP8Q_BF16;
+  else refuse("cache.k: expected int8, float8_e4m3fn or bfloat16, got %s", c10::toString(type));
+  if (v.scalar_type() != type || k.dim() != 4 || v.sizes() != k.sizes())
+    refuse("cache.k and cache.v: expected one type and shape [pages, heads, page_size, head_dim]");
+  c.pages = k.size(0);
+  c.heads = k.size(1);
+  c.page_size = k.size(2);
+  c.head_dim = k.size(3);
+  const int64_t page = c.heads * c.page_size * c.head_dim, rows = c.heads * c.page_size;
+  auto stride = [&](const at::Tensor& x, int64_t size, const char* name) {
+    int64_t expected = 1;
+    bool fine = true;
+    for (int64_t d = x.dim() - 1; d > 0; --d) {
+      fine = fine && (x.size(d) == 1 || x.stride(d) == expected);
+      expected *= x.size(d);
+    }
+    if (!fine && x.numel() > 0) refuse("%s: a page has to be contiguous", name);
+    return c.pages > 1 ? x.stride(0) : size;
+  };
+  c.k_stride = stride(k, page, "cache.k");
+  c.v_stride = stride(v, page, "cache.v");
+  c.k = k.data_ptr();
+  c.v = v.data_ptr();
+  if (c.type == FP8Q_BF16) {
+    if (t[2] || t[3]) refuse("cache: scales beside bfloat16 values");
+    return c;
+  }
+  const at::IntArrayRef shape = k.sizes().slice(0, 3);
+  for (int i = 2; i < 4; ++i) {
+    const char* name = i == 2 ? "cache.k_scale" : "cache.v_scale";
+    if (!t[i] || t[i]->scalar_type() != at::kFloat || t[i]->sizes() != shape)
+      refuse("%s: expected float32 [pages, heads, page_size]", name);
+    (i == 2 ? c.k_scale_stride : c.v_scale_stride) = stride(*t[i], rows, name);
+    (i == 2 ? c.k_scale : c.v_scale) = static_cast<float*>(t[i]->data_ptr());
+  }
+  return c;
+}
+
+// A page table: int32 [batch, width], rows at one stride.
+struct Table {
+  const int32_t* p;
+  int64_t ld, width;
+};
+Table table_of(const at::Tensor& t, int64_t batch) {
+  if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != batch ||
+      (t.size(1) > 1 && t.stride(1) != 1))
+    refuse("page_table: expected int32 [%lld, width] with adjacent pages", (long long)batch);
+  return Table{static_cast<const int32_t*>(t.data_ptr()), batch > 1 ? t.stride(0) : t.size(1),
+               t.size(1)};
+}
+
+// qk_norm_rope(q, k, inv_freq, positions, axis, interleaved, q_weight, k_weight, eps, q_out, k_out)
+PyObject* qk_norm_rope(PyObject* const* arg, Py_ssize_t n) {
+  arguments(n, 11);
+  const at::Tensor &q = *tensor(arg[0], "q"), &k = *tensor(arg[1], "k");
+  const at::Tensor* rot[3] = {tensor(arg[2], "inv_freq", true), tensor(arg[3], "positions", true),
+                              tensor(arg[4], "axis", true)};
+  const at::Tensor* qw = tensor(arg[6], "q_weight", true);
+  const at::Tensor* kw = tensor(arg[7], "k_weight", true);
+  const double eps = PyFloat_AsDouble(arg[8]);
+  if (PyErr_Occurred()) throw Refused{};
+  const at::Tensor* q_out = tensor(arg[9], "q_out", true);
+  const at::Tensor* k_out = tensor(arg[10], "k_out", true);
+  const at::Device dev =
+      device_of(q, "q", {&k, rot[0], rot[1], rot[2], qw, kw, q_out, k_out});
+  const Heads qh = head_rows(q, "q"), kh = head_rows(k, "k");
+  if (kh.tokens != qh.tokens || kh.dim != qh.dim) refuse("q and k: expected one number of tokens and head_dim");
+  const void* qwp = head_weight(qw, qh.dim, "q_weight");
+  const void* kwp = head_weight(kw, qh.dim, "k_weight");
+  fp8q_rotary r{};
+  const bool turned = rotary_of(&r, arg + 2, qh.tokens, rot);
+  HeadsOut qo(q_out, arg[9], qh, "q_out"), ko(k_out, arg[10], kh, "k_out");
+  int status = 0;
+  {
+    Unlocked unlocked;
+    void *qp = qo.data(dev), *kp = ko.data(dev);
+    status = g_rope(qp, qo.ld(), kp, ko.ld(), q.data_ptr(), qh.ld, k.data_ptr(), kh.ld, qwp, kwp,
+                    float(eps), turned ? &r : nullptr, qh.tokens, qh.heads, kh.heads, qh.dim,
+                    c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+  }
+  check(status, "fp8q_qk_norm_rope");
+  PyObject* tuple = PyTuple_New(2);
+  if (!tuple) throw Refused{};
+  try {
+    PyTuple_SET_ITEM(tuple, 0, qo.object());
+    PyTuple_SET_ITEM(tuple, 1, ko.object());
+  } catch (...) {
+    Py_DECREF(tuple);
+    throw;
+  }
+  return tuple;
+}
+
+// cache_write(k, v, ck, cv, sk, sv, slots, q, inv_freq, positions, axis, interleaved, q_weight,
+//             k_weight, eps, q_out)
+PyObject* cache_write(PyObject* const* arg, Py_ssize_t n) {
+  arguments(n, 16);
+  const at::Tensor &k = *tensor(arg[0], "k"), &v = *tensor(arg[1], "v");
+  const at::Tensor* parts[4] = {tensor(arg[2], "cache.k"), tensor(arg[3], "cache.v"),
+                                tensor(arg[4], "cache.k_scale", true),
+                                tensor(arg[5], "cache.v_scale", true)};
+  const at::Tensor& slots = *tensor(arg[6], "slots");
+  const at::Tensor* q = tensor(arg[7], "q", true);
+  const at::Tensor* rot[3] = {tensor(arg[8], "inv_freq", true), tensor(arg[9], "positions", true),
+                              tensor(arg[10], "axis", true)};
+  const at::Tensor* qw = tensor(arg[12], "q_weight", true);
+  const at::Tensor* kw = tensor(arg[13], "k_weight", true);
+  const double eps = PyFloat_AsDouble(arg[14]);
+  if (PyErr_Occurred()) throw Refused{};
+  const at::Tensor* q_out = tensor(arg[15], "q_out", true);
+  const at::Device dev = device_of(k, "k", {&v, parts[0], parts[1], parts[2], parts[3], &slots, q,
+                                            rot[0], rot[1], rot[2], qw, kw, q_out});
+  const fp8q_paged_cache cache = cache_of(parts);
+  const Heads kh = head_rows(k, "k"), vh = head_rows(v, "v");
+  if (vh.tokens != kh.tokens || vh.heads != kh.heads || vh.dim != kh.dim)
+    refuse("k and v: expected one shape");
+  if (kh.heads != cache.heads || kh.dim != cache.head_dim)
+    refuse("k: expected the cache's [tokens, %lld, %lld]", (long long)cache.heads,
+           (long long)cache.head_dim);
+  if (slots.scalar_type() != at::kLong || slots.numel() != kh.tokens || !slots.is_contiguous())
+    refuse("slots: expected %lld contiguous int64 values", (long long)kh.tokens);
+  std::optional<HeadsOut> qo;
+  Heads qh{kh.tokens, 0, kh.dim, 0};
+  if (q) {
+    qh = head_rows(*q, "q");
+    if (qh.tokens != kh.tokens || qh.dim != kh.dim || qh.heads < 1)
+      refuse("q: expected [%lld, heads, %lld]", (long long)kh.tokens, (long long)kh.dim);
+    qo.emplace(q_out, arg[15], qh, "q_out");
+  } else if (q_out || qw) {
+    refuse("q_out and q_weight: given without q");
+  }
+  const void* qwp = head_weight(qw, kh.dim, "q_weight");
+  const void* kwp = head_weight(kw, kh.dim, "k_weight");
+  fp8q_rotary r{};
+  const bool turned = rotary_of(&r, arg + 8, kh.tokens, rot);
+  int status = 0;
+  {
+    Unlocked unlocked;
+    void* qp = qo ? qo->data(dev) : nullptr;
+    status = g_write(&cache, static_cast<const int64_t*>(slots.data_ptr()), qp, qo ? qo->ld() : 0,
+                     q ? q->data_ptr() : nullptr, qh.ld, k.data_ptr(), kh.ld, v.data_ptr(), vh.ld,
+                     qwp, kwp, float(eps), turned ? &r : nullptr, kh.tokens, qh.heads,
+                     c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+  }
+  check(status, "fp8q_cache_write");
+  if (qo) return qo->object();
+  Py_RETURN_NONE;
+}
+
+// cache_read(ck, cv, sk, sv, page_table, offsets, rows, k, v)
+PyObject* cache_read(PyObject* const* arg, Py_ssize_t n) {
+  arguments(n, 9);
+  const at::Tensor* parts[4] = {tensor(arg[0], "cache.k"), tensor(arg[1], "cache.v"),
+                                tensor(arg[2], "cache.k_scale", true),
+                                tensor(arg[3], "cache.v_scale", true)};
+  const at::Tensor &table = *tensor(arg[4], "page_table"), &offsets = *tensor(arg[5], "offsets");
+  const int64_t rows = PyLong_AsLongLong(arg[6]);
+  if (PyErr_Occurred()) throw Refused{};
+  const at::Tensor *k = tensor(arg[7], "k", true), *v = tensor(arg[8], "v", true);
+  const at::Device dev = device_of(*parts[0], "cache.k", {parts[1], parts[2], parts[3], &table,
+                                                          &offsets, k, v});
+  const fp8q_paged_cache cache = cache_of(parts);
+  if (rows < 0) refuse("rows: expected 0 or more");
+  if (offsets.scalar_type() != at::kLong || offsets.dim() != 1 || offsets.size(0) < 1 ||
+      !offsets.is_contiguous())
+    refuse("offsets: expected contiguous int64 [batch + 1]");
+  const int64_t batch = offsets.size(0) - 1;
+  const Table t = table_of(table, batch);
+  const std::array<int64_t, 3> shape{rows, cache.heads, cache.head_dim};
+  Out ko(k, arg[7], shape, at::kBFloat16, "k"), vo(v, arg[8], shape, at::kBFloat16, "v");
+  int status = 0;
+  {
+    Unlocked unlocked;
+    void *kp = ko.data(dev), *vp = vo.data(dev);
+    status = g_read(kp, vp, &cache, t.p, t.ld, t.width, static_cast<const int64_t*>(offsets.data_ptr()),
+                    batch, rows, c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+  }
+  check(status, "fp8q_cache_read");
+  return results({&ko, &vo});
+}
+
+// paged_attention(q, ck, cv, sk, sv, page_table, lengths, scale, window, return_lse, out, lse)
+PyObject* paged_attention(PyObject* const* arg, Py_ssize_t n) {
+  arguments(n, 12);
+  const at::Tensor& q = *tensor(arg[0], "q");
+  const at::Tensor* parts[4] = {tensor(arg[1], "cache.k"), tensor(arg[2], "cache.v"),
+                                tensor(arg[3], "cache.k_scale", true),
+                                tensor(arg[4], "cache.v_scale", true)};
+  const at::Tensor &table = *tensor(arg[5], "page_table"), &lengths = *tensor(arg[6], "lengths");
+  const bool own_scale = arg[7] != Py_None;
+  const double scale = own_scale ? PyFloat_AsDouble(arg[7]) : 0.0;
+  const int64_t window = PyLong_AsLongLong(arg[8]);
+  const int want_lse = PyObject_IsTrue(arg[9]);
+  if (PyErr_Occurred()) throw Refused{};
+  const at::Tensor *out = tensor(arg[10], "out", true), *lse = tensor(arg[11], "lse", true);
+  const at::Device dev = device_of(q, "q", {parts[0], parts[1], parts[2], parts[3], &table, &lengths,
+                                            out, lse});
+  const fp8q_paged_cache cache = cache_of(parts);
+  const Heads qh = head_rows(q, "q");
+  if (qh.dim != cache.head_dim || cache.heads < 1 || qh.heads < 1 || qh.heads % cache.heads != 0)
+    refuse("q: expected [batch, a multiple of %lld heads, %lld]", (long long)cache.heads,
+           (long long)cache.head_dim);
+  if (lengths.scalar_type() != at::kInt || lengths.numel() != qh.tokens || !lengths.is_contiguous())
+    refuse("lengths: expected %lld contiguous int32 values", (long long)qh.tokens);
+  const Table t = table_of(table, qh.tokens);
+  if (lse && !want_lse) refuse("lse: given without return_lse");
+  const std::array<int64_t, 3> shape{qh.tokens, qh.heads, qh.dim};
+  Out o(out, arg[10], shape, at::kBFloat16, "out");
+  std::optional<Out> l;
+  if (want_lse) l.emplace(lse, arg[11], at::IntArrayRef(shape).slice(0, 2), at::kFloat, "lse");
+  int status = 0;
+  at::Tensor workspace;  // (stays this stream's when it goes: later work of the stream may take it)
+  {
+    Unlocked unlocked;
+    const int64_t bytes = g_attn_size(&cache, qh.tokens, qh.heads, t.width);
+    void* wp = nullptr;
+    if (bytes > 0) {
+      workspace = at::detail::empty_cuda({bytes}, at::kByte, dev, std::nullopt);
+      wp = workspace.data_ptr();
+    }
+    void* op = o.data(dev);
+    float* lp = l ? static_cast<float*>(l->data(dev)) : nullptr;
+    status = g_attn(op, lp, q.data_ptr(), qh.ld, &cache, t.p, t.ld, t.width,
+                    static_cast<const int32_t*>(lengths.data_ptr()), qh.tokens, qh.heads,
+                    own_scale ? float(scale) : 1.0f / std::sqrt(float(qh.dim)), window, wp,
+                    bytes > 0 ? bytes : 0, c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+  }
+  check(status, "fp8q_paged_attention");
+  return l ? results({&o, &*l}) : o.object();
+}
+
+// init(...): the C entry points' addresses and the error raiser
 PyObject* init(PyObject* const* arg, Py_ssize_t n) {
-  arguments(n, 4);
-  void* f[3];
-  for (int i = 0; i < 3; ++i) f[i] = PyLong_AsVoidPtr(arg[i]);
+  arguments(n, 9);
+  void* f[8];
+  for (int i = 0; i < 8; ++i) f[i] = PyLong_AsVoidPtr(arg[i]);
   if (PyErr_Occurred()) throw Refused{};
   g_rms = reinterpret_cast<RmsFn>(f[0]);
   g_silu = reinterpret_cast<SiluFn>(f[1]);
   g_matmul = reinterpret_cast<MatmulFn>(f[2]);
+  g_rope = reinterpret_cast<RopeFn>(f[3]);
+  g_write = reinterpret_cast<WriteFn>(f[4]);
+  g_read = reinterpret_cast<ReadFn>(f[5]);
+  g_attn = reinterpret_cast<AttnFn>(f[6]);
+  g_attn_size = reinterpret_cast<AttnSizeFn>(f[7]);
   Py_XDECREF(g_check);
-  Py_INCREF(arg[3]);
-  g_check = arg[3];
+  Py_INCREF(arg[8]);
+  g_check = arg[8];
   Py_RETURN_NONE;
 }
 
@@ -322,7 +685,10 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {method<init>("init"), method<rms_norm_quant>("rms_norm_quant"),
                            method<silu_mul_quant>("silu_mul_quant"),
-                           method<int8_matmul>("int8_matmul"), {nullptr, nullptr, 0, nullptr}};
+                           method<int8_matmul>("int8_matmul"), method<qk_norm_rope>("qk_norm_rope"),
+                           method<cache_write>("cache_write"), method<cache_read>("cache_read"),
+                           method<paged_attention>("paged_attention"),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 

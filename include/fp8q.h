@@ -14,6 +14,11 @@
  *   silu_mul_quant          SiLU(gate) * up -> 8-bit rows, one fp32 scale each.
  *   int8_matmul             product of int8 rows and int8 weights with a scale for each row
  *                           (token) and each weight row (output channel).
+ *   qk_norm_rope            per-head RMSNorm and rotation of q and k, from positions.
+ *   cache_write             the same pass, k and v to the pages of a cache (bf16, or 8-bit rows
+ *                           with one fp32 scale each).
+ *   cache_read              sequences of a paged cache back as bf16 rows.
+ *   paged_attention         attention of one new token per sequence over a paged cache.
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers to row-major, contiguous arrays on the current
@@ -74,7 +79,7 @@ typedef enum fp8q_status {
     FP8Q_ERR_UNSUPPORTED = 4, /* current device is not compute capability 10.3                */
     FP8Q_ERR_ALIAS = 5,       /* an output overlaps an input or another output (see per call) */
     FP8Q_ERR_CUDA = 6,        /* a CUDA runtime query or the kernel launch failed             */
-    FP8Q_ERR_VALUE = 7        /* a scalar argument is out of range (eps, q_type, out_type)     */
+    FP8Q_ERR_VALUE = 7        /* a scalar argument is out of range (eps, q_type, out_type, ...) */
 } fp8q_status;
 
 /*
@@ -326,8 +331,137 @@ fp8q_status fp8q_int8_matmul(void* out, const int8_t* a, int64_t lda, const floa
                              const int8_t* w, const float* w_scale, const void* bias_bf16,
                              int out_type, int64_t m, int64_t n, int64_t k, cudaStream_t stream);
 
+/* Element type of a cache beside FP8Q_INT8 and FP8Q_E4M3. */
+#define FP8Q_BF16 2
+
+/*
+ * A paged key/value cache: token t of a sequence lies in the page that its page table names at
+ * t / page_size, at row t % page_size of each head. A slot is page * page_size + row.
+ */
+typedef struct fp8q_paged_cache {
+    void* k;         /* [pages, heads, page_size, head_dim] of `type`, 16-byte aligned            */
+    void* v;
+    float* k_scale;  /* [pages, heads, page_size] fp32, 4-byte aligned; NULL for FP8Q_BF16        */
+    float* v_scale;
+    int64_t k_stride, v_stride;              /* values between pages: >= heads*page_size*head_dim,
+                                                a multiple of 16 (k and v may be the halves of one
+                                                [pages, 2, ...] array); pages are contiguous       */
+    int64_t k_scale_stride, v_scale_stride;  /* values between pages of the scales                */
+    int64_t pages;
+    int64_t page_size;  /* a multiple of 16, 16 .. 1024; pages * page_size < 2^47                  */
+    int64_t heads;      /* key/value heads, 1 .. 4096                                              */
+    int64_t head_dim;   /* 64, 128 or 256                                                          */
+    int type;           /* FP8Q_INT8, FP8Q_E4M3 or FP8Q_BF16                                       */
+} fp8q_paged_cache;
+
+/* A rotation by positions on one or several axes (time, height, width, ...). */
+typedef struct fp8q_rotary {
+    const double* inv_freq;   /* [pairs] radians a position (device)                               */
+    const int32_t* axis;      /* [pairs] the axis whose position turns the pair (device); NULL: 0.
+                                 Values outside 0 .. axes-1 count as the nearest of these          */
+    const void* positions;    /* [axes, tokens] int32 or int64 (device)                            */
+    int64_t position_stride;  /* values between axes (>= tokens where axes > 1)                    */
+    int position_bytes;       /* 4 or 8                                                            */
+    int axes;                 /* >= 1                                                              */
+    int pairs;                /* 1 .. head_dim/2: the first 2*pairs values of a head are rotated   */
+    int interleaved;          /* pairs (2i, 2i+1); else (i, i + pairs), pairs a multiple of 8 or
+                                 head_dim/2                                                        */
+} fp8q_rotary;
+
+/*
+ * Per-head norm and rotation of q and k, all in fp32 and rounded once:
+ *   n_j = x_j * w_j / sqrt(mean_i(x_i^2) + eps)      (n = x without a weight)
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t) for each rotated pair of n,
+ *             t = inv_freq[i] * position[axis[i]][token]
+ * Angles are reduced exactly, at any position (the frequency is rounded to 2^-53 of itself).
+ *
+ *   q_out, k_out  out [tokens, heads, head_dim] bf16, row strides q_out_ld, k_out_ld; may be exactly
+ *                     q (k) with its stride
+ *   q, k          in  bf16, row strides q_ld, k_ld (values, >= heads*head_dim, a multiple of 8), heads
+ *                     adjacent: tensors, or column slices of one packed product
+ *   q_weight, k_weight  in [head_dim] bf16, 16-byte aligned; NULL: no norm
+ *   rotary        NULL: no rotation
+ *   q_heads, kv_heads   1 .. 4096;  head_dim 64, 128 or 256;  eps > 0 where there is a weight
+ *   Aliasing: an output may not overlap another output or an input, but for the exact case above.
+ */
+fp8q_status fp8q_qk_norm_rope(void* q_out, int64_t q_out_ld, void* k_out, int64_t k_out_ld,
+                              const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                              const void* q_weight, const void* k_weight, float eps,
+                              const fp8q_rotary* rotary, int64_t tokens, int64_t q_heads,
+                              int64_t kv_heads, int64_t head_dim, cudaStream_t stream);
+
+/*
+ * The same pass with k (normed and rotated) and v (as it is) going to the cache's rows slots[token]:
+ * bf16, or codes and scale as fp8q_rms_norm_quant's: P = max|x|, inv = RN(QMAX * RN(1/P)),
+ * codes RNE(x * inv) or E4M3(RN(x * inv)), scale = RN(P / QMAX); a row with a NaN or an infinity gets
+ * the scale NaN and codes 0, one with P < 2^-100 zeros.
+ *
+ *   q_out, q    NULL with q_heads 0: only k and v. Else as above
+ *   k, v        in  [tokens, heads, head_dim] bf16, row strides k_ld, v_ld
+ *   slots       in  [tokens] int64 (device). A token with a negative slot is not stored (its q is
+ *                   computed); one past the cache is not stored either and sets
+ *                   FP8Q_DEVERR_BAD_INDEX. Tokens of one call must not share a slot: whose values
+ *                   it holds then is not defined
+ *   Aliasing: q_out and the cache's arrays overlap no input and not each other (q_out may be q).
+ */
+fp8q_status fp8q_cache_write(const fp8q_paged_cache* cache, const int64_t* slots, void* q_out,
+                             int64_t q_out_ld, const void* q, int64_t q_ld, const void* k,
+                             int64_t k_ld, const void* v, int64_t v_ld, const void* q_weight,
+                             const void* k_weight, float eps, const fp8q_rotary* rotary,
+                             int64_t tokens, int64_t q_heads, cudaStream_t stream);
+
+/*
+ * Sequences read back: row offsets[b] + t of k_out and v_out is token t of sequence b,
+ * RN_bf16(code * scale) (bf16: the value).
+ *
+ *   k_out, v_out  out [rows, heads, head_dim] bf16, contiguous, 16-byte aligned. Rows before
+ *                     offsets[0] and from offsets[batch] on are left as they are
+ *   page_table    in  [batch, width] int32 pages, row stride table_ld (4-byte aligned)
+ *   offsets       in  [batch + 1] int64, not falling (device)
+ *   A token whose page is outside the cache or past the table's width reads as zeros and sets
+ *   FP8Q_DEVERR_BAD_INDEX.
+ */
+fp8q_status fp8q_cache_read(void* k_out, void* v_out, const fp8q_paged_cache* cache,
+                            const int32_t* page_table, int64_t table_ld, int64_t width,
+                            const int64_t* offsets, int64_t batch, int64_t rows,
+                            cudaStream_t stream);
+
+/*
+ * Attention of one new token per sequence: with n = lengths[b] tokens in the cache (the new one's
+ * own among them) and head h of q reading key/value head h / (q_heads / heads),
+ *   s_t = scale * q . k_t,  out = sum_t exp(s_t) v_t / sum_t exp(s_t),  lse = ln sum_t exp(s_t)
+ * over t in [max(0, n - window), n) (window 0: all). A sequence without tokens gets zeros and
+ * lse -infinity. Logits, maxima and sums are fp32, 8-bit codes exact, a weight times its value's
+ * scale is rounded to fp16 (and to a multiple of 2^-33 of the largest; bf16 cache: to 16 bits), the
+ * output once to bf16. Keys and values outside
+ * the range may hold anything.
+ *
+ *   out         out [batch, q_heads, head_dim] bf16, contiguous, 16-byte aligned
+ *   lse         out [batch, q_heads] fp32 or NULL
+ *   q           in  [batch, q_heads, head_dim] bf16, row stride q_ld (a multiple of 8)
+ *   page_table  in  [batch, width] int32, row stride table_ld; only entries of pages within the range
+ *                   are read. A page outside the cache is left out of the sums and sets
+ *                   FP8Q_DEVERR_BAD_INDEX
+ *   lengths     in  [batch] int32 (device); clamped to 0 .. width*page_size
+ *   q_heads     a multiple of cache->heads;  width*page_size < 2^30;  scale finite;  window >= 0
+ *   workspace   device buffer of workspace_bytes >= fp8q_paged_attention_workspace(...), 16-byte
+ *               aligned, contents irrelevant before and after; calls that may run at the same time
+ *               need one each. NULL where that size is 0
+ * One kernel, and a second that joins the pieces of long sequences where a sequence may have any.
+ */
+fp8q_status fp8q_paged_attention(void* out, float* lse, const void* q, int64_t q_ld,
+                                 const fp8q_paged_cache* cache, const int32_t* page_table,
+                                 int64_t table_ld, int64_t width, const int32_t* lengths,
+                                 int64_t batch, int64_t q_heads, float scale, int64_t window,
+                                 void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of fp8q_paged_attention's workspace on the current device; -1 for unsupported sizes. */
+int64_t fp8q_paged_attention_workspace(const fp8q_paged_cache* cache, int64_t batch,
+                                       int64_t q_heads, int64_t width);
+
 /* Bits of the device error word (fp8q_device_error). */
 #define FP8Q_DEVERR_WAIT_TIMEOUT 1u /* a kernel gave up on a bounded shared-memory wait */
+#define FP8Q_DEVERR_BAD_INDEX 2u    /* a slot or page outside the cache (the access was left out) */
 
 /*
  * Reads and clears the device error word of the current device. Every wait inside the
@@ -352,8 +486,8 @@ int fp8q_last_cuda_error(void);
 const char* fp8q_last_error_detail(void);
 
 /* Library ABI version: 0x00MMmmpp (0.2.0: token_cat_nvfp4 and qkv_epilogue added; 0.3.0:
- * fp8q_device_error added, later rms_norm_quant, silu_mul_quant and int8_matmul: new entry
- * points beside unchanged ones keep the number). */
+ * fp8q_device_error added, later rms_norm_quant, silu_mul_quant, int8_matmul and the paged cache:
+ * new entry points beside unchanged ones keep the number). */
 int fp8q_version(void);
 
 #ifdef __cplusplus
