@@ -214,8 +214,13 @@ int attn_warps(const fp8q_paged_cache& c) {
   return c.head_dim * (c.type == FP8Q_BF16 ? 2 : 1) >= 512 ? 4 : 8;
 }
 
+// CTAs an SM (AttnLayout::kCtas).
+int attn_ctas(const fp8q_paged_cache& c, int nt) {
+  return c.head_dim * (c.type == FP8Q_BF16 ? 2 : 1) <= 128 && nt == 1 ? 2 : 1;
+}
+
 struct AttnShape {
-  int nt, blocks, grid;
+  int nt, blocks, warps, grid, segments;
   bool join;  // sequences may be long enough for several CTAs
 };
 
@@ -227,8 +232,10 @@ AttnShape attn_shape(const fp8q_paged_cache& c, int64_t batch, int64_t q_heads, 
   s.blocks = int((group + 8 * s.nt - 1) / (8 * s.nt));
   const int64_t most = width * (c.page_size / 16);  // tiles of a sequence
   const int64_t segments = batch * c.heads * s.blocks;
-  s.grid = int(std::min<int64_t>(sms, segments * std::max<int64_t>(most, 1)));
-  s.join = most > attn_warps(c);
+  s.warps = attn_warps(c);
+  s.segments = int(segments);
+  s.grid = int(std::min<int64_t>(sms * attn_ctas(c, s.nt), segments * std::max<int64_t>(most, 1)));
+  s.join = most > s.warps;  // (AttnSplit: by tile only then)
   return s;
 }
 
@@ -238,19 +245,25 @@ fp8q_status check_attention(const fp8q_paged_cache& c, int64_t batch, int64_t q_
   if (st != FP8Q_OK) return st;
   if (batch < 0 || batch > (1 << 20) || q_heads < 1 || q_heads > kMaxHeads * 64 ||
       q_heads % c.heads != 0 || batch * q_heads > INT32_MAX || width < 0 ||
-      width * c.page_size >= (int64_t(1) << 30))
+      width * c.page_size >= (int64_t(1) << 30) ||
+      width * (c.page_size / 16) * q_heads > INT32_MAX)  // (tiles of a sequence, all heads)
     return FP8Q_ERR_SHAPE;
   return FP8Q_OK;
 }
 
+// A slot for each warp and two for each CTA (AttnParams::part_o, part_ml).
+int64_t workspace_slots(const AttnShape& s) { return int64_t(s.grid) * (s.warps + 2); }
 int64_t workspace_bytes_of(const AttnShape& s, int64_t head_dim) {
-  return s.join ? int64_t(2) * s.grid * 8 * s.nt * (head_dim + 2) * 4 : 0;
+  return s.join ? (workspace_slots(s) * head_dim + int64_t(2) * s.grid * 2) * 8 * s.nt * 4 : 0;
 }
+
+fp8q::FastDiv fast_div_by(int64_t d) { return fp8q::FastDiv{d == 1 ? 0 : UINT64_MAX / uint64_t(d) + 1}; }
 
 template <int TYPE, int D, int NT>
 fp8q_status launch_attention(const fp8q::AttnParams& p, const AttnShape& s, cudaStream_t stream) {
   using L = fp8q::AttnLayout<TYPE, D, NT>;
-  static_assert(L::kStages >= 2 && L::kBytes <= 232448, "two stages fit an SM's shared memory");
+  static_assert(L::kStages >= 2 && L::kStages <= 16 && L::kBytes <= L::kMost, "a ring fits its SM's share");
+  static_assert(L::kItems % fp8q::kJoinItems == 0, "whole CTAs of the join");
   auto* fn = fp8q::paged_attention_kernel<TYPE, D, NT>;
   int bps = 0;
   fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), L::kWarps * 32, L::kBytes, &bps);
@@ -258,9 +271,9 @@ fp8q_status launch_attention(const fp8q::AttnParams& p, const AttnShape& s, cuda
   if (bps <= 0) return cuda_fail(cudaErrorInvalidConfiguration, "occupancy", (long long)L::kBytes);
   st = launch(fn, dim3(unsigned(s.grid)), dim3(L::kWarps * 32), size_t(L::kBytes), stream, p);
   if (st != FP8Q_OK || !s.join) return st;
-  const unsigned segments = unsigned(p.batch * p.cache.heads * p.blocks);
-  return launch(fp8q::attn_join_kernel<D, L::kWarps, NT>, dim3(segments, std::min(8 * NT, p.group)),
-                dim3(D / 2), 0, stream, p);
+  return launch(fp8q::attn_join_kernel<TYPE, D, NT>,
+                dim3(unsigned(std::min(p.segments, p.grid)), L::kItems / fp8q::kJoinItems),
+                dim3(fp8q::kJoinWarps * 32), 0, stream, p);
 }
 
 template <int TYPE>
@@ -514,7 +527,8 @@ fp8q_status fp8q_paged_attention(void* out, float* lse, const void* q, int64_t q
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = p.part_o ? p.part_o + int64_t(2) * s.grid * 8 * s.nt * cache->head_dim : nullptr;
+  p.part_ml = p.part_o ? reinterpret_cast<float2*>(p.part_o + workspace_slots(s) * 8 * s.nt * cache->head_dim)
+                       : nullptr;
   p.batch = int(batch);
   p.width = cache->pages > 0 ? int(width) : 0;  // no page to read: no tokens
   p.window = int(std::min<int64_t>(window, INT32_MAX));
@@ -522,6 +536,11 @@ fp8q_status fp8q_paged_attention(void* out, float* lse, const void* q, int64_t q
   p.group = int(q_heads / cache->heads);
   p.blocks = s.blocks;
   p.grid = s.grid;
+  p.segments = s.segments;
+  p.heads = int(cache->heads) * s.blocks;
+  p.warp_rounds = int((int64_t(s.segments) + int64_t(s.grid) * s.warps - 1) / (int64_t(s.grid) * s.warps));
+  p.by_warps = fast_div_by(int64_t(s.grid) * s.warps);
+  p.by_heads = fast_div_by(p.heads);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.page_tiles = int(cache->page_size / 16);
   p.tile_magic = uint32_t(((int64_t(1) << 32) + p.page_tiles - 1) / p.page_tiles);

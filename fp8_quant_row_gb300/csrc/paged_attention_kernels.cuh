@@ -31,6 +31,14 @@
 
 namespace fp8q {
 
+// x / d for x * d < 2^64.
+struct FastDiv {
+  uint64_t magic;  // ceil(2^64 / d); 0 for d = 1
+};
+__device__ __forceinline__ int64_t fast_div(int64_t x, FastDiv d) {
+  return d.magic ? int64_t(__umul64hi(uint64_t(x), d.magic)) : x;
+}
+
 struct AttnParams {
   const uint16_t* q;  // [batch, q_heads, D], row stride q_ld
   int64_t q_ld;
@@ -40,11 +48,16 @@ struct AttnParams {
   const int32_t* lengths;
   uint16_t* out;  // [batch, q_heads, D]
   float* lse;     // [batch, q_heads] or null
-  float* part_o;  // partial sums of pieces: [2 grid][heads of a block][D]
-  float* part_ml;  // [2 grid][heads of a block][2]: maximum (log2 units), sum
+  // Sums of pieces of segments: values (AttnLayout::kPiece of them) and for each head the maximum
+  // (log2 units) and the sum; a slot for each warp's first piece, then two for each CTA.
+  float* part_o;
+  float2* part_ml;
   int batch, width, window;  // width: pages a sequence may have
   int q_heads, group, blocks;  // heads a key/value head; blocks of 8 NT of them
   int grid;  // CTAs of the attention kernel
+  int segments, heads;  // heads: blocks of heads a sequence
+  int warp_rounds;      // segments a warp, if each warp takes whole ones
+  FastDiv by_warps, by_heads;  // by grid * warps, by heads
   float scale_log2;
   uint32_t tile_magic;  // ceil(2^32 / (page_size / 16))
   int page_tiles;
@@ -56,19 +69,23 @@ template <int TYPE, int D, int NT>
 struct AttnLayout {
   static constexpr int E = TYPE == kCacheBf16 ? 2 : 1;
   static constexpr int kWarps = D * E >= 512 ? 4 : 8;
+  static constexpr int kCtas = D * E <= 128 && NT == 1 ? 2 : 1;  // an SM
   static constexpr int KP = D * E / 64;   // 16-byte pieces of a key row a lane (four lanes a row)
   static constexpr int VB = D * E >= 128 ? 16 : 8;  // bytes of a value piece (eight lanes a row)
   static constexpr int VP = D * E / (8 * VB);
   static constexpr int kHalf = 16 * D * E;  // a tile's keys
   static constexpr int kScales = TYPE == kCacheBf16 ? 0 : 128;
   static constexpr int kStage = 2 * kHalf + kScales;
-  static constexpr int kMergePass = 4;  // blocks of 16 values merged at a time
-  static constexpr int kMerge = kWarps * kMergePass * 128 * 4;
-  static constexpr int kStats = kWarps * 8 * NT * 2 * 4;
-  static constexpr int kRoom = (232448 - kMerge - kStats) / (kWarps * kStage);
-  static constexpr int kStages = kRoom < 6 ? kRoom : 6;
-  static constexpr int kBytes = kWarps * kStages * kStage + kMerge + kStats;
   static constexpr int MT = D / 16;
+  static constexpr int kItems = NT * MT * 2;       // pairs of values a lane holds of a piece
+  static constexpr int kPiece = kItems * 64;       // values of a piece: 8 NT heads
+  static constexpr int kStats = kWarps * 2 * (8 * NT * 20 + 8);  // of the CTA's pieces
+  static constexpr int kMost = kCtas == 2 ? 115200 : 232448;
+  static constexpr int kRoom = (kMost - kStats) / (kWarps * kStage);
+  static constexpr int kStages = kRoom < 6 ? kRoom : 6;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kBytes = kWarps * kRing + kStats;
+  static_assert(kRing >= kPiece * 4, "a warp's ring holds its last piece");
 };
 
 // A sequence's tiles: [first, first + n), its tokens [lo, hi).
@@ -144,28 +161,30 @@ __device__ __forceinline__ AttnPlace attn_find(const AttnParams& P, int64_t mine
   return r;
 }
 
-// How the tiles are shared out (never by tile where no sequence has more than W: the host launches
-// no join then). kByTile: CTA c takes tiles [c, c + 1) * quota of all; kBySegment: CTA
-// c the segments c, c + grid, ...; kByWarp: each warp its own segments.
+// How the tiles are shared out. A segment is a sequence's tiles for one block of heads.
+//   kByTile     each warp the same number of tiles, of all in one order (sequence, block of heads,
+//               tile): pieces of segments are joined by the CTA, and by the join kernel across CTAs
+//   kBySegment  a CTA for each segment, its warps the same number of tiles
+//   kByWarp     each warp whole segments
+// Costs in tiles of a warp (about 0.5 us). Never by tile where no sequence has more tiles than a CTA
+// has warps: the host launches no join then.
 constexpr int kByTile = 0, kBySegment = 1, kByWarp = 2;
+constexpr int kCostJoin = 8, kCostMerge = 3;
 struct AttnSplit {
   int mode;
-  int64_t quota;
+  int64_t quota;  // by tile: of a warp
 };
 template <int W>
 __device__ __forceinline__ AttnSplit attn_split(const AttnParams& P, int64_t tiles, int most) {
-  const int64_t heads = int64_t(P.cache.heads) * P.blocks;
-  const int64_t all = tiles * heads, segments = heads * P.batch;
   AttnSplit s;
-  s.mode = kByTile;
-  s.quota = max((all + P.grid - 1) / P.grid, int64_t(1));
-  // rounds of a tile a warp: shared by tiles, whole segments a CTA, whole segments a warp
-  const int64_t by_tile = (s.quota + W - 1) / W + 2 * (1 + s.quota * segments / max(all, int64_t(1)));
-  const int64_t per_cta = (segments + P.grid - 1) / P.grid;
-  const int64_t by_segment = per_cta * ((most + W - 1) / W + 2) - 1;
-  const int64_t by_warp = (segments + int64_t(P.grid) * W - 1) / (int64_t(P.grid) * W) * (most + 1);
-  if (by_segment <= by_tile || most <= W) s.mode = kBySegment;
-  if (by_warp <= by_segment && (by_warp <= by_tile || most <= W)) s.mode = kByWarp;
+  const int64_t all = tiles * P.heads, warps = int64_t(P.grid) * W;
+  s.quota = max(fast_div(all + warps - 1, P.by_warps), int64_t(1));
+  const int64_t by_tile = most <= W ? INT64_MAX : s.quota + kCostJoin;
+  const int64_t by_segment =
+      P.segments <= P.grid ? (most + W - 1) / W + kCostMerge : INT64_MAX;
+  const int64_t by_warp = P.warp_rounds == 1 ? most : s.quota + most;
+  s.mode = by_segment <= by_tile ? kBySegment : kByTile;
+  if (by_warp <= min(by_tile, by_segment)) s.mode = kByWarp;
   return s;
 }
 
@@ -235,8 +254,23 @@ __device__ __forceinline__ int attn_value_of(int j, int r) {
   return ((j / per) * 8 + r) * (VB / E) + (j % per) * 2;
 }
 
+__device__ __forceinline__ float attn_lse(float top, float sum) {
+  return sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Two values of a head's row of the output, from sums over all its tokens.
+template <int TYPE, int D>
+__device__ __forceinline__ void attn_store(const AttnParams& P, int b, int head, int block, int r,
+                                           float2 o, float top, float sum) {
+  const int64_t row = int64_t(b) * P.q_heads + head;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *reinterpret_cast<uint32_t*>(P.out + row * D + attn_value_of<TYPE, D>(block, r)) =
+      pack_bf16x2(o.x * inv, o.y * inv);
+  if (P.lse && r == 0 && block == 0) P.lse[row] = attn_lse(top, sum);
+}
+
 template <int TYPE, int D, int NT>
-__global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, 1)
+__global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayout<TYPE, D, NT>::kCtas)
     paged_attention_kernel(const __grid_constant__ AttnParams P) {
   using L = AttnLayout<TYPE, D, NT>;
   constexpr bool QUANT = TYPE != kCacheBf16;
@@ -244,73 +278,88 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, 1)
   constexpr int KS = QUANT ? 4 : 2;  // matrix steps (16 values of a key row) a piece
   extern __shared__ __align__(128) uint8_t attn_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  uint8_t* ring = attn_smem + warp * (S * L::kStage);
-  float* merge = reinterpret_cast<float*>(attn_smem + W * S * L::kStage);
-  float* stats = reinterpret_cast<float*>(attn_smem + W * S * L::kStage + L::kMerge);
+  uint8_t* ring = attn_smem + warp * L::kRing;
+  float2* stats = reinterpret_cast<float2*>(attn_smem + W * L::kRing);  // [warp][first, last][head]
+  float2* total = stats + 2 * W * 8 * NT;                         // of a piece's segment
+  float* factor = reinterpret_cast<float*>(total + 2 * W * 8 * NT);  // of a piece in its segment
+  int2* open = reinterpret_cast<int2*>(factor + 2 * W * 8 * NT);     // [warp][first, last]
   allow_dependents();
   wait_for_producers();
 
   int most;
   int64_t mine, incl;
   const int64_t tiles = attn_scan(P, most, mine, incl);
-  const int heads = P.cache.heads * P.blocks;
+  const int heads = P.heads;
   const AttnSplit split = attn_split<W>(P, tiles, most);
-  const bool by_warp = split.mode == kByWarp, by_tile = split.mode == kByTile;
-  const int64_t segments = int64_t(heads) * P.batch;
-  const int64_t unit = by_warp ? int64_t(blockIdx.x) * W + warp : blockIdx.x;
-  const int64_t units = by_warp ? int64_t(P.grid) * W : P.grid;
-  const int step = by_warp ? 1 : W;
+  const bool by_warp = split.mode == kByWarp;
+  const int unit = blockIdx.x * W + warp, units = P.grid * W;
 
-  // The first segment (its number) and tile of this unit.
-  int64_t seg0 = unit, left0 = INT64_MAX;  // left0: tiles of this CTA's share
-  int pos0 = 0;
-  if (by_tile) {
-    const int64_t t0 = min(split.quota * unit, tiles * heads), t1 = min(t0 + split.quota, tiles * heads);
-    if (t0 >= t1) return;
-    const AttnPlace at = attn_find(P, mine, incl, t0 / heads);
-    const int64_t local = t0 - at.before * heads;
-    const int n = attn_span(P, at.b).n;
-    seg0 = int64_t(at.b) * heads + local / n;
-    pos0 = int(local % n);
-    left0 = t1 - t0;
+  // This warp's share: from tile pos0 of segment (b0, h0) on, `share` tiles (by warp: segment after
+  // segment).
+  int b0 = 0, h0 = 0, pos0 = 0;
+  int64_t share = 0;
+  if (by_warp) {
+    if (unit < P.segments) {
+      b0 = unit / heads;
+      h0 = unit - b0 * heads;
+      share = INT32_MAX;
+    }
+  } else if (split.mode == kBySegment) {
+    if (int(blockIdx.x) < P.segments) {
+      b0 = int(blockIdx.x) / heads;
+      h0 = int(blockIdx.x) - b0 * heads;
+      const int n = attn_span(P, b0).n, q = (n + W - 1) / W;
+      pos0 = min(q * warp, n);
+      share = min(q, n - pos0);
+    }
+  } else {
+    const int64_t t0 = min(split.quota * unit, tiles * heads);
+    share = min(split.quota, tiles * heads - t0);
+    if (share > 0) {
+      const AttnPlace at = attn_find(P, mine, incl, fast_div(t0, P.by_heads));
+      const int n = attn_span(P, at.b).n;
+      const uint32_t local = uint32_t(t0 - at.before * heads);
+      b0 = at.b;
+      h0 = int(local / uint32_t(n));
+      pos0 = int(local - uint32_t(h0) * uint32_t(n));
+    }
   }
-  const int64_t seg_step = by_tile ? 1 : units;
+  // The segment after (b, h): false if there is none.
+  auto next_segment = [&](int& b, int& h) {
+    if (by_warp) {
+      const int64_t seg = int64_t(b) * heads + h + units;
+      if (seg >= P.segments) return false;
+      b = int(seg) / heads;
+      h = int(seg) - b * heads;
+    } else if (++h == heads) {
+      h = 0;
+      ++b;
+    }
+    return b < P.batch;
+  };
 
   // ---- the fetching side: the next tile to copy
-  int64_t f_seg = seg0, f_left = left0;
-  int f_n = 0, f_first = 0, f_lo = 0, f_hi = 0, f_h = 0, f_b = 0;
-  int f_pos = pos0 + (by_warp ? 0 : warp);
-  int f_used = pos0;  // (by tiles: where this segment's part of the share begins)
-  auto f_load = [&]() {
-    f_b = int(f_seg / heads);
-    f_h = int(f_seg - int64_t(f_b) * heads) / P.blocks;
-    const AttnSpan s = attn_span(P, f_b);
-    f_n = s.n;
-    f_first = s.first;
-    f_lo = s.lo;
-    f_hi = s.hi;
-  };
-  bool f_more = f_seg < segments;
-  if (f_more) f_load();
-  // Moves on to a segment that has the tile f_pos.
+  int f_b = b0, f_h = h0, f_pos = pos0, f_end = 0;
+  // Pages of the piece from f_page0 on, one a lane, and the 32 after them: their loads are under way
+  // long before they are needed.
+  int f_page0 = 0, f_pages = 0, f_pages_next = 0;
+  int64_t f_left = share;  // tiles, this piece's included
+  AttnSpan f = {0, 0, 0, 0};
+  bool f_more = share > 0;
+  // The piece at f_pos, or the next that has a tile.
   auto f_settle = [&]() {
-    while (f_more) {
-      const int end = int(min(int64_t(f_n), f_used + f_left));  // of this segment's part
-      if (f_pos < end) return;
-      const int over = by_tile ? f_pos - end : warp;  // the tiles go round the warps
-      if (by_tile) f_left -= end - f_used;
-      f_used = 0;
-      f_seg += seg_step;
-      f_more = f_seg < segments && f_left > 0;
-      if (!f_more) return;
-      f_pos = by_warp ? 0 : over;
-      f_load();
-    }
-  };
-  int f_page = -1;
-  auto f_lookup = [&]() {
-    if (f_more) {
-      f_page = P.table[f_b * P.table_ld + attn_page(P, f_first + f_pos)];
+    for (; f_more; f_pos = 0) {
+      f = attn_span(P, f_b);
+      f_end = int(min(int64_t(f.n), f_pos + f_left));
+      if (f_pos < f_end) {
+        const int32_t* table = P.table + f_b * P.table_ld;
+        const int last = attn_page(P, f.first + f_end - 1);
+        f_page0 = attn_page(P, f.first + f_pos);
+        f_pages = table[min(f_page0 + lane, last)];
+        if (f_page0 + 32 <= last) f_pages_next = table[min(f_page0 + 32 + lane, last)];
+        break;
+      }
+      f_more = next_segment(f_b, f_h);
     }
   };
   uint32_t bad = 0;  // which of the tiles under way have no page, the newest in bit 0
@@ -318,16 +367,24 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, 1)
   auto fetch = [&]() {
     bad <<= 1;
     if (f_more) {
-      const int tile = f_first + f_pos;
-      const int in_page = tile - attn_page(P, tile) * P.page_tiles;
+      const int tile = f.first + f_pos;
+      const int nth = attn_page(P, tile), in_page = tile - nth * P.page_tiles;
+      if (nth == f_page0 + 32) {
+        f_page0 = nth;
+        f_pages = f_pages_next;
+        const int last = attn_page(P, f.first + f_end - 1);
+        if (nth + 32 <= last)
+          f_pages_next = P.table[f_b * P.table_ld + min(nth + 32 + lane, last)];
+      }
+      const int f_page = __shfl_sync(0xffffffffu, f_pages, nth - f_page0);
       const bool fine = f_page >= 0 && f_page < P.cache.pages;
       if (!fine) {
         bad |= 1;
         if (lane == 0) report_device_error(kDevErrBadIndex);
       }
       const int64_t page = fine ? f_page : 0;
-      const int lo = fine ? f_lo - tile * 16 : 16, hi = fine ? f_hi - tile * 16 : 0;
-      const int64_t row = int64_t(f_h) * P.cache.page_size + in_page * 16;
+      const int lo = fine ? f.lo - tile * 16 : 16, hi = fine ? f.hi - tile * 16 : 0;
+      const int64_t row = int64_t(f_h / P.blocks) * P.cache.page_size + in_page * 16;
       const uint32_t dst = smem_addr(ring + fs * L::kStage);
       const uint8_t* k = P.cache.k + page * P.cache.k_stride + row * (D * E);
       const uint8_t* v = P.cache.v + page * P.cache.v_stride + row * (D * E);
@@ -354,31 +411,54 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, 1)
                                : P.cache.v_scale + page * P.cache.vs_stride;
         cp_async_if<4>(dst + 2 * L::kHalf + (c * 8 + r) * 4, s + row + t, t >= lo && t < hi);
       }
-      f_pos += step;
-      f_settle();
-      f_lookup();
+      if (!by_warp) f_more = --f_left > 0;
+      if (++f_pos == f_end && f_more) {
+        f_more = next_segment(f_b, f_h);
+        f_pos = 0;
+        f_settle();
+      }
     }
     cp_async_commit();
     fs = fs + 1 == S ? 0 : fs + 1;
   };
+  // The part of a segment's queries that a lane holds, as it lies in memory. (The first segment's is
+  // asked for before the tiles, so that it does not arrive behind them.)
+  uint4 qx[NT][KP * KS / 2];
+  auto load_q = [&](int b, int hb) {
+    const int h = hb / P.blocks, block = hb - h * P.blocks;
+    const int live = min(8 * NT, P.group - block * 8 * NT);
+    const uint16_t* q = P.q + b * P.q_ld + int64_t(h * P.group + block * 8 * NT) * D;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int n = j * 8 + r;
+      const uint4* row = reinterpret_cast<const uint4*>(q + n * D);
+#pragma unroll
+      for (int p = 0; p < KP; ++p)
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i)
+          qx[j][p * (KS / 2) + i] =
+              n < live ? row[(p * 4 + c) * (KS / 2) + i] : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (share > 0) load_q(b0, h0);
   f_settle();
-  f_lookup();
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) fetch();
 
   // ---- the computing side
   int cs = 0;
-  int turn = 0;  // (by tiles: the warp that takes the segment's first tile)
-  int64_t left = left0;
-  for (int64_t seg = seg0; seg < segments && left > 0; seg += seg_step) {
-    const int b = int(seg / heads), hb = int(seg - int64_t(b) * heads);
-    const int h = hb / P.blocks, block = hb - h * P.blocks;
+  int64_t left = share;
+  int2 open_first = {-1, 0}, open_last = {-1, 0};  // pieces: segment, whether it starts (1), ends (2)
+  bool more = share > 0;
+  for (int b = b0, hb = h0, begin = pos0; more; begin = 0, more = left > 0 && next_segment(b, hb)) {
+    if (b != b0 || hb != h0) load_q(b, hb);
     const AttnSpan span = attn_span(P, b);
-    const int begin = seg == seg0 ? pos0 : 0;
     const int end = int(min(int64_t(span.n), begin + left));
-    if (by_tile && span.n == 0) continue;
-    const int count = end - begin;
-    left -= by_tile ? count : 0;
+    if (!by_warp) {
+      if (span.n == 0) continue;
+      left -= end - begin;
+    }
+    const int h = hb / P.blocks, block = hb - h * P.blocks;
     const int head0 = h * P.group + block * 8 * NT;          // first query head of the block
     const int live = min(8 * NT, P.group - block * 8 * NT);  // query heads in it
 
@@ -387,14 +467,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, 1)
     float fac[NT][2];  // logits in log2 units, for the lane's two heads
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int n = j * 8 + r;
-      const uint4* row = reinterpret_cast<const uint4*>(P.q + b * P.q_ld + int64_t(head0 + n) * D);
-      uint4 x[KP * KS / 2];
-#pragma unroll
-      for (int p = 0; p < KP; ++p)
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i)
-          x[p * (KS / 2) + i] = n < live ? row[(p * 4 + c) * (KS / 2) + i] : make_uint4(0, 0, 0, 0);
+      const uint4* x = qx[j];
       if (!QUANT) {
 #pragma unroll
         for (int i = 0; i < KP * KS / 2; ++i) {
@@ -439,8 +512,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, 1)
       for (int x = 0; x < 2; ++x) m[j][x] = kAttnNone, l[j][x] = 0.0f, kf[j][x] = 0x1p100f;
     }
 
-    const int start = by_warp ? begin : begin + ((warp - turn) & (W - 1));
-    for (int pos = start; pos < end; pos += step) {
+    for (int pos = begin; pos < end; ++pos) {
       __syncwarp();  // (the stage that fetch() overwrites has been read by all lanes)
       fetch();
       cp_async_wait<S - 1>();
@@ -618,132 +690,232 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, 1)
           for (int i = 0; i < MT; ++i) o[j][i][x] *= inv, o[j][i][x + 2] *= inv;
         }
       }
-    if (by_warp) {
+    if (begin == 0 && end == span.n) {  // a whole segment
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int n = j * 8 + 2 * c + x;
           if (n >= live) continue;
-          const int64_t row = int64_t(b) * P.q_heads + head0 + n;
-          const float inv = l[j][x] == 0.0f ? 0.0f : 1.0f / l[j][x];
 #pragma unroll
           for (int i = 0; i < MT; ++i)
-            *reinterpret_cast<uint32_t*>(P.out + row * D + attn_value_of<TYPE, D>(i, r)) =
-                pack_bf16x2(o[j][i][x] * inv, o[j][i][x + 2] * inv);
-          if (P.lse && r == 0)
-            P.lse[row] = l[j][x] == 0.0f ? -INFINITY : (m[j][x] + log2f(l[j][x])) * 0.6931471805599453f;
+            attn_store<TYPE, D>(P, b, head0 + n, i, r, make_float2(o[j][i][x], o[j][i][x + 2]),
+                                m[j][x], l[j][x]);
         }
       continue;
     }
-    // ---- the CTA's sums: its warps' joined, 64 values of the head at a time
-    if (r == 0) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float* at = stats + (warp * 8 * NT + j * 8 + 2 * c + x) * 2;
-          at[0] = m[j][x];
-          at[1] = l[j][x];
-        }
+    // A piece: the warp's last one stays in its ring, an earlier one (there can be one, its first)
+    // waits in the workspace.
+    const bool last = left <= 0;
+    float2* to = last ? reinterpret_cast<float2*>(ring)
+                      : reinterpret_cast<float2*>(P.part_o + int64_t(unit) * L::kPiece);
+    if (last) {
+      cp_async_wait<0>();
+      __syncwarp();  // (all lanes have read the ring)
     }
-    const bool whole = begin == 0 && end == span.n;
-    const int slot = 2 * blockIdx.x + (seg == seg0 ? 0 : 1);
-    constexpr int BP = L::kMergePass;
+    const int2 what = make_int2(b * heads + hb, (begin == 0 ? 1 : 0) | (end == span.n ? 2 : 0));
+    if (last) open_last = what; else open_first = what;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i0 = 0; i0 < MT; i0 += BP) {
+      for (int x = 0; x < 2; ++x) {
+        if (r == 0)
+          stats[(warp * 2 + last) * (8 * NT) + j * 8 + 2 * c + x] = make_float2(m[j][x], l[j][x]);
 #pragma unroll
-        for (int i = 0; i < BP; ++i)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            merge[((warp * BP + i) * 4 + x) * 32 + lane] = o[j][i0 + i][x];
-        __syncthreads();
-        for (int e = threadIdx.x; e < BP * 64; e += W * 32) {
-          const int ln = e & 31, x = (e >> 5) & 1, i = e >> 6;
-          const int n = j * 8 + 2 * (ln & 3) + x;
-          if (n < live) {
-            float top = kAttnNone;
-#pragma unroll
-            for (int v = 0; v < W; ++v) top = fmaxf(top, stats[(v * 8 * NT + n) * 2]);
-            float sum = 0.0f, a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-            for (int v = 0; v < W; ++v) {
-              const float f = ex2(stats[(v * 8 * NT + n) * 2] - top);
-              sum += f * stats[(v * 8 * NT + n) * 2 + 1];
-              a0 += f * merge[((v * BP + i) * 4 + x) * 32 + ln];
-              a1 += f * merge[((v * BP + i) * 4 + x + 2) * 32 + ln];
-            }
-            const int d = attn_value_of<TYPE, D>(i0 + i, ln >> 2);
-            const bool first = i0 == 0 && i == 0 && (ln >> 2) == 0;
-            if (whole) {
-              const int64_t row = int64_t(b) * P.q_heads + head0 + n;
-              const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-              *reinterpret_cast<uint32_t*>(P.out + row * D + d) = pack_bf16x2(a0 * inv, a1 * inv);
-              if (P.lse && first)
-                P.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-            } else {
-              const int64_t row = int64_t(slot) * (8 * NT) + n;
-              *reinterpret_cast<float2*>(P.part_o + row * D + d) = make_float2(a0, a1);
-              if (first) P.part_ml[2 * row] = top, P.part_ml[2 * row + 1] = sum;
-            }
-          }
-        }
-        __syncthreads();
+        for (int i = 0; i < MT; ++i)
+          to[((j * MT + i) * 2 + x) * 32 + lane] = make_float2(o[j][i][x], o[j][i][x + 2]);
       }
-    if (by_tile) turn = (turn + count) & (W - 1);
   }
   cp_async_wait<0>();
+  if (by_warp) return;
+
+  // ---- the CTA's pieces: those of a segment follow each other (warp 0's first, its last, warp 1's
+  // first, ...), only its last can be a warp's first
+  if (lane == 0) open[2 * warp] = open_first, open[2 * warp + 1] = open_last;
+  __syncthreads();
+  // a thread for each piece and head: the segment's maximum and sum, the piece's factor
+  for (int e = threadIdx.x; e < 2 * W * 8 * NT; e += W * 32) {
+    const int p = e / (8 * NT), n = e % (8 * NT), seg = open[p].x;
+    float top = kAttnNone, sum = 0.0f;
+    if (seg >= 0) {
+      float2 ml[2 * W];
+#pragma unroll
+      for (int q = 0; q < 2 * W; ++q)
+        ml[q] = open[q].x == seg ? stats[q * (8 * NT) + n] : make_float2(kAttnNone, 0.0f);
+#pragma unroll
+      for (int q = 0; q < 2 * W; ++q) top = fmaxf(top, ml[q].x);
+#pragma unroll
+      for (int q = 0; q < 2 * W; ++q) sum += ex2(ml[q].x - top) * ml[q].y;
+      factor[e] = ex2(stats[e].x - top);
+      total[e] = make_float2(top, sum);
+    }
+  }
+  __syncthreads();
+  for (int p0 = 0, seen = -1; p0 < 2 * W; ++p0) {
+    const int2 first = open[p0];
+    if (first.x < 0 || first.x == seen) continue;
+    seen = first.x;
+    const int b = seen / heads, hb = seen - b * heads;
+    const int h = hb / P.blocks, block = hb - h * P.blocks;
+    const int live = min(8 * NT, P.group - block * 8 * NT);
+    int tail = -1, ends = 0;  // its last piece where that is a warp's first
+#pragma unroll
+    for (int q = 0; q < 2 * W; ++q)
+      if (open[q].x == seen) {
+        ends = open[q].y & 2;
+        if (q % 2 == 0) tail = q;
+      }
+    const bool starts = first.y & 1, whole = starts && ends;
+    const int slot = 2 * blockIdx.x + starts;  // where it goes on in other CTAs
+#pragma unroll
+    for (int i0 = 0; i0 < L::kItems / W; ++i0) {
+      const int i = i0 * W + warp, n = (i / (2 * MT)) * 8 + 2 * c + (i & 1);
+      if (n >= live) continue;
+      float2 acc = make_float2(0.0f, 0.0f);
+      if (tail >= 0) {
+        const float2 v = reinterpret_cast<const float2*>(
+            P.part_o + (int64_t(blockIdx.x) * W + (tail >> 1)) * L::kPiece)[i * 32 + lane];
+        const float f = factor[tail * (8 * NT) + n];
+        acc = make_float2(f * v.x, f * v.y);
+      }
+#pragma unroll
+      for (int q = 1; q < 2 * W; q += 2)
+        if (open[q].x == seen) {
+          const float2 v = reinterpret_cast<const float2*>(attn_smem + (q >> 1) * L::kRing)[i * 32 + lane];
+          const float f = factor[q * (8 * NT) + n];
+          acc.x += f * v.x;
+          acc.y += f * v.y;
+        }
+      const float2 ml = total[p0 * (8 * NT) + n];
+      if (whole) {
+        attn_store<TYPE, D>(P, b, h * P.group + block * 8 * NT + n, (i >> 1) % MT, r, acc, ml.x, ml.y);
+      } else {
+        reinterpret_cast<float2*>(P.part_o + int64_t(units + slot) * L::kPiece)[i * 32 + lane] = acc;
+        if (r == 0 && ((i >> 1) % MT) == 0) P.part_ml[slot * (8 * NT) + n] = ml;
+      }
+    }
+  }
+  // sequences without tokens: no warp has them
+  for (int64_t seg = unit; seg < P.segments; seg += units) {
+    const int b = int(seg) / heads, hb = int(seg) - b * heads;
+    if (attn_span(P, b).n > 0) continue;
+    const int h = hb / P.blocks, block = hb - h * P.blocks;
+    for (int n = 0; n < min(8 * NT, P.group - block * 8 * NT); ++n) {
+      const int64_t row = int64_t(b) * P.q_heads + h * P.group + block * 8 * NT + n;
+      for (int i = lane; i < D / 2; i += 32) reinterpret_cast<uint32_t*>(P.out + row * D)[i] = 0u;
+      if (P.lse && lane == 0) P.lse[row] = -INFINITY;
+    }
+  }
 }
 
-// Joins the pieces of segments that several CTAs shared: a CTA for each segment and query head.
-template <int D, int W, int NT>
-__global__ void __launch_bounds__(D / 2) attn_join_kernel(const __grid_constant__ AttnParams P) {
+// Joins the pieces of segments that several CTAs shared. A CTA for each segment, or, where there are
+// more of them, for each CTA of the attention kernel and the segment that goes on behind it; its warps
+// take the pieces in turn, all loads of a warp's pieces under way at once.
+constexpr int kJoinWarps = 4, kJoinItems = 4, kJoinAhead = 6;
+
+template <int TYPE, int D, int NT>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams P) {
+  using L = AttnLayout<TYPE, D, NT>;
+  __shared__ float2 sums[kJoinWarps][kJoinItems][32];
+  __shared__ float2 stats[kJoinWarps][kJoinItems][4];
   wait_for_producers();
   allow_dependents();
   int most;
   int64_t mine, incl;
   const int64_t tiles = attn_scan(P, most, mine, incl);
-  const AttnSplit split = attn_split<W>(P, tiles, most);
+  const AttnSplit split = attn_split<L::kWarps>(P, tiles, most);
   if (split.mode != kByTile) return;
-  const int heads = P.cache.heads * P.blocks;
-  const int b = blockIdx.x / heads, hb = blockIdx.x - b * heads;
-  const int h = hb / P.blocks, block = hb - h * P.blocks, n = blockIdx.y;
-  if (n >= min(8 * NT, P.group - block * 8 * NT)) return;
-  // tiles before sequence b
-  const int per = (P.batch + 31) >> 5, owner = b / per;
-  int64_t before = __shfl_sync(0xffffffffu, incl - mine, owner);
-  for (int i = owner * per; i < b; ++i) before += attn_span(P, i).n;
-  const int count = attn_span(P, b).n;
-  const int64_t row = int64_t(b) * P.q_heads + h * P.group + block * 8 * NT + n;
-  if (count == 0) {  // no token: no CTA has it
-    *reinterpret_cast<uint32_t*>(P.out + row * D + 2 * threadIdx.x) = 0u;
-    if (P.lse && threadIdx.x == 0) P.lse[row] = -INFINITY;
-    return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int heads = P.heads;
+  const int64_t quota = split.quota * L::kWarps;  // of a CTA
+  int b, hb, count;
+  int64_t s0;  // the segment's first tile
+  if (P.segments <= P.grid) {
+    b = int(blockIdx.x) / heads;
+    hb = int(blockIdx.x) - b * heads;
+    const int per = (P.batch + 31) >> 5, owner = b / per;
+    int64_t before = __shfl_sync(0xffffffffu, incl - mine, owner);
+    for (int i = owner * per; i < b; ++i) before += attn_span(P, i).n;
+    count = attn_span(P, b).n;
+    if (count == 0) return;
+    s0 = before * heads + int64_t(hb) * count;
+  } else {
+    const int64_t t = (int64_t(blockIdx.x) + 1) * quota - 1;  // the CTA's last tile
+    if (t >= tiles * heads) return;
+    const AttnPlace at = attn_find(P, mine, incl, fast_div(t, P.by_heads));
+    count = attn_span(P, at.b).n;
+    const uint32_t local = uint32_t(t - at.before * heads);
+    b = at.b;
+    hb = int(local / uint32_t(count));
+    s0 = at.before * heads + int64_t(hb) * count;
+    if (s0 < int64_t(blockIdx.x) * quota) return;  // began in an earlier CTA
   }
-  const int64_t s0 = before * heads + int64_t(hb) * count, s1 = s0 + count;
-  const int64_t c0 = s0 / split.quota, c1 = (s1 - 1) / split.quota;
-  if (c0 == c1) return;  // whole
-  auto slot = [&](int64_t cta) {  // 0 where the piece is its CTA's first
-    const bool first = cta > c0 || s0 == c0 * split.quota;
-    return (2 * cta + (first ? 0 : 1)) * (8 * NT) + n;
-  };
-  float top = kAttnNone;
-  for (int64_t i = c0; i <= c1; ++i) top = fmaxf(top, P.part_ml[2 * slot(i)]);
-  float sum = 0.0f, a0 = 0.0f, a1 = 0.0f;
-  for (int64_t i = c0; i <= c1; ++i) {
-    const int64_t at = slot(i);
-    const float f = ex2(P.part_ml[2 * at] - top);
-    const float2 v = *reinterpret_cast<const float2*>(P.part_o + at * D + 2 * threadIdx.x);
-    sum += f * P.part_ml[2 * at + 1];
-    a0 += f * v.x;
-    a1 += f * v.y;
+  const int c0 = int(s0 / quota), pieces = int((s0 + count - 1) / quota) - c0 + 1;
+  if (pieces == 1) return;
+  const int h = hb / P.blocks, block = hb - h * P.blocks;
+  const int live = min(8 * NT, P.group - block * 8 * NT);
+  const int units = P.grid * L::kWarps, item0 = blockIdx.y * kJoinItems;
+  float top[kJoinItems], sum[kJoinItems];
+  float2 acc[kJoinItems];
+#pragma unroll
+  for (int i = 0; i < kJoinItems; ++i) top[i] = kAttnNone, sum[i] = 0.0f, acc[i] = make_float2(0.0f, 0.0f);
+  for (int q = warp; q < pieces; q += kJoinWarps * kJoinAhead) {
+    float2 ml[kJoinAhead][kJoinItems], v[kJoinAhead][kJoinItems];
+#pragma unroll
+    for (int a = 0; a < kJoinAhead; ++a)
+#pragma unroll
+      for (int i = 0; i < kJoinItems; ++i) {
+        const int p = q + a * kJoinWarps, it = item0 + i;
+        const int n = (it / (2 * L::MT)) * 8 + 2 * c + (it & 1);
+        ml[a][i] = make_float2(kAttnNone, 0.0f);
+        v[a][i] = make_float2(0.0f, 0.0f);
+        if (p < pieces && n < live) {
+          const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);  // the first piece is its CTA's last
+          ml[a][i] = P.part_ml[slot * (8 * NT) + n];
+          v[a][i] = reinterpret_cast<const float2*>(P.part_o + int64_t(units + slot) * L::kPiece)[it * 32 + lane];
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < kJoinItems; ++i) {
+      float t = top[i];
+#pragma unroll
+      for (int a = 0; a < kJoinAhead; ++a) t = fmaxf(t, ml[a][i].x);
+      const float f0 = ex2(top[i] - t);
+      top[i] = t;
+      sum[i] *= f0;
+      acc[i].x *= f0;
+      acc[i].y *= f0;
+#pragma unroll
+      for (int a = 0; a < kJoinAhead; ++a) {
+        const float f = ex2(ml[a][i].x - t);
+        sum[i] += f * ml[a][i].y;
+        acc[i].x += f * v[a][i].x;
+        acc[i].y += f * v[a][i].y;
+      }
+    }
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  *reinterpret_cast<uint32_t*>(P.out + row * D + 2 * threadIdx.x) = pack_bf16x2(a0 * inv, a1 * inv);
-  if (P.lse && threadIdx.x == 0)
-    P.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+#pragma unroll
+  for (int i = 0; i < kJoinItems; ++i) {
+    sums[warp][i][lane] = acc[i];
+    if (r == 0) stats[warp][i][c] = make_float2(top[i], sum[i]);
+  }
+  __syncthreads();
+  for (int i = warp; i < kJoinItems; i += kJoinWarps) {
+    const int it = item0 + i, n = (it / (2 * L::MT)) * 8 + 2 * c + (it & 1);
+    if (n >= live) continue;
+    float t = kAttnNone, s = 0.0f;
+    float2 a = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) t = fmaxf(t, stats[w][i][c].x);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float f = ex2(stats[w][i][c].x - t);
+      s += f * stats[w][i][c].y;
+      a.x += f * sums[w][i][lane].x;
+      a.y += f * sums[w][i][lane].y;
+    }
+    attn_store<TYPE, D>(P, b, h * P.group + block * 8 * NT + n, (it >> 1) % L::MT, r, a, t, s);
+  }
 }
 
 }  // namespace fp8q
