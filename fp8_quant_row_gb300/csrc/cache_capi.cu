@@ -137,12 +137,22 @@ fp8q_status launch_heads(fp8q::HeadsParams p, const DeviceInfo& dev, cudaStream_
   int bps = 0;
   const fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), fp8q::kHeadsThreads, 0, &bps);
   if (st != FP8Q_OK) return st;
-  const int64_t resident = int64_t(dev.sms) * std::max(bps, 1) * kWarps;
+  const int64_t resident = int64_t(dev.sms) * std::max(bps, 1);
   const int steps = (p.q_heads + HPW - 1) / HPW + (CACHE ? 2 : 1) * ((p.kv_heads + HPW - 1) / HPW);
-  // a warp takes a whole token where there are enough of them, so that its angles are formed once
-  p.parts = int(std::min<int64_t>(steps, (resident + p.tokens - 1) / p.tokens));
-  const int64_t units = p.tokens * p.parts;
-  const int64_t grid = std::min<int64_t>((units + kWarps - 1) / kWarps, resident / kWarps);
+  // Tokens a group, by the rounds of groups and a round's length: a warp's steps and about three steps'
+  // time for the angles and the barrier.
+  p.group_tokens = 1;
+  int64_t best = INT64_MAX;
+  for (int t = 1; t <= fp8q::kHeadsTokens; t *= 2) {
+    const int64_t rounds = ((p.tokens + t - 1) / t + resident - 1) / resident;
+    const int64_t cost = rounds * ((steps * t + kWarps - 1) / kWarps + 3);
+    if (cost < best) best = cost, p.group_tokens = t;
+  }
+  // With few tokens, as many CTAs a token as have a step for each warp.
+  p.parts = int(std::max<int64_t>(
+      1, std::min<int64_t>((steps + kWarps - 1) / kWarps, resident / std::min(p.tokens, resident))));
+  const int64_t groups = (p.tokens + p.group_tokens - 1) / p.group_tokens;
+  const int64_t grid = std::min<int64_t>(groups, std::max<int64_t>(resident / p.parts, 1)) * p.parts;
   return launch(fn, dim3(unsigned(grid)), dim3(fp8q::kHeadsThreads), 0, stream, p);
 }
 
@@ -162,8 +172,7 @@ fp8q_status launch_heads_rope(const fp8q::HeadsParams& p, const fp8q_rotary* r, 
                               const DeviceInfo& dev, cudaStream_t stream) {
   if (!r) return launch_heads_type<D, fp8q::kRopeNone>(p, type, dev, stream);
   if (r->interleaved) return launch_heads_type<D, fp8q::kRopePairs>(p, type, dev, stream);
-  if (r->pairs == D / 2) return launch_heads_type<D, fp8q::kRopeHalves>(p, type, dev, stream);
-  return launch_heads_type<D, fp8q::kRopePart>(p, type, dev, stream);
+  return launch_heads_type<D, fp8q::kRopeHalves>(p, type, dev, stream);
 }
 
 // type: of the cache, -1 without one.

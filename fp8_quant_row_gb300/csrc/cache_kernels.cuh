@@ -44,7 +44,7 @@ __device__ __forceinline__ int64_t page_of(int64_t x, uint64_t magic) {
   return int64_t(__umul64hi(uint64_t(x), magic));
 }
 
-constexpr int kRopeNone = 0, kRopeHalves = 1, kRopePairs = 2, kRopePart = 3;
+constexpr int kRopeNone = 0, kRopeHalves = 1, kRopePairs = 2;
 constexpr int kMaxPairs = 128;
 
 struct RopeView {
@@ -70,7 +70,8 @@ struct HeadsParams {
   CacheView cache;
   RopeView rope;
   int64_t tokens;
-  int q_heads, kv_heads, parts;
+  int q_heads, kv_heads;
+  int group_tokens, parts;  // tokens a CTA takes at a time (1, 2, 4, 8), CTAs that share a token
   float eps;
 };
 
@@ -111,58 +112,55 @@ __device__ __forceinline__ int64_t rope_position(const RopeView& r, int axis, in
                 : static_cast<const int32_t*>(r.positions)[at];
 }
 
-__device__ __forceinline__ void rope_angle(const RopeView& r, const RopeTable& t, int pair,
-                                           int64_t token, float& c, float& s) {
-  c = 1.0f;
-  s = 0.0f;
-  if (pair < r.pairs) {
-    const uint64_t turn = uint64_t(rope_position(r, t.axis[pair], token)) * t.step[pair];
-    turn_cos_sin(uint32_t(turn >> 32), c, s);
-  }
+// A copy to shared memory, zeros where `in` is false.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_if(uint32_t dst, const void* src, bool in) {
+  static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "a copy of 4, 8 or 16 bytes");
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
+                 "r"(in ? BYTES : 0)
+                 : "memory");
 }
 
-// Eight bf16 values of a 16-byte chunk as fp32.
-__device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[2 * i] = bf_lo(u[i]), x[2 * i + 1] = bf_hi(u[i]);
+// Eight bf16 values of a 16-byte chunk as fp32 pairs.
+__device__ __forceinline__ void unpack8(uint4 w, f2 (&x)[4]) {
+  x[0] = bf2_to_f2(w.x), x[1] = bf2_to_f2(w.y), x[2] = bf2_to_f2(w.z), x[3] = bf2_to_f2(w.w);
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const f2 (&x)[4]) {
+  return make_uint4(pack_bf16x2(f2_lo(x[0]), f2_hi(x[0])), pack_bf16x2(f2_lo(x[1]), f2_hi(x[1])),
+                    pack_bf16x2(f2_lo(x[2]), f2_hi(x[2])), pack_bf16x2(f2_lo(x[3]), f2_hi(x[3])));
 }
+__device__ __forceinline__ f2 neg2(f2 a) { return f2{a.v ^ 0x8000000080000000ull}; }
 
-template <bool INT8>
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
-  const f2 p[4] = {f2_make(x[0], x[1]), f2_make(x[2], x[3]), f2_make(x[4], x[5]),
-                   f2_make(x[6], x[7])};
-  return rq_codes8<INT8>(p, inv);
-}
-
-// One row of the cache: bf16, or codes and scale. (a, b: the lane's two chunks of the row; u: the
-// lane's place in it; all lanes of the warp take part, `live` ones store.)
+// One row of the cache: bf16, or codes and scale. (a, b: the lane's chunks ca and cb of the row; all
+// lanes of the warp take part, `live` ones store; one lane a row is the `first`.)
 template <int D, int TYPE>
-__device__ __forceinline__ void store_row(const float (&a)[8], const float (&b)[8], int u, bool live,
-                                          uint8_t* row, float* scale) {
-  constexpr int LPH = D / 16;
+__device__ __forceinline__ void store_row(const f2 (&a)[4], const f2 (&b)[4], int ca, int cb,
+                                          bool first, bool live, uint8_t* row, float* scale) {
   if (TYPE == kCacheBf16) {
     if (live) {
-      reinterpret_cast<uint4*>(row)[u] = pack8(a);
-      reinterpret_cast<uint4*>(row)[LPH + u] = pack8(b);
+      reinterpret_cast<uint4*>(row)[ca] = pack8(a);
+      reinterpret_cast<uint4*>(row)[cb] = pack8(b);
     }
     return;
   }
   constexpr bool INT8 = TYPE == kCacheInt8;
   float top = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = absmax3(top, a[j], b[j]);
+  for (int j = 0; j < 4; ++j)
+    top = absmax3(absmax3(top, f2_lo(a[j]), f2_hi(a[j])), f2_lo(b[j]), f2_hi(b[j]));
 #pragma unroll
-  for (int o = 1; o < LPH; o <<= 1) top = absmax3(top, __shfl_xor_sync(0xffffffffu, top, o), 0.0f);
+  for (int o = 1; o < D / 16; o <<= 1)
+    top = absmax3(top, __shfl_xor_sync(0xffffffffu, top, o), 0.0f);
   const float inv = rq_inverse<INT8>(top);
   if (live) {
-    reinterpret_cast<uint2*>(row)[u] = codes8<INT8>(a, inv);
-    reinterpret_cast<uint2*>(row)[LPH + u] = codes8<INT8>(b, inv);
-    if (u == 0) {
+    reinterpret_cast<uint2*>(row)[ca] = rq_codes8<INT8>(a, inv);
+    reinterpret_cast<uint2*>(row)[cb] = rq_codes8<INT8>(b, inv);
+    if (first) {
       float s = top >= kRqTiny ? __fdiv_rn(top, rq_qmax<INT8>()) : 0.0f;
       if (!(top <= 3.402823466e38f)) s = __uint_as_float(0x7FC00000u);
       *scale = s;
@@ -170,32 +168,97 @@ __device__ __forceinline__ void store_row(const float (&a)[8], const float (&b)[
   }
 }
 
-// A unit is a token's share of head steps: steps of 32 / (D / 16) heads, q's first, then k's and
-// v's, `parts` warps taking them in turn. CACHE: k and v go to the cache (else k to k_out).
-constexpr int kHeadsThreads = 256;
+// A CTA takes groups of T tokens, 8 / T warps a token. The group's angles are formed once, a thread
+// each, into one of two buffers (one barrier a group); then each warp takes steps of 32 / (D / 16)
+// heads, q's first, then k's and v's. A step's rows come through a ring of the warp's own (cp.async,
+// each lane the pieces that it reads), two steps ahead of the current one and on into the next group.
+// `parts` CTAs share a token's steps where there are few tokens. CACHE: k and v go to the cache (else
+// k to k_out).
+// A lane's chunks: with rotated halves a pair of chunks `half` apart (of the first 2 half of a row; of
+// the others one from either half of them), so that the pairs (i, i + pairs) lie in one lane for a part
+// of a head too; else one from either half of the row.
+constexpr int kHeadsThreads = 256, kHeadsWarps = 8, kHeadsTokens = 8, kHeadsStages = 3;
 
 template <int D, int ROPE, bool CACHE, int TYPE>
 __global__ void __launch_bounds__(kHeadsThreads) heads_kernel(const __grid_constant__ HeadsParams P) {
-  constexpr int LPH = D / 16, HPW = 32 / LPH;
+  constexpr int LPH = D / 16, HPW = 32 / LPH, PAIRS = D / 2;
   __shared__ RopeTable table;
-  const int lane = threadIdx.x & 31, g = lane / LPH, u = lane % LPH;
+  __shared__ __align__(16) float cos_s[2][ROPE ? kHeadsTokens * PAIRS : 1];
+  __shared__ __align__(16) float sin_s[2][ROPE ? kHeadsTokens * PAIRS : 1];
+  __shared__ uint4 ring_s[kHeadsWarps][kHeadsStages][2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / LPH, u = lane % LPH;
+  const int T = P.group_tokens, warps = kHeadsWarps / T;  // of a token, in this CTA
+  const int mine = warp / warps;                          // this warp's token in the group
   wait_for_producers();
   allow_dependents();
   if (ROPE != kRopeNone) rope_table(table, P.rope);
+  const int pairs = ROPE ? P.rope.pairs : 0;
+  const int half = ROPE == kRopeHalves ? pairs / 8 : LPH;
+  const int ca = u < half ? u : u + half, cb = u < half ? u + half : u + LPH;
   const int q_steps = (P.q_heads + HPW - 1) / HPW, kv_steps = (P.kv_heads + HPW - 1) / HPW;
   const int steps = q_steps + (CACHE ? 2 : 1) * kv_steps;
-  const int64_t units = P.tokens * P.parts;
-  const int64_t stride = int64_t(gridDim.x) * (kHeadsThreads / 32);
-  for (int64_t unit = int64_t(blockIdx.x) * (kHeadsThreads / 32) + (threadIdx.x >> 5); unit < units;
-       unit += stride) {
-    const int64_t token = unit / P.parts;
-    const int part = int(unit - token * P.parts);
+  const int64_t groups = (P.tokens + T - 1) / T;
+  const int step0 = (blockIdx.x % P.parts) * warps + (warp - mine * warps), stride = P.parts * warps;
+  const int grid = gridDim.x / P.parts;
+  // The next step to copy.
+  int64_t f_group = blockIdx.x / P.parts;
+  int f_step = step0, fs = 0;
+  auto fetch = [&]() {
+    const int64_t token = f_group * T + mine;
+    if (f_group < groups && f_step < steps && token < P.tokens) {
+      const int kind = f_step < q_steps ? 0 : f_step < q_steps + kv_steps ? 1 : 2;
+      const int h = (f_step - (kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + kv_steps)) * HPW + g;
+      const bool in = h < (kind == 0 ? P.q_heads : P.kv_heads);
+      const uint16_t* src = kind == 0   ? P.q + token * P.q_ld
+                            : kind == 1 ? P.k + token * P.k_ld
+                                        : P.v + token * P.v_ld;
+      const uint4* row = reinterpret_cast<const uint4*>(src + int64_t(in ? h : 0) * D);
+      cp_async_if<16>(smem_addr(&ring_s[warp][fs][0][lane]), row + ca, in);
+      cp_async_if<16>(smem_addr(&ring_s[warp][fs][1][lane]), row + cb, in);
+      f_step += stride;
+      if (f_step >= steps) f_step = step0, f_group += grid;
+    }
+    cp_async_commit();
+    fs = fs + 1 == kHeadsStages ? 0 : fs + 1;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kHeadsStages - 1; ++i) fetch();
+  int buffer = 0, stage = 0;
+  for (int64_t group = blockIdx.x / P.parts; group < groups; group += grid, buffer ^= 1) {
+    const int64_t token = group * T + mine;
+    const bool exists = token < P.tokens;
+    int64_t slot = 0;
+    if (CACHE && exists) slot = P.slots[token];
+    if constexpr (ROPE != kRopeNone) {
+      const int count = int(min(int64_t(T), P.tokens - group * T)) * pairs;
+      for (int i = threadIdx.x; i < count; i += kHeadsThreads) {
+        const int t = i / pairs, pair = i - t * pairs;
+        const uint64_t turn =
+            uint64_t(rope_position(P.rope, table.axis[pair], group * T + t)) * table.step[pair];
+        turn_cos_sin(uint32_t(turn >> 32), cos_s[buffer][t * PAIRS + pair],
+                     sin_s[buffer][t * PAIRS + pair]);
+      }
+      __syncthreads();
+    }
+    if (!exists) continue;
+    // cos and sin of the lane's pairs, two to a word pair
+    f2 cs[ROPE ? 4 : 1], sn[ROPE ? 4 : 1];
+    if constexpr (ROPE != kRopeNone) {
+      const int p0 = mine * PAIRS + u * (ROPE == kRopeHalves ? 8 : 4);
+      const int p1 = p0 + (ROPE == kRopeHalves ? 4 : D / 4);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float4 c = *reinterpret_cast<const float4*>(&cos_s[buffer][x ? p1 : p0]);
+        const float4 s = *reinterpret_cast<const float4*>(&sin_s[buffer][x ? p1 : p0]);
+        cs[2 * x] = f2_make(c.x, c.y), cs[2 * x + 1] = f2_make(c.z, c.w);
+        sn[2 * x] = f2_make(s.x, s.y), sn[2 * x + 1] = f2_make(s.z, s.w);
+      }
+    }
     // where this token's k and v go
     int64_t page = 0;
     int at = 0;
     bool store = true;
     if (CACHE) {
-      const int64_t slot = P.slots[token];
       store = slot >= 0 && slot < P.cache.pages * P.cache.page_size;
       if (store) {
         page = page_of(slot, P.cache.page_magic);
@@ -204,104 +267,59 @@ __global__ void __launch_bounds__(kHeadsThreads) heads_kernel(const __grid_const
         report_device_error(kDevErrBadIndex);
       }
     }
-    // cos and sin of the lane's pairs: slot 0 chunk a, slot 1 chunk b
-    constexpr int NC = ROPE == kRopePart ? 16 : 8;
-    float cs[NC], sn[NC];
-    if (ROPE == kRopeHalves) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) rope_angle(P.rope, table, u * 8 + j, token, cs[j], sn[j]);
-    } else if (ROPE == kRopePairs) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        rope_angle(P.rope, table, (j < 4 ? 0 : D / 4 - 4) + u * 4 + j, token, cs[j], sn[j]);
-    } else if (ROPE == kRopePart) {
-      // the chunk pairs with another, `half` chunks away; the second of a pair has -s
-      const int half = P.rope.pairs / 8;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int chunk = u + (j < 8 ? 0 : LPH);
-        const int first = chunk < half ? chunk : chunk - half;
-        rope_angle(P.rope, table, chunk < 2 * half ? first * 8 + (j & 7) : kMaxPairs, token, cs[j],
-                   sn[j]);
-        if (chunk < half) sn[j] = -sn[j];
-      }
-    }
-    for (int step = part; step < steps; step += P.parts) {
+    for (int step = step0; step < steps; step += stride) {
       const int kind = step < q_steps ? 0 : step < q_steps + kv_steps ? 1 : 2;
       const int h = (step - (kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + kv_steps)) * HPW + g;
       const bool live = h < (kind == 0 ? P.q_heads : P.kv_heads);
-      const uint16_t* src = kind == 0   ? P.q + token * P.q_ld
-                            : kind == 1 ? P.k + token * P.k_ld
-                                        : P.v + token * P.v_ld;
-      uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
-      if (live) {
-        const uint4* row = reinterpret_cast<const uint4*>(src + int64_t(h) * D);
-        wa = ld_stream(row + u);
-        wb = ld_stream(row + LPH + u);
-      }
-      float a[8], b[8];
-      unpack8(wa, a);
-      unpack8(wb, b);
+      fetch();
+      cp_async_wait<kHeadsStages - 1>();
+      f2 a[4], b[4];
+      unpack8(ring_s[warp][stage][0][lane], a);
+      unpack8(ring_s[warp][stage][1][lane], b);
+      stage = stage + 1 == kHeadsStages ? 0 : stage + 1;
       const uint16_t* weight = kind == 0 ? P.q_weight : P.k_weight;
       if (kind < 2 && weight) {
-        float sum = 0.0f;
+        const uint4 wa = reinterpret_cast<const uint4*>(weight)[ca];
+        const uint4 wb = reinterpret_cast<const uint4*>(weight)[cb];
+        f2 s0 = mul2(a[0], a[0]), s1 = mul2(b[0], b[0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = __fmaf_rn(a[j], a[j], __fmaf_rn(b[j], b[j], sum));
+        for (int j = 1; j < 4; ++j) s0 = fma2(a[j], a[j], s0), s1 = fma2(b[j], b[j], s1);
+        s0 = add2(s0, s1);
+        float sum = f2_lo(s0) + f2_hi(s0);
 #pragma unroll
         for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float r = __frsqrt_rn(__fmaf_rn(sum, 1.0f / D, P.eps));
-        float w[8];
-        unpack8(*reinterpret_cast<const uint4*>(weight + u * 8), w);
+        const f2 rr = f2_make(r, r);
+        f2 w[4];
+        unpack8(wa, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = a[j] * r * w[j];
-        unpack8(*reinterpret_cast<const uint4*>(weight + D / 2 + u * 8), w);
+        for (int j = 0; j < 4; ++j) a[j] = mul2(mul2(a[j], rr), w[j]);
+        unpack8(wb, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = b[j] * r * w[j];
+        for (int j = 0; j < 4; ++j) b[j] = mul2(mul2(b[j], rr), w[j]);
       }
       if (kind < 2) {
-        if (ROPE == kRopeHalves) {
+        if constexpr (ROPE == kRopeHalves) {
+          if (u < half) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float x = a[j], y = b[j];
-            a[j] = x * cs[j] - y * sn[j];
-            b[j] = y * cs[j] + x * sn[j];
+            for (int j = 0; j < 4; ++j) {
+              const f2 x = a[j], y = b[j];
+              a[j] = fma2(y, neg2(sn[j]), mul2(x, cs[j]));
+              b[j] = fma2(x, sn[j], mul2(y, cs[j]));
+            }
           }
-        } else if (ROPE == kRopePairs) {
+        } else if constexpr (ROPE == kRopePairs) {
           // (pairs that are not rotated stay: an infinity beside a zero sine would not)
-          const bool all = P.rope.pairs == D / 2;
+          const bool all = pairs == PAIRS;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float x = a[2 * j], y = a[2 * j + 1];
-            if (all || u * 4 + j < P.rope.pairs) {
-              a[2 * j] = x * cs[j] - y * sn[j];
-              a[2 * j + 1] = y * cs[j] + x * sn[j];
-            }
-            const float z = b[2 * j], w = b[2 * j + 1];
-            if (all || D / 4 + u * 4 + j < P.rope.pairs) {
-              b[2 * j] = z * cs[4 + j] - w * sn[4 + j];
-              b[2 * j + 1] = w * cs[4 + j] + z * sn[4 + j];
-            }
-          }
-        } else if (ROPE == kRopePart) {
-          const int half = P.rope.pairs / 8;
-          const int ya = u < half ? u + half : u < 2 * half ? u - half : u;
-          const int xb = u + LPH;
-          const int yb = xb < half ? xb + half : xb < 2 * half ? xb - half : xb;
-          float oa[8], ob[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float pa0 = __shfl_sync(0xffffffffu, a[j], ya % LPH, LPH);
-            const float pa1 = __shfl_sync(0xffffffffu, b[j], ya % LPH, LPH);
-            const float pb0 = __shfl_sync(0xffffffffu, a[j], yb % LPH, LPH);
-            const float pb1 = __shfl_sync(0xffffffffu, b[j], yb % LPH, LPH);
-            oa[j] = a[j] * cs[j] + (ya < LPH ? pa0 : pa1) * sn[j];
-            ob[j] = b[j] * cs[8 + j] + (yb < LPH ? pb0 : pb1) * sn[8 + j];
-          }
-          // a chunk that is not rotated stays as it is (an infinity beside a zero sine would not)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (u < 2 * half) a[j] = oa[j];
-            if (xb < 2 * half) b[j] = ob[j];
+            const float c0 = (j & 1) ? f2_hi(cs[j / 2]) : f2_lo(cs[j / 2]);
+            const float s0 = (j & 1) ? f2_hi(sn[j / 2]) : f2_lo(sn[j / 2]);
+            const float c1 = (j & 1) ? f2_hi(cs[2 + j / 2]) : f2_lo(cs[2 + j / 2]);
+            const float s1 = (j & 1) ? f2_hi(sn[2 + j / 2]) : f2_lo(sn[2 + j / 2]);
+            const float x = f2_lo(a[j]), y = f2_hi(a[j]), z = f2_lo(b[j]), w = f2_hi(b[j]);
+            if (all || u * 4 + j < pairs) a[j] = f2_make(x * c0 - y * s0, y * c0 + x * s0);
+            if (all || D / 4 + u * 4 + j < pairs) b[j] = f2_make(z * c1 - w * s1, w * c1 + z * s1);
           }
         }
       }
@@ -309,8 +327,8 @@ __global__ void __launch_bounds__(kHeadsThreads) heads_kernel(const __grid_const
         uint16_t* dst = kind == 0 ? P.q_out + token * P.q_out_ld : P.k_out + token * P.k_out_ld;
         if (live) {
           uint4* row = reinterpret_cast<uint4*>(dst + int64_t(h) * D);
-          row[u] = pack8(a);
-          row[LPH + u] = pack8(b);
+          row[ca] = pack8(a);
+          row[cb] = pack8(b);
         }
       } else if (CACHE) {
         constexpr int E = TYPE == kCacheBf16 ? 2 : 1;
@@ -319,7 +337,7 @@ __global__ void __launch_bounds__(kHeadsThreads) heads_kernel(const __grid_const
                                   : P.cache.v + page * P.cache.v_stride) + row * (D * E);
         float* scale = kind == 1 ? P.cache.k_scale + page * P.cache.ks_stride + row
                                  : P.cache.v_scale + page * P.cache.vs_stride + row;
-        store_row<D, TYPE>(a, b, u, live && store, dst, scale);
+        store_row<D, TYPE>(a, b, ca, cb, u == 0, live && store, dst, scale);
       }
     }
   }
@@ -366,7 +384,8 @@ __device__ __forceinline__ uint4 dequant8(uint2 w, float s) {
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) x[j] *= s;
-  return pack8(x);
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
 }
 
 // A CTA takes 16 output rows, that is tokens: their places are looked up once, then each lane copies

@@ -190,19 +190,6 @@ __device__ __forceinline__ AttnSplit attn_split(const AttnParams& P, int64_t til
 
 // ------------------------------------------------------------------------------------------
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async_if(uint32_t dst, const void* src, bool in) {
-  static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "a copy of 4, 8 or 16 bytes");
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 16 : 0)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
-                 "r"(in ? BYTES : 0)
-                 : "memory");
-}
-
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
