@@ -96,14 +96,10 @@ struct RopeTable {
   int axis[kMaxPairs];
 };
 
-__device__ __forceinline__ void rope_table(RopeTable& t, const RopeView& r) {
-  for (int i = threadIdx.x; i < r.pairs; i += blockDim.x) {
-    double turns = r.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
-    turns -= rint(turns);
-    t.step[i] = uint64_t(__double2ll_rn(turns * 18446744073709551616.0));
-    t.axis[i] = r.axis ? min(max(r.axis[i], 0), r.axes - 1) : 0;
-  }
-  __syncthreads();
+__device__ __forceinline__ uint64_t rope_step(double inv_freq) {
+  double turns = inv_freq * 0.15915494309189535;  // 1 / (2 pi)
+  turns -= rint(turns);
+  return uint64_t(__double2ll_rn(turns * 18446744073709551616.0));
 }
 
 __device__ __forceinline__ int64_t rope_position(const RopeView& r, int axis, int64_t token) {
@@ -177,21 +173,25 @@ __device__ __forceinline__ void store_row(const f2 (&a)[4], const f2 (&b)[4], in
 // A lane's chunks: with rotated halves a pair of chunks `half` apart (of the first 2 half of a row; of
 // the others one from either half of them), so that the pairs (i, i + pairs) lie in one lane for a part
 // of a head too; else one from either half of the row.
+template <int N>
+struct Kind {
+  static constexpr int value = N;
+};
 constexpr int kHeadsThreads = 256, kHeadsWarps = 8, kHeadsTokens = 8, kHeadsStages = 3;
 
 template <int D, int ROPE, bool CACHE, int TYPE>
-__global__ void __launch_bounds__(kHeadsThreads) heads_kernel(const __grid_constant__ HeadsParams P) {
+__global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_constant__ HeadsParams P) {
   constexpr int LPH = D / 16, HPW = 32 / LPH, PAIRS = D / 2;
   __shared__ RopeTable table;
   __shared__ __align__(16) float cos_s[2][ROPE ? kHeadsTokens * PAIRS : 1];
   __shared__ __align__(16) float sin_s[2][ROPE ? kHeadsTokens * PAIRS : 1];
   __shared__ uint4 ring_s[kHeadsWarps][kHeadsStages][2][32];
+  __shared__ float4 weight_s[2][D / 4];  // q's, k's: values 0-3 of each chunk, then values 4-7
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / LPH, u = lane % LPH;
   const int T = P.group_tokens, warps = kHeadsWarps / T;  // of a token, in this CTA
   const int mine = warp / warps;                          // this warp's token in the group
   wait_for_producers();
   allow_dependents();
-  if (ROPE != kRopeNone) rope_table(table, P.rope);
   const int pairs = ROPE ? P.rope.pairs : 0;
   const int half = ROPE == kRopeHalves ? pairs / 8 : LPH;
   const int ca = u < half ? u : u + half, cb = u < half ? u + half : u + LPH;
@@ -200,29 +200,69 @@ __global__ void __launch_bounds__(kHeadsThreads) heads_kernel(const __grid_const
   const int64_t groups = (P.tokens + T - 1) / T;
   const int step0 = (blockIdx.x % P.parts) * warps + (warp - mine * warps), stride = P.parts * warps;
   const int grid = gridDim.x / P.parts;
-  // The next step to copy.
+  // The next step to copy: its head's row, at strides of `ahead` heads within q, k and v.
+  const int ahead = stride * HPW;
   int64_t f_group = blockIdx.x / P.parts;
-  int f_step = step0, fs = 0;
-  auto fetch = [&]() {
+  int f_step = step0, f_end = 0, f_h = 0, f_heads = 0, fs = 0;
+  const uint16_t *f_src = nullptr, *f_row = nullptr;  // the head's row; some row of the token
+  bool f_more = false;
+  auto f_start = [&]() {
     const int64_t token = f_group * T + mine;
-    if (f_group < groups && f_step < steps && token < P.tokens) {
-      const int kind = f_step < q_steps ? 0 : f_step < q_steps + kv_steps ? 1 : 2;
-      const int h = (f_step - (kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + kv_steps)) * HPW + g;
-      const bool in = h < (kind == 0 ? P.q_heads : P.kv_heads);
-      const uint16_t* src = kind == 0   ? P.q + token * P.q_ld
-                            : kind == 1 ? P.k + token * P.k_ld
-                                        : P.v + token * P.v_ld;
-      const uint4* row = reinterpret_cast<const uint4*>(src + int64_t(in ? h : 0) * D);
+    f_more = f_step < steps && token < P.tokens;
+    if (!f_more) return;
+    const int kind = f_step < q_steps ? 0 : f_step < q_steps + kv_steps ? 1 : 2;
+    const int begin = kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + kv_steps;
+    f_end = kind == 0 ? q_steps : begin + kv_steps;
+    f_heads = kind == 0 ? P.q_heads : P.kv_heads;
+    f_h = (f_step - begin) * HPW + g;
+    f_row = kind == 0 ? P.q + token * P.q_ld : kind == 1 ? P.k + token * P.k_ld : P.v + token * P.v_ld;
+    f_src = f_row + int64_t(f_h) * D;
+  };
+  auto fetch = [&]() {
+    if (f_more) {
+      const bool in = f_h < f_heads;
+      const uint4* row = reinterpret_cast<const uint4*>(in ? f_src : f_row);
       cp_async_if<16>(smem_addr(&ring_s[warp][fs][0][lane]), row + ca, in);
       cp_async_if<16>(smem_addr(&ring_s[warp][fs][1][lane]), row + cb, in);
       f_step += stride;
-      if (f_step >= steps) f_step = step0, f_group += grid;
+      f_h += ahead;
+      f_src += ahead * D;
+      if (f_step >= f_end) {
+        if (f_step >= steps) f_step = step0, f_group += grid;
+        f_start();
+      }
     }
     cp_async_commit();
     fs = fs + 1 == kHeadsStages ? 0 : fs + 1;
   };
+  f_start();
 #pragma unroll 1
   for (int i = 0; i < kHeadsStages - 1; ++i) fetch();
+
+  // the weights and the rotation's table, all their loads under way at once
+  static_assert(PAIRS <= kHeadsThreads && 2 * D <= 2 * kHeadsThreads, "an entry or two a thread");
+  uint32_t wv[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = threadIdx.x + j * kHeadsThreads;
+    const uint16_t* w = i >= D ? P.k_weight : P.q_weight;
+    if (i < 2 * D && w) wv[j] = w[i % D];
+  }
+  if constexpr (ROPE != kRopeNone) {
+    if (threadIdx.x < pairs) {
+      const int axis = P.rope.axis ? P.rope.axis[threadIdx.x] : 0;
+      table.step[threadIdx.x] = rope_step(P.rope.inv_freq[threadIdx.x]);
+      table.axis[threadIdx.x] = min(max(axis, 0), P.rope.axes - 1);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = threadIdx.x + j * kHeadsThreads, x = i % D;
+    if (i < 2 * D)
+      reinterpret_cast<float*>(weight_s[i / D])[(x & 4) * (D / 8) + (x >> 3) * 4 + (x & 3)] =
+          __uint_as_float(wv[j] << 16);
+  }
+  __syncthreads();
   int buffer = 0, stage = 0;
   for (int64_t group = blockIdx.x / P.parts; group < groups; group += grid, buffer ^= 1) {
     const int64_t token = group * T + mine;
@@ -267,39 +307,54 @@ __global__ void __launch_bounds__(kHeadsThreads) heads_kernel(const __grid_const
         report_device_error(kDevErrBadIndex);
       }
     }
-    for (int step = step0; step < steps; step += stride) {
-      const int kind = step < q_steps ? 0 : step < q_steps + kv_steps ? 1 : 2;
-      const int h = (step - (kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + kv_steps)) * HPW + g;
-      const bool live = h < (kind == 0 ? P.q_heads : P.kv_heads);
-      fetch();
-      cp_async_wait<kHeadsStages - 1>();
-      f2 a[4], b[4];
-      unpack8(ring_s[warp][stage][0][lane], a);
-      unpack8(ring_s[warp][stage][1][lane], b);
-      stage = stage + 1 == kHeadsStages ? 0 : stage + 1;
-      const uint16_t* weight = kind == 0 ? P.q_weight : P.k_weight;
-      if (kind < 2 && weight) {
-        const uint4 wa = reinterpret_cast<const uint4*>(weight)[ca];
-        const uint4 wb = reinterpret_cast<const uint4*>(weight)[cb];
-        f2 s0 = mul2(a[0], a[0]), s1 = mul2(b[0], b[0]);
-#pragma unroll
-        for (int j = 1; j < 4; ++j) s0 = fma2(a[j], a[j], s0), s1 = fma2(b[j], b[j], s1);
-        s0 = add2(s0, s1);
-        float sum = f2_lo(s0) + f2_hi(s0);
-#pragma unroll
-        for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float r = __frsqrt_rn(__fmaf_rn(sum, 1.0f / D, P.eps));
-        const f2 rr = f2_make(r, r);
-        f2 w[4];
-        unpack8(wa, w);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = mul2(mul2(a[j], rr), w[j]);
-        unpack8(wb, w);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = mul2(mul2(b[j], rr), w[j]);
+    int step = step0;
+    // The steps of q, k or v: heads from `h` on.
+    auto run = [&](auto what, int begin, int end, int heads) {
+      constexpr int KIND = decltype(what)::value;
+      constexpr bool TO_CACHE = CACHE && KIND > 0;
+      constexpr int E = TYPE == kCacheBf16 ? 2 : 1;
+      int h = (step - begin) * HPW + g;
+      uint16_t* dst = nullptr;
+      uint8_t* to = nullptr;
+      float* scale = nullptr;
+      if constexpr (TO_CACHE) {
+        const int64_t row = int64_t(h) * P.cache.page_size + at;
+        to = (KIND == 1 ? P.cache.k + page * P.cache.k_stride : P.cache.v + page * P.cache.v_stride) +
+             row * (D * E);
+        scale = KIND == 1 ? P.cache.k_scale + page * P.cache.ks_stride + row
+                          : P.cache.v_scale + page * P.cache.vs_stride + row;
+      } else {
+        dst = (KIND == 0 ? P.q_out + token * P.q_out_ld : P.k_out + token * P.k_out_ld) + int64_t(h) * D;
       }
-      if (kind < 2) {
-        if constexpr (ROPE == kRopeHalves) {
+      const uint4* weight = reinterpret_cast<const uint4*>(KIND == 0 ? P.q_weight : P.k_weight);
+      for (; step < end; step += stride) {
+        fetch();
+        cp_async_wait<kHeadsStages - 1>();
+        f2 a[4], b[4];
+        unpack8(ring_s[warp][stage][0][lane], a);
+        unpack8(ring_s[warp][stage][1][lane], b);
+        stage = stage + 1 == kHeadsStages ? 0 : stage + 1;
+        if (KIND < 2 && weight) {
+          f2 s0 = mul2(a[0], a[0]), s1 = mul2(b[0], b[0]);
+#pragma unroll
+          for (int j = 1; j < 4; ++j) s0 = fma2(a[j], a[j], s0), s1 = fma2(b[j], b[j], s1);
+          s0 = add2(s0, s1);
+          float sum = f2_lo(s0) + f2_hi(s0);
+#pragma unroll
+          for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          const float r = __frsqrt_rn(__fmaf_rn(sum, 1.0f / D, P.eps));
+          const f2 rr = f2_make(r, r);
+          const float4* w = weight_s[KIND & 1];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float4 p = w[x * (D / 8) + ca], q = w[x * (D / 8) + cb];
+            a[2 * x] = mul2(mul2(a[2 * x], rr), f2_make(p.x, p.y));
+            a[2 * x + 1] = mul2(mul2(a[2 * x + 1], rr), f2_make(p.z, p.w));
+            b[2 * x] = mul2(mul2(b[2 * x], rr), f2_make(q.x, q.y));
+            b[2 * x + 1] = mul2(mul2(b[2 * x + 1], rr), f2_make(q.z, q.w));
+          }
+        }
+        if constexpr (KIND < 2 && ROPE == kRopeHalves) {
           if (u < half) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -308,38 +363,43 @@ __global__ void __launch_bounds__(kHeadsThreads) heads_kernel(const __grid_const
               b[j] = fma2(x, sn[j], mul2(y, cs[j]));
             }
           }
-        } else if constexpr (ROPE == kRopePairs) {
-          // (pairs that are not rotated stay: an infinity beside a zero sine would not)
-          const bool all = pairs == PAIRS;
+        } else if constexpr (KIND < 2 && ROPE == kRopePairs) {
+          auto turn = [&](f2 v, int j) {
+            const float c = (j & 1) ? f2_hi(cs[j / 2]) : f2_lo(cs[j / 2]);
+            const float s = (j & 1) ? f2_hi(sn[j / 2]) : f2_lo(sn[j / 2]);
+            const float x = f2_lo(v), y = f2_hi(v);
+            return f2_make(x * c - y * s, y * c + x * s);
+          };
+          if (pairs == PAIRS) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float c0 = (j & 1) ? f2_hi(cs[j / 2]) : f2_lo(cs[j / 2]);
-            const float s0 = (j & 1) ? f2_hi(sn[j / 2]) : f2_lo(sn[j / 2]);
-            const float c1 = (j & 1) ? f2_hi(cs[2 + j / 2]) : f2_lo(cs[2 + j / 2]);
-            const float s1 = (j & 1) ? f2_hi(sn[2 + j / 2]) : f2_lo(sn[2 + j / 2]);
-            const float x = f2_lo(a[j]), y = f2_hi(a[j]), z = f2_lo(b[j]), w = f2_hi(b[j]);
-            if (all || u * 4 + j < pairs) a[j] = f2_make(x * c0 - y * s0, y * c0 + x * s0);
-            if (all || D / 4 + u * 4 + j < pairs) b[j] = f2_make(z * c1 - w * s1, w * c1 + z * s1);
+            for (int j = 0; j < 4; ++j) a[j] = turn(a[j], j), b[j] = turn(b[j], 4 + j);
+          } else {  // pairs that are not rotated stay: an infinity beside a zero sine would not
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (u * 4 + j < pairs) a[j] = turn(a[j], j);
+              if (D / 4 + u * 4 + j < pairs) b[j] = turn(b[j], 4 + j);
+            }
           }
         }
-      }
-      if (kind == 0 || !CACHE) {
-        uint16_t* dst = kind == 0 ? P.q_out + token * P.q_out_ld : P.k_out + token * P.k_out_ld;
-        if (live) {
-          uint4* row = reinterpret_cast<uint4*>(dst + int64_t(h) * D);
-          row[ca] = pack8(a);
-          row[cb] = pack8(b);
+        const bool live = h < heads;
+        if constexpr (TO_CACHE) {
+          store_row<D, TYPE>(a, b, ca, cb, u == 0, live && store, to, scale);
+          to += int64_t(ahead) * P.cache.page_size * (D * E);
+          scale += ahead * P.cache.page_size;
+        } else {
+          if (live) {
+            uint4* row = reinterpret_cast<uint4*>(dst);
+            row[ca] = pack8(a);
+            row[cb] = pack8(b);
+          }
+          dst += ahead * D;
         }
-      } else if (CACHE) {
-        constexpr int E = TYPE == kCacheBf16 ? 2 : 1;
-        const int64_t row = int64_t(h) * P.cache.page_size + at;
-        uint8_t* dst = (kind == 1 ? P.cache.k + page * P.cache.k_stride
-                                  : P.cache.v + page * P.cache.v_stride) + row * (D * E);
-        float* scale = kind == 1 ? P.cache.k_scale + page * P.cache.ks_stride + row
-                                 : P.cache.v_scale + page * P.cache.vs_stride + row;
-        store_row<D, TYPE>(a, b, ca, cb, u == 0, live && store, dst, scale);
+        h += ahead;
       }
-    }
+    };
+    run(Kind<0>(), 0, q_steps, P.q_heads);
+    run(Kind<1>(), q_steps, q_steps + kv_steps, P.kv_heads);
+    if constexpr (CACHE) run(Kind<2>(), q_steps + kv_steps, steps, P.kv_heads);
   }
 }
 
