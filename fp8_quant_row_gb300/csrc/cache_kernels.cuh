@@ -122,6 +122,14 @@ __device__ __forceinline__ void cp_async_if(uint32_t dst, const void* src, bool 
                  : "memory");
 }
 
+__device__ __forceinline__ uint4 lds_words(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+
 // Eight bf16 values of a 16-byte chunk as fp32 pairs.
 __device__ __forceinline__ void unpack8(uint4 w, f2 (&x)[4]) {
   x[0] = bf2_to_f2(w.x), x[1] = bf2_to_f2(w.y), x[2] = bf2_to_f2(w.z), x[3] = bf2_to_f2(w.w);
@@ -173,6 +181,13 @@ __device__ __forceinline__ void store_row(const f2 (&a)[4], const f2 (&b)[4], in
 // A lane's chunks: with rotated halves a pair of chunks `half` apart (of the first 2 half of a row; of
 // the others one from either half of them), so that the pairs (i, i + pairs) lie in one lane for a part
 // of a head too; else one from either half of the row.
+// 1 / sqrt(x): the approximate instruction (2^-22) and one Newton step, within an ulp.
+__device__ __forceinline__ float heads_rsqrt(float x) {
+  float y;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return __fmaf_rn(0.5f * y, __fmaf_rn(-x * y, y, 1.0f), y);
+}
+
 template <int N>
 struct Kind {
   static constexpr int value = N;
@@ -206,6 +221,7 @@ __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_co
   int f_step = step0, f_end = 0, f_h = 0, f_heads = 0, fs = 0;
   const uint16_t *f_src = nullptr, *f_row = nullptr;  // the head's row; some row of the token
   bool f_more = false;
+  const uint32_t ring = smem_addr(&ring_s[warp][0][0][lane]);
   auto f_start = [&]() {
     const int64_t token = f_group * T + mine;
     f_more = f_step < steps && token < P.tokens;
@@ -222,8 +238,8 @@ __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_co
     if (f_more) {
       const bool in = f_h < f_heads;
       const uint4* row = reinterpret_cast<const uint4*>(in ? f_src : f_row);
-      cp_async_if<16>(smem_addr(&ring_s[warp][fs][0][lane]), row + ca, in);
-      cp_async_if<16>(smem_addr(&ring_s[warp][fs][1][lane]), row + cb, in);
+      cp_async_if<16>(ring + fs, row + ca, in);
+      cp_async_if<16>(ring + fs + 512, row + cb, in);
       f_step += stride;
       f_h += ahead;
       f_src += ahead * D;
@@ -233,7 +249,7 @@ __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_co
       }
     }
     cp_async_commit();
-    fs = fs + 1 == kHeadsStages ? 0 : fs + 1;
+    fs = fs == (kHeadsStages - 1) * 1024 ? 0 : fs + 1024;
   };
   f_start();
 #pragma unroll 1
@@ -331,9 +347,9 @@ __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_co
         fetch();
         cp_async_wait<kHeadsStages - 1>();
         f2 a[4], b[4];
-        unpack8(ring_s[warp][stage][0][lane], a);
-        unpack8(ring_s[warp][stage][1][lane], b);
-        stage = stage + 1 == kHeadsStages ? 0 : stage + 1;
+        unpack8(lds_words(ring + stage), a);
+        unpack8(lds_words(ring + stage + 512), b);
+        stage = stage == (kHeadsStages - 1) * 1024 ? 0 : stage + 1024;
         if (KIND < 2 && weight) {
           f2 s0 = mul2(a[0], a[0]), s1 = mul2(b[0], b[0]);
 #pragma unroll
@@ -342,7 +358,7 @@ __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_co
           float sum = f2_lo(s0) + f2_hi(s0);
 #pragma unroll
           for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          const float r = __frsqrt_rn(__fmaf_rn(sum, 1.0f / D, P.eps));
+          const float r = heads_rsqrt(__fmaf_rn(sum, 1.0f / D, P.eps));
           const f2 rr = f2_make(r, r);
           const float4* w = weight_s[KIND & 1];
 #pragma unroll
