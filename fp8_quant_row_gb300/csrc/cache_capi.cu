@@ -255,7 +255,8 @@ fp8q_status check_attention(const fp8q_paged_cache& c, int64_t batch, int64_t q_
   if (batch < 0 || batch > (1 << 20) || q_heads < 1 || q_heads > kMaxHeads * 64 ||
       q_heads % c.heads != 0 || batch * q_heads > INT32_MAX || width < 0 ||
       width * c.page_size >= (int64_t(1) << 30) ||
-      width * (c.page_size / 16) * q_heads > INT32_MAX)  // (tiles of a sequence, all heads)
+      // (tiles of a sequence over all heads, of all sequences, with what the split adds to each)
+      (width * (c.page_size / 16) + 4) * std::max(q_heads, batch) > INT32_MAX)
     return FP8Q_ERR_SHAPE;
   return FP8Q_OK;
 }
@@ -550,6 +551,7 @@ fp8q_status fp8q_paged_attention(void* out, float* lse, const void* q, int64_t q
   p.warp_rounds = int((int64_t(s.segments) + int64_t(s.grid) * s.warps - 1) / (int64_t(s.grid) * s.warps));
   p.by_warps = fast_div_by(int64_t(s.grid) * s.warps);
   p.by_heads = fast_div_by(p.heads);
+  p.by_blocks = fast_div_by(p.blocks);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.page_tiles = int(cache->page_size / 16);
   p.tile_magic = uint32_t(((int64_t(1) << 32) + p.page_tiles - 1) / p.page_tiles);

@@ -122,6 +122,18 @@ __device__ __forceinline__ void cp_async_if(uint32_t dst, const void* src, bool 
                  : "memory");
 }
 
+// The same where `in` is known to hold for ALL.
+template <int BYTES, bool ALL>
+__device__ __forceinline__ void cp_async_part(uint32_t dst, const void* src, bool in) {
+  if (!ALL)
+    cp_async_if<BYTES>(dst, src, in);
+  else if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint4 lds_words(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"

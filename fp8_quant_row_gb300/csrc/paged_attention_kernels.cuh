@@ -54,10 +54,10 @@ struct AttnParams {
   float2* part_ml;
   int batch, width, window;  // width: pages a sequence may have
   int q_heads, group, blocks;  // heads a key/value head; blocks of 8 NT of them
-  int grid;  // CTAs of the attention kernel
+  int grid;             // CTAs of the attention kernel
   int segments, heads;  // heads: blocks of heads a sequence
   int warp_rounds;      // segments a warp, if each warp takes whole ones
-  FastDiv by_warps, by_heads;  // by grid * warps, by heads
+  FastDiv by_warps, by_heads, by_blocks;  // by grid * warps, by heads, by blocks
   float scale_log2;
   uint32_t tile_magic;  // ceil(2^32 / (page_size / 16))
   int page_tiles;
@@ -92,6 +92,11 @@ struct AttnLayout {
 struct AttnSpan {
   int lo, hi, first, n;
 };
+// Where tiles are shared out, a segment counts as so many more: its queries, page lookups and
+// accumulators cost a warp about that (33 sequences of 1 .. 2000 tokens, 8 heads: 38.8 us with 0).
+constexpr int kAttnExtra = 3;
+__device__ __forceinline__ int attn_weight(const AttnSpan& s) { return s.n ? s.n + kAttnExtra : 0; }
+
 __device__ __forceinline__ AttnSpan attn_span(const AttnParams& P, int b) {
   AttnSpan s;
   s.hi = min(max(P.lengths[b], 0), P.width * P.cache.page_size);
@@ -106,85 +111,88 @@ __device__ __forceinline__ int attn_page(const AttnParams& P, int tile) {
   return P.page_tiles == 1 ? tile : int(__umulhi(uint32_t(tile), P.tile_magic));
 }
 
-// The work's split, found by each warp from the lengths: all tiles in one order (sequence, block of
-// heads, tile), an equal share of them for each CTA; or, where the segments (a sequence's tiles for one
-// block of heads) are short, whole segments for each CTA or each warp.
+// The work's split, found by each warp from the lengths (the loops are kept rolled: code that runs
+// once costs the time to fetch it). A segment is a sequence's tiles for one block of heads.
 
-// The sequence that holds tile `at` of a block of heads, and the tiles before it.
-struct AttnPlace {
-  int b;
-  int64_t before;
+// Weighted tiles of a block of heads: over all sequences, those of this lane's sequences and those up
+// to them; the longest's tiles.
+struct AttnScan {
+  int total, mine, incl, most;
 };
-
-// Totals over the sequences; with `want` >= 0 also the sequence that holds that tile.
-__device__ __forceinline__ int64_t attn_scan(const AttnParams& P, int& most, int64_t& mine,
-                                             int64_t& incl) {
+__device__ __forceinline__ AttnScan attn_scan(const AttnParams& P) {
   const int lane = threadIdx.x & 31;
-  const int per = (P.batch + 31) >> 5, b0 = min(lane * per, P.batch), b1 = min(b0 + per, P.batch);
-  mine = 0;
-  most = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int n = attn_span(P, b).n;
-    mine += n;
-    most = max(most, n);
+  const int per = (P.batch + 31) >> 5, b1 = min(lane * per + per, P.batch);
+  AttnScan s = {0, 0, 0, 0};
+#pragma unroll 1
+  for (int b = lane * per; b < b1; ++b) {
+    const AttnSpan x = attn_span(P, b);
+    s.mine += attn_weight(x);
+    s.most = max(s.most, x.n);
   }
-  most = __reduce_max_sync(0xffffffffu, most);
-  incl = mine;
+  s.most = __reduce_max_sync(0xffffffffu, s.most);
+  s.incl = s.mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int v = __shfl_up_sync(0xffffffffu, s.incl, o);
+    if (lane >= o) s.incl += v;
   }
-  return __shfl_sync(0xffffffffu, incl, 31);
+  s.total = __shfl_sync(0xffffffffu, s.incl, 31);
+  return s;
 }
 
-__device__ __forceinline__ AttnPlace attn_find(const AttnParams& P, int64_t mine, int64_t incl,
-                                               int64_t want) {
-  const int per = (P.batch + 31) >> 5;
-  const unsigned has = __ballot_sync(0xffffffffu, want < incl);
+// The sequence that holds the weighted tile `want` (below the total) of a block of heads, and those
+// before it.
+struct AttnPlace {
+  int b, before;
+};
+__device__ __forceinline__ AttnPlace attn_find(const AttnParams& P, const AttnScan& s, int want) {
+  const int owner = __ffs(__ballot_sync(0xffffffffu, want < s.incl)) - 1;
   AttnPlace r;
-  if (has == 0) {  // past the last
-    r.b = P.batch;
-    r.before = __shfl_sync(0xffffffffu, incl, 31);
-    return r;
+  r.before = __shfl_sync(0xffffffffu, s.incl - s.mine, owner);
+  r.b = owner * ((P.batch + 31) >> 5);
+#pragma unroll 1
+  for (;; ++r.b) {  // (ends within the owner's sequences: their sum passes `want`)
+    const int n = attn_weight(attn_span(P, r.b));
+    if (want < r.before + n) return r;
+    r.before += n;
   }
-  const int owner = __ffs(has) - 1;
-  int64_t before = __shfl_sync(0xffffffffu, incl - mine, owner);
-  int b = owner * per;
-  for (;; ++b) {  // (ends within the owner's sequences: their sum passes `want`)
-    const int n = attn_span(P, b).n;
-    if (want < before + n) break;
-    before += n;
-  }
-  r.b = b;
-  r.before = before;
-  return r;
 }
 
-// How the tiles are shared out. A segment is a sequence's tiles for one block of heads.
-//   kByTile     each warp the same number of tiles, of all in one order (sequence, block of heads,
-//               tile): pieces of segments are joined by the CTA, and by the join kernel across CTAs
+// How the tiles are shared out.
+//   kByTile     each warp the same number of weighted tiles, of all in one order (sequence, block of
+//               heads, tile): pieces of segments are joined by the CTA, and by the join kernel across CTAs
 //   kBySegment  a CTA for each segment, its warps the same number of tiles
 //   kByWarp     each warp whole segments
 // Costs in tiles of a warp (about 0.5 us). Never by tile where no sequence has more tiles than a CTA
 // has warps: the host launches no join then.
 constexpr int kByTile = 0, kBySegment = 1, kByWarp = 2;
-constexpr int kCostJoin = 8, kCostMerge = 3;
+constexpr int kCostJoin = 8, kCostMerge = 2;
 struct AttnSplit {
-  int mode;
-  int64_t quota;  // by tile: of a warp
+  int mode, quota;  // quota: by tile, of a warp
 };
 template <int W>
-__device__ __forceinline__ AttnSplit attn_split(const AttnParams& P, int64_t tiles, int most) {
+__device__ __forceinline__ AttnSplit attn_split(const AttnParams& P, const AttnScan& scan) {
   AttnSplit s;
-  const int64_t all = tiles * P.heads, warps = int64_t(P.grid) * W;
-  s.quota = max(fast_div(all + warps - 1, P.by_warps), int64_t(1));
-  const int64_t by_tile = most <= W ? INT64_MAX : s.quota + kCostJoin;
-  const int64_t by_segment =
-      P.segments <= P.grid ? (most + W - 1) / W + kCostMerge : INT64_MAX;
-  const int64_t by_warp = P.warp_rounds == 1 ? most : s.quota + most;
+  s.quota = max(int(fast_div(int64_t(scan.total) * P.heads + (P.grid * W - 1), P.by_warps)), 1);
+  const int by_tile = scan.most <= W ? INT32_MAX : s.quota + kCostJoin;
+  const int by_segment =
+      P.segments <= P.grid ? (scan.most + W - 1) / W + kCostMerge : INT32_MAX;
+  const int by_warp = (P.warp_rounds == 1 ? 0 : s.quota) + scan.most;
   s.mode = by_segment <= by_tile ? kBySegment : kByTile;
-  if (by_warp <= min(by_tile, by_segment)) s.mode = kByWarp;
+  if (by_warp < min(by_tile, by_segment)) s.mode = kByWarp;
+  return s;
+}
+
+// A segment: sequence, key/value head, block of that head's queries.
+struct AttnSegment {
+  int b, h, block;
+};
+__device__ __forceinline__ AttnSegment attn_segment(const AttnParams& P, int seg) {
+  AttnSegment s;
+  s.b = int(fast_div(seg, P.by_heads));
+  const int rest = seg - s.b * P.heads;
+  s.h = int(fast_div(rest, P.by_blocks));
+  s.block = rest - s.h * P.blocks;
   return s;
 }
 
@@ -233,13 +241,17 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   }
 }
 
-// First value (of two) of rows r and r + 8 in block j of O^T, for row r of the lanes.
+// Values of a head in one row of the lanes: runs of `kRun` side by side, blocks j of O^T holding two
+// each (in rows r and r + 8).
 template <int TYPE, int D>
-__device__ __forceinline__ int attn_value_of(int j, int r) {
-  constexpr int E = TYPE == kCacheBf16 ? 2 : 1;
-  constexpr int VB = D * E >= 128 ? 16 : 8, per = VB / E / 2;  // blocks a piece
-  return ((j / per) * 8 + r) * (VB / E) + (j % per) * 2;
-}
+struct AttnValues {
+  static constexpr int E = TYPE == kCacheBf16 ? 2 : 1;
+  static constexpr int kRun = (D * E >= 128 ? 16 : 8) / E;
+  // the first value of block j's two in row r of the lanes
+  static __device__ __forceinline__ int of(int j, int r) {
+    return ((j / (kRun / 2)) * 8 + r) * kRun + (j % (kRun / 2)) * 2;
+  }
+};
 
 __device__ __forceinline__ float attn_lse(float top, float sum) {
   return sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
@@ -247,13 +259,12 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 
 // Two values of a head's row of the output, from sums over all its tokens.
 template <int TYPE, int D>
-__device__ __forceinline__ void attn_store(const AttnParams& P, int b, int head, int block, int r,
-                                           float2 o, float top, float sum) {
-  const int64_t row = int64_t(b) * P.q_heads + head;
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  *reinterpret_cast<uint32_t*>(P.out + row * D + attn_value_of<TYPE, D>(block, r)) =
+__device__ __forceinline__ void attn_store(const AttnParams& P, int64_t row, int block, int r, float2 o,
+                                           float2 ml) {
+  const float inv = ml.y == 0.0f ? 0.0f : __fdividef(1.0f, ml.y);
+  *reinterpret_cast<uint32_t*>(P.out + row * D + AttnValues<TYPE, D>::of(block, r)) =
       pack_bf16x2(o.x * inv, o.y * inv);
-  if (P.lse && r == 0 && block == 0) P.lse[row] = attn_lse(top, sum);
+  if (P.lse && r == 0 && block == 0) P.lse[row] = attn_lse(ml.x, ml.y);
 }
 
 template <int TYPE, int D, int NT>
@@ -267,224 +278,200 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   uint8_t* ring = attn_smem + warp * L::kRing;
   float2* stats = reinterpret_cast<float2*>(attn_smem + W * L::kRing);  // [warp][first, last][head]
-  float2* total = stats + 2 * W * 8 * NT;                         // of a piece's segment
+  float2* total = stats + 2 * W * 8 * NT;                            // of a piece's segment
   float* factor = reinterpret_cast<float*>(total + 2 * W * 8 * NT);  // of a piece in its segment
   int2* open = reinterpret_cast<int2*>(factor + 2 * W * 8 * NT);     // [warp][first, last]
   allow_dependents();
   wait_for_producers();
 
-  int most;
-  int64_t mine, incl;
-  const int64_t tiles = attn_scan(P, most, mine, incl);
-  const int heads = P.heads;
-  const AttnSplit split = attn_split<W>(P, tiles, most);
+  const AttnScan scan = attn_scan(P);
+  const AttnSplit split = attn_split<W>(P, scan);
   const bool by_warp = split.mode == kByWarp;
   const int unit = blockIdx.x * W + warp, units = P.grid * W;
 
-  // This warp's share: from tile pos0 of segment (b0, h0) on, `share` tiles (by warp: segment after
-  // segment).
-  int b0 = 0, h0 = 0, pos0 = 0;
-  int64_t share = 0;
-  if (by_warp) {
-    if (unit < P.segments) {
-      b0 = unit / heads;
-      h0 = unit - b0 * heads;
-      share = INT32_MAX;
-    }
-  } else if (split.mode == kBySegment) {
-    if (int(blockIdx.x) < P.segments) {
-      b0 = int(blockIdx.x) / heads;
-      h0 = int(blockIdx.x) - b0 * heads;
-      const int n = attn_span(P, b0).n, q = (n + W - 1) / W;
-      pos0 = min(q * warp, n);
-      share = min(q, n - pos0);
+  // This warp's share: from weighted tile `at0` of segment s0 on, `share` of them (by warp: segment
+  // after segment). `extra` ones stand before a segment's tiles.
+  const int extra = split.mode == kByTile ? kAttnExtra : 0;
+  AttnSegment s0 = {0, 0, 0};
+  int at0 = 0, share = 0;
+  if (split.mode == kByTile) {
+    const int64_t t0 = int64_t(split.quota) * unit, all = int64_t(scan.total) * P.heads;
+    if (t0 < all) {
+      share = int(min(int64_t(split.quota), all - t0));
+      const AttnPlace at = attn_find(P, scan, int(fast_div(t0, P.by_heads)));
+      const uint32_t local = uint32_t(t0 - int64_t(at.before) * P.heads);
+      const uint32_t n = attn_weight(attn_span(P, at.b)), hb = local / n;
+      s0 = attn_segment(P, int(hb));
+      s0.b = at.b;
+      at0 = int(local - hb * n);
     }
   } else {
-    const int64_t t0 = min(split.quota * unit, tiles * heads);
-    share = min(split.quota, tiles * heads - t0);
-    if (share > 0) {
-      const AttnPlace at = attn_find(P, mine, incl, fast_div(t0, P.by_heads));
-      const int n = attn_span(P, at.b).n;
-      const uint32_t local = uint32_t(t0 - at.before * heads);
-      b0 = at.b;
-      h0 = int(local / uint32_t(n));
-      pos0 = int(local - uint32_t(h0) * uint32_t(n));
+    const int seg = by_warp ? unit : blockIdx.x;
+    if (seg < P.segments) {
+      s0 = attn_segment(P, seg);
+      share = INT32_MAX;
+      if (!by_warp) {
+        const int n = attn_span(P, s0.b).n, q = (n + W - 1) / W;
+        at0 = min(q * warp, n);
+        share = min(q, n - at0);
+      }
     }
   }
-  // The segment after (b, h): false if there is none.
-  auto next_segment = [&](int& b, int& h) {
+  // The segment after s: false if there is none.
+  auto next_segment = [&](AttnSegment& s) {
     if (by_warp) {
-      const int64_t seg = int64_t(b) * heads + h + units;
-      if (seg >= P.segments) return false;
-      b = int(seg) / heads;
-      h = int(seg) - b * heads;
-    } else if (++h == heads) {
-      h = 0;
-      ++b;
+      const int seg = (s.b * P.heads + s.h * P.blocks + s.block);
+      if (seg >= P.segments - units) return false;
+      s = attn_segment(P, seg + units);
+    } else if (++s.block == P.blocks) {
+      s.block = 0;
+      if (++s.h == P.cache.heads) s.h = 0, ++s.b;
     }
-    return b < P.batch;
+    return s.b < P.batch;
   };
 
   // ---- the fetching side: the next tile to copy
-  int f_b = b0, f_h = h0, f_pos = pos0, f_end = 0;
+  AttnSegment fg = s0;
+  AttnSpan f = {0, 0, 0, 0};
+  int f_at = at0, f_left = share, f_pos = 0, f_end = 0, f_row = 0;  // f_row: tiles into the page
   // Pages of the piece from f_page0 on, one a lane, and the 32 after them: their loads are under way
   // long before they are needed.
   int f_page0 = 0, f_pages = 0, f_pages_next = 0;
-  int64_t f_left = share;  // tiles, this piece's included
-  AttnSpan f = {0, 0, 0, 0};
-  bool f_more = share > 0;
-  // The piece at f_pos, or the next that has a tile.
+  bool f_more = share > 0, f_new = true, f_fine = true;
+  // this lane's part of the tile: its first key piece, value piece, and its scale
+  const uint8_t *f_k = nullptr, *f_v = nullptr;
+  const float* f_s = nullptr;
+  // The piece that begins at f_at, or the next that has a tile.
   auto f_settle = [&]() {
-    for (; f_more; f_pos = 0) {
-      f = attn_span(P, f_b);
-      f_end = int(min(int64_t(f.n), f_pos + f_left));
+#pragma unroll 1
+    for (; f_more; f_at = 0) {
+      f = attn_span(P, fg.b);
+      const int part = min((f.n ? f.n + extra : 0) - f_at, f_left);
+      if (!by_warp) f_left -= part;
+      f_pos = max(f_at - extra, 0);
+      f_end = f_at + part - extra;
       if (f_pos < f_end) {
-        const int32_t* table = P.table + f_b * P.table_ld;
+        const int32_t* table = P.table + fg.b * P.table_ld;
         const int last = attn_page(P, f.first + f_end - 1);
         f_page0 = attn_page(P, f.first + f_pos);
+        f_row = f.first + f_pos - f_page0 * P.page_tiles;
         f_pages = table[min(f_page0 + lane, last)];
         if (f_page0 + 32 <= last) f_pages_next = table[min(f_page0 + 32 + lane, last)];
+        f_new = true;
         break;
       }
-      f_more = next_segment(f_b, f_h);
+      f_more = f_left > 0 && next_segment(fg);
     }
   };
   uint32_t bad = 0;  // which of the tiles under way have no page, the newest in bit 0
-  int fs = 0;
+  uint32_t f_dst = smem_addr(ring) + lane * 16;
+  const uint32_t ring_end = f_dst + L::kRing;
   auto fetch = [&]() {
     bad <<= 1;
     if (f_more) {
       const int tile = f.first + f_pos;
-      const int nth = attn_page(P, tile), in_page = tile - nth * P.page_tiles;
-      if (nth == f_page0 + 32) {
-        f_page0 = nth;
-        f_pages = f_pages_next;
-        const int last = attn_page(P, f.first + f_end - 1);
-        if (nth + 32 <= last)
-          f_pages_next = P.table[f_b * P.table_ld + min(nth + 32 + lane, last)];
+      if (f_new) {
+        const int nth = attn_page(P, tile);
+        if (nth == f_page0 + 32) {
+          f_page0 = nth;
+          f_pages = f_pages_next;
+          const int last = attn_page(P, f.first + f_end - 1);
+          if (nth + 32 <= last)
+            f_pages_next = P.table[fg.b * P.table_ld + min(nth + 32 + lane, last)];
+        }
+        const int page = __shfl_sync(0xffffffffu, f_pages, nth - f_page0);
+        f_fine = page >= 0 && page < P.cache.pages;
+        if (!f_fine && lane == 0) report_device_error(kDevErrBadIndex);
+        const int64_t p = f_fine ? page : 0;
+        const int64_t row = int64_t(fg.h) * P.cache.page_size + f_row * 16;
+        f_k = P.cache.k + p * P.cache.k_stride + (row + r) * (D * E) + c * 16;
+        f_v = P.cache.v + p * P.cache.v_stride + (row + 2 * c) * (D * E) + r * L::VB;
+        if (QUANT)
+          f_s = (c < 2 ? P.cache.k_scale + p * P.cache.ks_stride
+                       : P.cache.v_scale + p * P.cache.vs_stride) + row + r + 8 * (c & 1);
+        f_new = false;
       }
-      const int f_page = __shfl_sync(0xffffffffu, f_pages, nth - f_page0);
-      const bool fine = f_page >= 0 && f_page < P.cache.pages;
-      if (!fine) {
-        bad |= 1;
-        if (lane == 0) report_device_error(kDevErrBadIndex);
-      }
-      const int64_t page = fine ? f_page : 0;
-      const int lo = fine ? f.lo - tile * 16 : 16, hi = fine ? f.hi - tile * 16 : 0;
-      const int64_t row = int64_t(f_h / P.blocks) * P.cache.page_size + in_page * 16;
-      const uint32_t dst = smem_addr(ring + fs * L::kStage);
-      const uint8_t* k = P.cache.k + page * P.cache.k_stride + row * (D * E);
-      const uint8_t* v = P.cache.v + page * P.cache.v_stride + row * (D * E);
+      bad |= f_fine ? 0 : 1;
+      // The rows of the tile that are read; the others are filled with zeros.
+      const int lo = f_fine ? f.lo - tile * 16 : 16, hi = f.hi - tile * 16;
+      auto copy = [&](auto whole) {
+        constexpr bool ALL = decltype(whole)::value != 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = r + 8 * i;
-        const bool in = t >= lo && t < hi;
+        for (int i = 0; i < 2; ++i) {
+          const bool in = ALL || (r + 8 * i >= lo && r + 8 * i < hi);
 #pragma unroll
-        for (int p = 0; p < KP; ++p)
-          cp_async_if<16>(dst + ((i * KP + p) * 32 + lane) * 16, k + t * (D * E) + p * 64 + c * 16, in);
-      }
+          for (int p = 0; p < KP; ++p)
+            cp_async_part<16, ALL>(f_dst + (i * KP + p) * 512, f_k + i * 8 * (D * E) + p * 64, in);
+        }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 2 * c + (i & 1) + 8 * (i >> 1);
-        const bool in = t >= lo && t < hi;
+        for (int i = 0; i < 4; ++i) {
+          const int t = (i & 1) + 8 * (i >> 1);
+          const bool in = ALL || (2 * c + t >= lo && 2 * c + t < hi);
 #pragma unroll
-        for (int p = 0; p < VP; ++p)
-          cp_async_if<L::VB>(dst + L::kHalf + ((i * VP + p) * 32 + lane) * L::VB,
-                             v + t * (D * E) + (p * 8 + r) * L::VB, in);
-      }
-      if (QUANT) {
-        const int t = r + 8 * (c & 1);
-        const float* s = c < 2 ? P.cache.k_scale + page * P.cache.ks_stride
-                               : P.cache.v_scale + page * P.cache.vs_stride;
-        cp_async_if<4>(dst + 2 * L::kHalf + (c * 8 + r) * 4, s + row + t, t >= lo && t < hi);
-      }
-      if (!by_warp) f_more = --f_left > 0;
-      if (++f_pos == f_end && f_more) {
-        f_more = next_segment(f_b, f_h);
-        f_pos = 0;
+          for (int p = 0; p < VP; ++p)
+            cp_async_part<L::VB, ALL>(f_dst + L::kHalf - lane * (16 - L::VB) + (i * VP + p) * 32 * L::VB,
+                                      f_v + t * (D * E) + p * 8 * L::VB, in);
+        }
+        if (QUANT) {
+          const int t = r + 8 * (c & 1);
+          cp_async_part<4, ALL>(f_dst + 2 * L::kHalf - lane * 16 + (c * 8 + r) * 4, f_s,
+                                ALL || (t >= lo && t < hi));
+        }
+      };
+      if (lo <= 0 && hi >= 16) copy(Kind<1>());
+      else copy(Kind<0>());
+      f_k += 16 * D * E;
+      f_v += 16 * D * E;
+      f_s += 16;
+      f_new = ++f_row == P.page_tiles;
+      if (f_new) f_row = 0;
+      if (++f_pos == f_end) {
+        f_more = f_left > 0 && next_segment(fg);
+        f_at = 0;
         f_settle();
       }
     }
     cp_async_commit();
-    fs = fs + 1 == S ? 0 : fs + 1;
+    f_dst += L::kStage;
+    if (f_dst == ring_end) f_dst -= L::kRing;
   };
-  // The part of a segment's queries that a lane holds, as it lies in memory. (The first segment's is
-  // asked for before the tiles, so that it does not arrive behind them.)
-  uint4 qx[NT][KP * KS / 2];
-  auto load_q = [&](int b, int hb) {
-    const int h = hb / P.blocks, block = hb - h * P.blocks;
-    const int live = min(8 * NT, P.group - block * 8 * NT);
-    const uint16_t* q = P.q + b * P.q_ld + int64_t(h * P.group + block * 8 * NT) * D;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int n = j * 8 + r;
-      const uint4* row = reinterpret_cast<const uint4*>(q + n * D);
-#pragma unroll
-      for (int p = 0; p < KP; ++p)
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i)
-          qx[j][p * (KS / 2) + i] =
-              n < live ? row[(p * 4 + c) * (KS / 2) + i] : make_uint4(0, 0, 0, 0);
-    }
-  };
-  if (share > 0) load_q(b0, h0);
   f_settle();
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) fetch();
 
-  // ---- the computing side
-  int cs = 0;
-  int64_t left = share;
+  // ---- the computing side. Before the first tile the ring is filled.
+  int warm = S - 1, left = share;
+  const uint8_t* stage = ring;
   int2 open_first = {-1, 0}, open_last = {-1, 0};  // pieces: segment, whether it starts (1), ends (2)
+  AttnSegment sg = s0;
   bool more = share > 0;
-  for (int b = b0, hb = h0, begin = pos0; more; begin = 0, more = left > 0 && next_segment(b, hb)) {
-    if (b != b0 || hb != h0) load_q(b, hb);
-    const AttnSpan span = attn_span(P, b);
-    const int end = int(min(int64_t(span.n), begin + left));
+  for (int at = at0; more; at = 0, more = left > 0 && next_segment(sg)) {
+    const AttnSpan span = attn_span(P, sg.b);
+    const int part = min((span.n ? span.n + extra : 0) - at, left);
+    const int begin = max(at - extra, 0), end = at + part - extra;
     if (!by_warp) {
-      if (span.n == 0) continue;
-      left -= end - begin;
+      left -= part;
+      if (begin >= end) continue;
     }
-    const int h = hb / P.blocks, block = hb - h * P.blocks;
-    const int head0 = h * P.group + block * 8 * NT;          // first query head of the block
-    const int live = min(8 * NT, P.group - block * 8 * NT);  // query heads in it
+    const int head0 = sg.h * P.group + sg.block * 8 * NT;       // first query head of the block
+    const int live = min(8 * NT, P.group - sg.block * 8 * NT);  // query heads in it
+    const int64_t row0 = int64_t(sg.b) * P.q_heads + head0;
 
-    // q as the columns of S^T: the values that face this lane's part of a key row
+    // q as the columns of S^T: the values that face this lane's part of a key row. (As they lie in
+    // memory until the first tile; asked for before the ring's first tiles.)
     uint32_t qf[NT][KP * KS][2];
     float fac[NT][2];  // logits in log2 units, for the lane's two heads
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const uint4* x = qx[j];
-      if (!QUANT) {
+      const int n = j * 8 + r;
+      const uint4* row =
+          reinterpret_cast<const uint4*>(P.q + sg.b * P.q_ld + int64_t(head0 + n) * D) + c * (KS / 2);
 #pragma unroll
-        for (int i = 0; i < KP * KS / 2; ++i) {
-          qf[j][2 * i][0] = x[i].x, qf[j][2 * i][1] = x[i].y;
-          qf[j][2 * i + 1][0] = x[i].z, qf[j][2 * i + 1][1] = x[i].w;
-        }
-        fac[j][0] = fac[j][1] = P.scale_log2;
-      } else {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < KP * KS / 2; ++i)
-          m = max_u16x2(max_u16x2(m, x[i].x & 0x7FFF7FFFu),
-                        max_u16x2(x[i].y & 0x7FFF7FFFu,
-                                  max_u16x2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
-        uint32_t e = max(m & 0xFFFFu, m >> 16) >> 7;  // exponent of the head's largest value
-        e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
-        e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-        e = min(max(e, 10u), 244u);  // (smaller ones count as zero in effect, larger ones overflow)
-        const float up = __uint_as_float((254u - e + 8u) << 23);  // 2^(127 + 8 - e): below 2^9
-#pragma unroll
-        for (int i = 0; i < KP * KS / 2; ++i) {
-          const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            qf[j][2 * i + w / 2][w & 1] = pack_f16x2(bf_lo(u[w]) * up, bf_hi(u[w]) * up);
-        }
-        const float down = P.scale_log2 * __uint_as_float((e - 8u) << 23);  // 2^(e - 8 - 127)
-        fac[j][0] = __shfl_sync(0xffffffffu, down, 8 * c);
-        fac[j][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+      for (int i = 0; i < KP * KS / 2; ++i) {
+        const uint4 x = n < live ? row[(i / (KS / 2)) * 4 * (KS / 2) + i % (KS / 2)]
+                                 : make_uint4(0, 0, 0, 0);
+        qf[j][2 * i][0] = x.x, qf[j][2 * i][1] = x.y;
+        qf[j][2 * i + 1][0] = x.z, qf[j][2 * i + 1][1] = x.w;
       }
+      fac[j][0] = fac[j][1] = P.scale_log2;
     }
 
     float o[NT][MT][4];
@@ -499,13 +486,38 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
       for (int x = 0; x < 2; ++x) m[j][x] = kAttnNone, l[j][x] = 0.0f, kf[j][x] = 0x1p100f;
     }
 
-    for (int pos = begin; pos < end; ++pos) {
+#pragma unroll 1
+    for (int pos = begin - warm; pos < end; ++pos) {
       __syncwarp();  // (the stage that fetch() overwrites has been read by all lanes)
       fetch();
+      if (pos < begin) continue;
+      if (QUANT && pos == begin) {  // q to fp16
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < KP * KS; ++i)
+            m = max_u16x2(m, max_u16x2(qf[j][i][0] & 0x7FFF7FFFu, qf[j][i][1] & 0x7FFF7FFFu));
+          uint32_t e = max(m & 0xFFFFu, m >> 16) >> 7;  // exponent of the head's largest value
+          e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
+          e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+          e = min(max(e, 10u), 244u);  // (smaller ones count as zero in effect, larger ones overflow)
+          const float up = __uint_as_float((254u - e + 8u) << 23);  // 2^(127 + 8 - e): below 2^9
+#pragma unroll
+          for (int i = 0; i < KP * KS; ++i)
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              qf[j][i][w] = pack_f16x2(bf_lo(qf[j][i][w]) * up, bf_hi(qf[j][i][w]) * up);
+          const float down = P.scale_log2 * __uint_as_float((e - 8u) << 23);  // 2^(e - 8 - 127)
+          fac[j][0] = __shfl_sync(0xffffffffu, down, 8 * c);
+          fac[j][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+        }
+      }
       cp_async_wait<S - 1>();
       __syncwarp();
-      const uint8_t* stage = ring + cs * L::kStage;
-      cs = cs + 1 == S ? 0 : cs + 1;
+      const uint8_t* st = stage;
+      stage += L::kStage;
+      if (stage == ring + L::kRing) stage = ring;
       if ((bad >> (S - 1)) & 1) continue;
 
       // S^T
@@ -516,7 +528,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
         for (int x = 0; x < 4; ++x) s[j][0][x] = s[j][1][x] = 0.0f;
 #pragma unroll
       for (int p = 0; p < KP; ++p) {
-        const uint4* at = reinterpret_cast<const uint4*>(stage) + p * 32 + lane;
+        const uint4* at = reinterpret_cast<const uint4*>(st) + p * 32 + lane;
         const uint4 x4 = at[0], y4 = at[KP * 32];
         const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w}, y[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
@@ -538,7 +550,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
       // weights
       float ks[2] = {1.0f, 1.0f}, vs[2] = {1.0f, 1.0f};
       if (QUANT) {
-        const float* sc = reinterpret_cast<const float*>(stage + 2 * L::kHalf) + r;
+        const float* sc = reinterpret_cast<const float*>(st + 2 * L::kHalf) + r;
         ks[0] = sc[0], ks[1] = sc[8], vs[0] = sc[16], vs[1] = sc[24];
       }
       const int tok0 = (span.first + pos) * 16;
@@ -631,7 +643,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
         uint32_t x[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint8_t* at = stage + L::kHalf + ((i * VP + pc) * 32 + lane) * L::VB;
+          const uint8_t* at = st + L::kHalf + ((i * VP + pc) * 32 + lane) * L::VB;
           if (L::VB == 16) {
             const uint4 y = *reinterpret_cast<const uint4*>(at);
             x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
@@ -664,6 +676,8 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
       }
     }
 
+    warm = 0;
+
     // ---- this warp's sums
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -671,36 +685,48 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
       for (int x = 0; x < 2; ++x) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[j][x] += __shfl_xor_sync(0xffffffffu, l[j][x], d);
-        if (QUANT) {
-          const float inv = 1.0f / kf[j][x];
-#pragma unroll
-          for (int i = 0; i < MT; ++i) o[j][i][x] *= inv, o[j][i][x + 2] *= inv;
-        }
       }
-    if (begin == 0 && end == span.n) {  // a whole segment
+    const bool whole = begin == 0 && end == span.n;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float f = QUANT ? __fdividef(1.0f, kf[j][x]) : 1.0f;
+        if (whole) f = l[j][x] == 0.0f ? 0.0f : __fdividef(f, l[j][x]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[j][i][x] *= f, o[j][i][x + 2] *= f;
+      }
+    if (whole) {  // a whole segment
+      using V = AttnValues<TYPE, D>;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int n = j * 8 + 2 * c + x;
           if (n >= live) continue;
+          uint16_t* to = P.out + (row0 + n) * D + r * V::kRun;
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
-            attn_store<TYPE, D>(P, b, head0 + n, i, r, make_float2(o[j][i][x], o[j][i][x + 2]),
-                                m[j][x], l[j][x]);
+          for (int i = 0; i < MT; i += 4) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = pack_bf16x2(o[j][i + q][x], o[j][i + q][x + 2]);
+            *reinterpret_cast<uint4*>(to + V::of(i, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (P.lse && r == 0) P.lse[row0 + n] = attn_lse(m[j][x], l[j][x]);
         }
       continue;
     }
     // A piece: the warp's last one stays in its ring, an earlier one (there can be one, its first)
     // waits in the workspace.
     const bool last = left <= 0;
-    float2* to = last ? reinterpret_cast<float2*>(ring)
-                      : reinterpret_cast<float2*>(P.part_o + int64_t(unit) * L::kPiece);
+    float2* to = (last ? reinterpret_cast<float2*>(ring)
+                       : reinterpret_cast<float2*>(P.part_o + int64_t(unit) * L::kPiece)) + lane;
     if (last) {
       cp_async_wait<0>();
       __syncwarp();  // (all lanes have read the ring)
     }
-    const int2 what = make_int2(b * heads + hb, (begin == 0 ? 1 : 0) | (end == span.n ? 2 : 0));
+    const int2 what = make_int2(sg.b * P.heads + sg.h * P.blocks + sg.block,
+                                (begin == 0 ? 1 : 0) | (end == span.n ? 2 : 0));
     if (last) open_last = what; else open_first = what;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -710,7 +736,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
           stats[(warp * 2 + last) * (8 * NT) + j * 8 + 2 * c + x] = make_float2(m[j][x], l[j][x]);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-          to[((j * MT + i) * 2 + x) * 32 + lane] = make_float2(o[j][i][x], o[j][i][x + 2]);
+          to[((j * MT + i) * 2 + x) * 32] = make_float2(o[j][i][x], o[j][i][x + 2]);
       }
   }
   cp_async_wait<0>();
@@ -721,32 +747,32 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
   if (lane == 0) open[2 * warp] = open_first, open[2 * warp + 1] = open_last;
   __syncthreads();
   // a thread for each piece and head: the segment's maximum and sum, the piece's factor
+#pragma unroll 1
   for (int e = threadIdx.x; e < 2 * W * 8 * NT; e += W * 32) {
-    const int p = e / (8 * NT), n = e % (8 * NT), seg = open[p].x;
+    const int seg = open[e / (8 * NT)].x;
+    if (seg < 0) continue;
+    const float2* ml = stats + e % (8 * NT);
     float top = kAttnNone, sum = 0.0f;
-    if (seg >= 0) {
-      float2 ml[2 * W];
-#pragma unroll
-      for (int q = 0; q < 2 * W; ++q)
-        ml[q] = open[q].x == seg ? stats[q * (8 * NT) + n] : make_float2(kAttnNone, 0.0f);
-#pragma unroll
-      for (int q = 0; q < 2 * W; ++q) top = fmaxf(top, ml[q].x);
-#pragma unroll
-      for (int q = 0; q < 2 * W; ++q) sum += ex2(ml[q].x - top) * ml[q].y;
-      factor[e] = ex2(stats[e].x - top);
-      total[e] = make_float2(top, sum);
-    }
+#pragma unroll 4
+    for (int q = 0; q < 2 * W; ++q)
+      if (open[q].x == seg) top = fmaxf(top, ml[q * (8 * NT)].x);
+#pragma unroll 4
+    for (int q = 0; q < 2 * W; ++q)
+      if (open[q].x == seg) sum += ex2(ml[q * (8 * NT)].x - top) * ml[q * (8 * NT)].y;
+    factor[e] = ex2(stats[e].x - top);
+    total[e] = make_float2(top, sum);
   }
   __syncthreads();
-  for (int p0 = 0, seen = -1; p0 < 2 * W; ++p0) {
+  int seen = -1;
+#pragma unroll 1
+  for (int p0 = 0; p0 < 2 * W; ++p0) {
     const int2 first = open[p0];
     if (first.x < 0 || first.x == seen) continue;
     seen = first.x;
-    const int b = seen / heads, hb = seen - b * heads;
-    const int h = hb / P.blocks, block = hb - h * P.blocks;
-    const int live = min(8 * NT, P.group - block * 8 * NT);
+    const AttnSegment s = attn_segment(P, seen);
+    const int live = min(8 * NT, P.group - s.block * 8 * NT);
     int tail = -1, ends = 0;  // its last piece where that is a warp's first
-#pragma unroll
+#pragma unroll 4
     for (int q = 0; q < 2 * W; ++q)
       if (open[q].x == seen) {
         ends = open[q].y & 2;
@@ -754,51 +780,52 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
       }
     const bool starts = first.y & 1, whole = starts && ends;
     const int slot = 2 * blockIdx.x + starts;  // where it goes on in other CTAs
-#pragma unroll
-    for (int i0 = 0; i0 < L::kItems / W; ++i0) {
-      const int i = i0 * W + warp, n = (i / (2 * MT)) * 8 + 2 * c + (i & 1);
+#pragma unroll 1
+    for (int i = warp; i < L::kItems; i += W) {
+      const int n = (i / (2 * MT)) * 8 + 2 * c + (i & 1), at = i * 32 + lane;
       if (n >= live) continue;
       float2 acc = make_float2(0.0f, 0.0f);
       if (tail >= 0) {
         const float2 v = reinterpret_cast<const float2*>(
-            P.part_o + (int64_t(blockIdx.x) * W + (tail >> 1)) * L::kPiece)[i * 32 + lane];
+            P.part_o + (int64_t(blockIdx.x) * W + (tail >> 1)) * L::kPiece)[at];
         const float f = factor[tail * (8 * NT) + n];
         acc = make_float2(f * v.x, f * v.y);
       }
-#pragma unroll
-      for (int q = 1; q < 2 * W; q += 2)
-        if (open[q].x == seen) {
-          const float2 v = reinterpret_cast<const float2*>(attn_smem + (q >> 1) * L::kRing)[i * 32 + lane];
-          const float f = factor[q * (8 * NT) + n];
+#pragma unroll 4
+      for (int w = 0; w < W; ++w)
+        if (open[2 * w + 1].x == seen) {
+          const float2 v = reinterpret_cast<const float2*>(attn_smem + w * L::kRing)[at];
+          const float f = factor[(2 * w + 1) * (8 * NT) + n];
           acc.x += f * v.x;
           acc.y += f * v.y;
         }
       const float2 ml = total[p0 * (8 * NT) + n];
       if (whole) {
-        attn_store<TYPE, D>(P, b, h * P.group + block * 8 * NT + n, (i >> 1) % MT, r, acc, ml.x, ml.y);
+        attn_store<TYPE, D>(P, int64_t(s.b) * P.q_heads + s.h * P.group + s.block * 8 * NT + n,
+                            (i >> 1) % MT, r, acc, ml);
       } else {
-        reinterpret_cast<float2*>(P.part_o + int64_t(units + slot) * L::kPiece)[i * 32 + lane] = acc;
+        reinterpret_cast<float2*>(P.part_o + int64_t(units + slot) * L::kPiece)[at] = acc;
         if (r == 0 && ((i >> 1) % MT) == 0) P.part_ml[slot * (8 * NT) + n] = ml;
       }
     }
   }
   // sequences without tokens: no warp has them
+#pragma unroll 1
   for (int64_t seg = unit; seg < P.segments; seg += units) {
-    const int b = int(seg) / heads, hb = int(seg) - b * heads;
-    if (attn_span(P, b).n > 0) continue;
-    const int h = hb / P.blocks, block = hb - h * P.blocks;
-    for (int n = 0; n < min(8 * NT, P.group - block * 8 * NT); ++n) {
-      const int64_t row = int64_t(b) * P.q_heads + h * P.group + block * 8 * NT + n;
-      for (int i = lane; i < D / 2; i += 32) reinterpret_cast<uint32_t*>(P.out + row * D)[i] = 0u;
-      if (P.lse && lane == 0) P.lse[row] = -INFINITY;
-    }
+    const AttnSegment s = attn_segment(P, int(seg));
+    if (attn_span(P, s.b).n > 0) continue;
+    const int64_t row = int64_t(s.b) * P.q_heads + s.h * P.group + s.block * 8 * NT;
+    const int live = min(8 * NT, P.group - s.block * 8 * NT);
+#pragma unroll 1
+    for (int i = lane; i < live * (D / 2); i += 32) reinterpret_cast<uint32_t*>(P.out + row * D)[i] = 0u;
+    if (P.lse && lane < live) P.lse[row + lane] = -INFINITY;
   }
 }
 
 // Joins the pieces of segments that several CTAs shared. A CTA for each segment, or, where there are
-// more of them, for each CTA of the attention kernel and the segment that goes on behind it; its warps
-// take the pieces in turn, all loads of a warp's pieces under way at once.
-constexpr int kJoinWarps = 4, kJoinItems = 4, kJoinAhead = 6;
+// more of them, for each CTA of the attention kernel and the segment that goes on behind it, and for
+// four of a piece's pairs of values; its warps take the pieces in turn.
+constexpr int kJoinWarps = 8, kJoinItems = 4;
 
 template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams P) {
@@ -807,102 +834,84 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   __shared__ float2 stats[kJoinWarps][kJoinItems][4];
   wait_for_producers();
   allow_dependents();
-  int most;
-  int64_t mine, incl;
-  const int64_t tiles = attn_scan(P, most, mine, incl);
-  const AttnSplit split = attn_split<L::kWarps>(P, tiles, most);
+  const AttnScan scan = attn_scan(P);
+  const AttnSplit split = attn_split<L::kWarps>(P, scan);
   if (split.mode != kByTile) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const int heads = P.heads;
-  const int64_t quota = split.quota * L::kWarps;  // of a CTA
-  int b, hb, count;
-  int64_t s0;  // the segment's first tile
-  if (P.segments <= P.grid) {
-    b = int(blockIdx.x) / heads;
-    hb = int(blockIdx.x) - b * heads;
-    const int per = (P.batch + 31) >> 5, owner = b / per;
-    int64_t before = __shfl_sync(0xffffffffu, incl - mine, owner);
-    for (int i = owner * per; i < b; ++i) before += attn_span(P, i).n;
-    count = attn_span(P, b).n;
+  const int quota = split.quota * L::kWarps;  // of a CTA
+  const bool by_segment = P.segments <= P.grid;
+  // the sequence, and the segment's first weighted tile
+  const int64_t t = (int64_t(blockIdx.x) + 1) * quota - 1;  // the CTA's last tile
+  AttnSegment s;
+  int64_t first;
+  int count;
+  if (by_segment) {
+    s = attn_segment(P, blockIdx.x);
+    const int per = (P.batch + 31) >> 5;
+    int before = __shfl_sync(0xffffffffu, scan.incl - scan.mine, s.b / per);
+#pragma unroll 1
+    for (int i = s.b / per * per; i < s.b; ++i) before += attn_weight(attn_span(P, i));
+    count = attn_weight(attn_span(P, s.b));
     if (count == 0) return;
-    s0 = before * heads + int64_t(hb) * count;
+    first = int64_t(before) * P.heads + int64_t(s.h * P.blocks + s.block) * count;
   } else {
-    const int64_t t = (int64_t(blockIdx.x) + 1) * quota - 1;  // the CTA's last tile
-    if (t >= tiles * heads) return;
-    const AttnPlace at = attn_find(P, mine, incl, fast_div(t, P.by_heads));
-    count = attn_span(P, at.b).n;
-    const uint32_t local = uint32_t(t - at.before * heads);
-    b = at.b;
-    hb = int(local / uint32_t(count));
-    s0 = at.before * heads + int64_t(hb) * count;
-    if (s0 < int64_t(blockIdx.x) * quota) return;  // began in an earlier CTA
+    if (t >= int64_t(scan.total) * P.heads) return;
+    const AttnPlace at = attn_find(P, scan, int(fast_div(t, P.by_heads)));
+    count = attn_weight(attn_span(P, at.b));
+    const uint32_t hb = uint32_t(t - int64_t(at.before) * P.heads) / uint32_t(count);
+    s = attn_segment(P, int(hb));
+    s.b = at.b;
+    first = int64_t(at.before) * P.heads + int64_t(hb) * count;
+    if (first + kAttnExtra < int64_t(blockIdx.x) * quota) return;  // began in an earlier CTA
   }
-  const int c0 = int(s0 / quota), pieces = int((s0 + count - 1) / quota) - c0 + 1;
-  if (pieces == 1) return;
-  const int h = hb / P.blocks, block = hb - h * P.blocks;
-  const int live = min(8 * NT, P.group - block * 8 * NT);
-  const int units = P.grid * L::kWarps, item0 = blockIdx.y * kJoinItems;
-  float top[kJoinItems], sum[kJoinItems];
-  float2 acc[kJoinItems];
+  const int c0 = int((first + kAttnExtra) / quota), pieces = int((first + count - 1) / quota) - c0 + 1;
+  if (pieces == 1 || (!by_segment && c0 != int(blockIdx.x))) return;
+  const int live = min(8 * NT, P.group - s.block * 8 * NT);
+  const int item0 = blockIdx.y * kJoinItems;
+  float2 ml[kJoinItems], acc[kJoinItems];
 #pragma unroll
-  for (int i = 0; i < kJoinItems; ++i) top[i] = kAttnNone, sum[i] = 0.0f, acc[i] = make_float2(0.0f, 0.0f);
-  for (int q = warp; q < pieces; q += kJoinWarps * kJoinAhead) {
-    float2 ml[kJoinAhead][kJoinItems], v[kJoinAhead][kJoinItems];
-#pragma unroll
-    for (int a = 0; a < kJoinAhead; ++a)
-#pragma unroll
-      for (int i = 0; i < kJoinItems; ++i) {
-        const int p = q + a * kJoinWarps, it = item0 + i;
-        const int n = (it / (2 * L::MT)) * 8 + 2 * c + (it & 1);
-        ml[a][i] = make_float2(kAttnNone, 0.0f);
-        v[a][i] = make_float2(0.0f, 0.0f);
-        if (p < pieces && n < live) {
-          const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);  // the first piece is its CTA's last
-          ml[a][i] = P.part_ml[slot * (8 * NT) + n];
-          v[a][i] = reinterpret_cast<const float2*>(P.part_o + int64_t(units + slot) * L::kPiece)[it * 32 + lane];
-        }
-      }
+  for (int i = 0; i < kJoinItems; ++i) ml[i] = make_float2(kAttnNone, 0.0f), acc[i] = make_float2(0.0f, 0.0f);
+#pragma unroll 2
+  for (int p = warp; p < pieces; p += kJoinWarps) {
+    const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);  // the first piece is its CTA's last
+    const float2* from = reinterpret_cast<const float2*>(
+        P.part_o + (int64_t(P.grid) * L::kWarps + slot) * L::kPiece) + item0 * 32 + lane;
+    const float2* stat = P.part_ml + slot * (8 * NT) + (item0 / (2 * L::MT)) * 8 + 2 * c;
+    // (the four items are of one block of eight heads, in turn its heads 2c and 2c + 1)
+    const bool in0 = (item0 / (2 * L::MT)) * 8 + 2 * c < live, in1 = (item0 / (2 * L::MT)) * 8 + 2 * c + 1 < live;
+    const float2 none = make_float2(kAttnNone, 0.0f), zero = make_float2(0.0f, 0.0f);
+    const float2 x[2] = {in0 ? stat[0] : none, in1 ? stat[1] : none};
 #pragma unroll
     for (int i = 0; i < kJoinItems; ++i) {
-      float t = top[i];
-#pragma unroll
-      for (int a = 0; a < kJoinAhead; ++a) t = fmaxf(t, ml[a][i].x);
-      const float f0 = ex2(top[i] - t);
-      top[i] = t;
-      sum[i] *= f0;
-      acc[i].x *= f0;
-      acc[i].y *= f0;
-#pragma unroll
-      for (int a = 0; a < kJoinAhead; ++a) {
-        const float f = ex2(ml[a][i].x - t);
-        sum[i] += f * ml[a][i].y;
-        acc[i].x += f * v[a][i].x;
-        acc[i].y += f * v[a][i].y;
-      }
+      const float2 v = (i & 1 ? in1 : in0) ? from[i * 32] : zero;
+      const float top = fmaxf(ml[i].x, x[i & 1].x);
+      const float f0 = ex2(ml[i].x - top), f1 = ex2(x[i & 1].x - top);
+      ml[i] = make_float2(top, f0 * ml[i].y + f1 * x[i & 1].y);
+      acc[i] = make_float2(f0 * acc[i].x + f1 * v.x, f0 * acc[i].y + f1 * v.y);
     }
   }
 #pragma unroll
   for (int i = 0; i < kJoinItems; ++i) {
     sums[warp][i][lane] = acc[i];
-    if (r == 0) stats[warp][i][c] = make_float2(top[i], sum[i]);
+    if (r == 0) stats[warp][i][c] = ml[i];
   }
   __syncthreads();
-  for (int i = warp; i < kJoinItems; i += kJoinWarps) {
-    const int it = item0 + i, n = (it / (2 * L::MT)) * 8 + 2 * c + (it & 1);
-    if (n >= live) continue;
-    float t = kAttnNone, s = 0.0f;
-    float2 a = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) t = fmaxf(t, stats[w][i][c].x);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      const float f = ex2(stats[w][i][c].x - t);
-      s += f * stats[w][i][c].y;
-      a.x += f * sums[w][i][lane].x;
-      a.y += f * sums[w][i][lane].y;
-    }
-    attn_store<TYPE, D>(P, b, h * P.group + block * 8 * NT + n, (it >> 1) % L::MT, r, a, t, s);
+  if (warp >= kJoinItems) return;
+  const int it = item0 + warp, n = (it / (2 * L::MT)) * 8 + 2 * c + (it & 1);
+  if (n >= live) return;
+  float top = kAttnNone, sum = 0.0f;
+  float2 a = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, stats[w][warp][c].x);
+#pragma unroll 4
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float f = ex2(stats[w][warp][c].x - top);
+    sum += f * stats[w][warp][c].y;
+    a.x += f * sums[w][warp][lane].x;
+    a.y += f * sums[w][warp][lane].y;
   }
+  attn_store<TYPE, D>(P, int64_t(s.b) * P.q_heads + s.h * P.group + s.block * 8 * NT + n,
+                      (it >> 1) % L::MT, r, a, make_float2(top, sum));
 }
 
 }  // namespace fp8q
