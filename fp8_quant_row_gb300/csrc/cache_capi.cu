@@ -60,7 +60,7 @@ fp8q_status check_cache_shape(const fp8q_paged_cache& c) {
     if (s < page || s % 16 != 0 || s > kMaxLd / 16) return FP8Q_ERR_SHAPE;
   if (c.type != FP8Q_BF16)
     for (int64_t s : {c.k_scale_stride, c.v_scale_stride})
-      if (s < c.heads * c.page_size || s > kMaxLd / 16) return FP8Q_ERR_SHAPE;
+      if (s < c.heads * c.page_size || s % 4 != 0 || s > kMaxLd / 16) return FP8Q_ERR_SHAPE;
   return FP8Q_OK;
 }
 
@@ -68,7 +68,7 @@ fp8q_status check_cache_pointers(const fp8q_paged_cache& c) {
   const bool scaled = c.type != FP8Q_BF16;
   if (c.pages == 0) return FP8Q_OK;
   if (!c.k || !c.v || (scaled && (!c.k_scale || !c.v_scale))) return FP8Q_ERR_NULL;
-  if (!aligned16(c.k) || !aligned16(c.v) || !aligned4(c.k_scale) || !aligned4(c.v_scale))
+  if (!aligned16(c.k) || !aligned16(c.v) || !aligned16(c.k_scale) || !aligned16(c.v_scale))
     return FP8Q_ERR_ALIGN;
   return FP8Q_OK;
 }
@@ -269,6 +269,24 @@ int64_t workspace_bytes_of(const AttnShape& s, int64_t head_dim) {
 
 fp8q::FastDiv fast_div_by(int64_t d) { return fp8q::FastDiv{d == 1 ? 0 : UINT64_MAX / uint64_t(d) + 1}; }
 
+// Tensor map of a cache's pages: lines of 128 bytes at least, boxes of 16 tokens by 128 bytes.
+template <typename L>
+fp8q_status tile_map(CUtensorMap* map, uint8_t* pages, int64_t page_bytes, const fp8q::CacheView& c) {
+  EncodeTiled fn = nullptr;
+  const fp8q_status st = encode_tiled(&fn);
+  if (st != FP8Q_OK) return st;
+  const cuuint64_t lines = cuuint64_t(c.heads) * c.page_size * L::kLines / 16;
+  const cuuint64_t dims[3] = {cuuint64_t(L::kLine), lines, cuuint64_t(std::max<int64_t>(c.pages, 1))};
+  const cuuint64_t strides[2] = {cuuint64_t(L::kLine), cuuint64_t(page_bytes)};
+  const cuuint32_t box[3] = {128, cuuint32_t(L::kLines), 1};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pages, dims, strides, box, steps,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled", r);
+  return FP8Q_OK;
+}
+
 template <int TYPE, int D, int NT>
 fp8q_status launch_attention(const fp8q::AttnParams& p, const AttnShape& s, cudaStream_t stream) {
   using L = fp8q::AttnLayout<TYPE, D, NT>;
@@ -279,7 +297,13 @@ fp8q_status launch_attention(const fp8q::AttnParams& p, const AttnShape& s, cuda
   fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), L::kWarps * 32, L::kBytes, &bps);
   if (st != FP8Q_OK) return st;
   if (bps <= 0) return cuda_fail(cudaErrorInvalidConfiguration, "occupancy", (long long)L::kBytes);
-  st = launch(fn, dim3(unsigned(s.grid)), dim3(L::kWarps * 32), size_t(L::kBytes), stream, p);
+  CUtensorMap map_k, map_v;
+  st = tile_map<L>(&map_k, p.cache.k, p.cache.k_stride, p.cache);
+  if (st != FP8Q_OK) return st;
+  st = tile_map<L>(&map_v, p.cache.v, p.cache.v_stride, p.cache);
+  if (st != FP8Q_OK) return st;
+  st = launch(fn, dim3(unsigned(s.grid)), dim3(L::kWarps * 32), size_t(L::kBytes), stream, p, map_k,
+              map_v);
   if (st != FP8Q_OK || !s.join) return st;
   return launch(fp8q::attn_join_kernel<TYPE, D, NT>,
                 dim3(unsigned(std::min(p.segments, p.grid)), L::kItems / fp8q::kJoinItems),

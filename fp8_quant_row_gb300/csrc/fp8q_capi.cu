@@ -259,27 +259,6 @@ fp8q_status launch_silu(const fp8q::SiluParams& p, const DeviceInfo& dev, cudaSt
   }
 }
 
-// The driver's tensor-map encoder, through the runtime (the library links no libcuda).
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-fp8q_status encode_tiled(EncodeTiled* fn) {
-  static std::once_flag once;
-  static void* entry = nullptr;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    cudaDriverEntryPointQueryResult found;
-    err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &entry, 12000,
-                                           cudaEnableDefault, &found);
-    if (err == cudaSuccess && found != cudaDriverEntryPointSuccess) err = cudaErrorSymbolNotFound;
-  });
-  if (err != cudaSuccess) return cuda_fail(err, "cudaGetDriverEntryPointByVersion");
-  *fn = reinterpret_cast<EncodeTiled>(entry);
-  return FP8Q_OK;
-}
-
 // Tensor map of int8 rows [rows, k] at stride ld: boxes of 128 values of k x `box` rows, 128-byte
 // swizzle; values past k and rows past `rows` read as zero.
 fp8q_status int8_map(CUtensorMap* map, const int8_t* p, int64_t rows, int64_t k, int64_t ld,

@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "fp8q.h"
@@ -182,6 +183,27 @@ fp8q_status launch(void (*fn)(Args...), dim3 grid, dim3 block, size_t smem, cuda
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args...);
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx", (long long)smem);
+  return FP8Q_OK;
+}
+
+// The driver's tensor-map encoder, through the runtime (the library links no libcuda).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline fp8q_status encode_tiled(EncodeTiled* fn) {
+  static std::once_flag once;
+  static void* entry = nullptr;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult found;
+    err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &entry, 12000,
+                                           cudaEnableDefault, &found);
+    if (err == cudaSuccess && found != cudaDriverEntryPointSuccess) err = cudaErrorSymbolNotFound;
+  });
+  if (err != cudaSuccess) return cuda_fail(err, "cudaGetDriverEntryPointByVersion");
+  *fn = reinterpret_cast<EncodeTiled>(entry);
   return FP8Q_OK;
 }
 

@@ -341,12 +341,12 @@ fp8q_status fp8q_int8_matmul(void* out, const int8_t* a, int64_t lda, const floa
 typedef struct fp8q_paged_cache {
     void* k;         /* [pages, heads, page_size, head_dim] of `type`, 16-byte aligned            */
     void* v;
-    float* k_scale;  /* [pages, heads, page_size] fp32, 4-byte aligned; NULL for FP8Q_BF16        */
+    float* k_scale;  /* [pages, heads, page_size] fp32, 16-byte aligned; NULL for FP8Q_BF16       */
     float* v_scale;
     int64_t k_stride, v_stride;              /* values between pages: >= heads*page_size*head_dim,
                                                 a multiple of 16 (k and v may be the halves of one
                                                 [pages, 2, ...] array); pages are contiguous       */
-    int64_t k_scale_stride, v_scale_stride;  /* values between pages of the scales                */
+    int64_t k_scale_stride, v_scale_stride;  /* values between pages of the scales: a multiple of 4 */
     int64_t pages;
     int64_t page_size;  /* a multiple of 16, 16 .. 1024; pages * page_size < 2^47                  */
     int64_t heads;      /* key/value heads, 1 .. 4096                                              */
