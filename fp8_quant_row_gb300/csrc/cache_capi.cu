@@ -219,15 +219,6 @@ fp8q_status launch_read_dim(const fp8q::ReadParams& p, int64_t head_dim, cudaStr
 // fit the registers.
 int attn_columns(int64_t group, int64_t head_dim) { return group > 8 && head_dim <= 128 ? 2 : 1; }
 
-int attn_warps(const fp8q_paged_cache& c) {
-  return c.head_dim * (c.type == FP8Q_BF16 ? 2 : 1) >= 512 ? 4 : 8;
-}
-
-// CTAs an SM (AttnLayout::kCtas).
-int attn_ctas(const fp8q_paged_cache& c, int nt) {
-  return c.head_dim * (c.type == FP8Q_BF16 ? 2 : 1) <= 128 && nt == 1 ? 2 : 1;
-}
-
 struct AttnShape {
   int nt, blocks, warps, grid, segments;
   bool join;  // sequences may be long enough for several CTAs
@@ -241,9 +232,9 @@ AttnShape attn_shape(const fp8q_paged_cache& c, int64_t batch, int64_t q_heads, 
   s.blocks = int((group + 8 * s.nt - 1) / (8 * s.nt));
   const int64_t most = width * (c.page_size / 16);  // tiles of a sequence
   const int64_t segments = batch * c.heads * s.blocks;
-  s.warps = attn_warps(c);
+  s.warps = fp8q::attn_warps(c.type, int(c.head_dim), s.nt);
   s.segments = int(segments);
-  s.grid = int(std::min<int64_t>(sms * attn_ctas(c, s.nt), segments * std::max<int64_t>(most, 1)));
+  s.grid = int(std::min<int64_t>(sms * fp8q::attn_ctas(c.type, int(c.head_dim), s.nt), segments * std::max<int64_t>(most, 1)));
   s.join = most > s.warps;  // (AttnSplit: by tile only then)
   return s;
 }

@@ -69,11 +69,20 @@ struct AttnParams {
 
 constexpr float kAttnNone = -1e30f;  // the maximum before any token
 
+// Warps of a CTA and CTAs an SM: sixteen warps where their registers (accumulators D / 4 NT, queries
+// as many) leave room for that, else eight to twelve. (Two blocks of heads of 64: 12 warps 46.7 us, eight
+// 56.5, at 32 x 8000 tokens of 64 over 4 heads.)
+constexpr int attn_warps(int type, int d, int nt) {
+  return (type == kCacheBf16 ? 2 : 1) * d >= 512 || (d == 64 && nt == 2) ? 4 : 8;
+}
+constexpr int attn_ctas(int type, int d, int nt) {
+  return d == 64 && nt == 2 ? 3 : (type == kCacheBf16 ? 2 : 1) * d <= 128 && nt == 1 ? 2 : 1;
+}
+
 template <int TYPE, int D, int NT>
 struct AttnLayout {
   static constexpr int E = TYPE == kCacheBf16 ? 2 : 1;
-  static constexpr int kWarps = D * E >= 512 ? 4 : 8;
-  static constexpr int kCtas = D * E <= 128 && NT == 1 ? 2 : 1;  // an SM
+  static constexpr int kWarps = attn_warps(TYPE, D, NT), kCtas = attn_ctas(TYPE, D, NT);
   static constexpr int KP = D * E / 64;   // 16-byte pieces of a key row a lane (four lanes a row)
   static constexpr int VB = D * E >= 128 ? 16 : 8;  // bytes of a value piece (eight lanes a row)
   static constexpr int VP = D * E / (8 * VB);
@@ -87,7 +96,7 @@ struct AttnLayout {
   static constexpr int kItems = NT * MT * 2;       // pairs of values a lane holds of a piece
   static constexpr int kPiece = kItems * 64;       // values of a piece: 8 NT heads
   static constexpr int kStats = kWarps * 2 * (8 * NT * 20 + 8);  // of the CTA's pieces
-  static constexpr int kMost = kCtas == 2 ? 115200 : 232448;
+  static constexpr int kMost = 233472 / kCtas - 1024 - (233472 / kCtas) % 128;  // a CTA's share of an SM's
   static constexpr int kRoom = (kMost - kStats) / (kWarps * (kStage + kScales + 8));
   static constexpr int kStages = kRoom < 6 ? kRoom : 6;
   static constexpr int kRing = kStages * kStage;
@@ -301,7 +310,6 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
   float2* total = stats + 2 * W * 8 * NT;                            // of a piece's segment
   float* factor = reinterpret_cast<float*>(total + 2 * W * 8 * NT);  // of a piece in its segment
   int2* open = reinterpret_cast<int2*>(factor + 2 * W * 8 * NT);     // [warp][first, last]
-  allow_dependents();
   if (lane == 0) {
     if (warp == 0) {  // the copies' descriptions, ahead of their first use
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
@@ -312,6 +320,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
   }
   __syncwarp();
   wait_for_producers();
+  allow_dependents();  // (not before: the join reads the lengths while this kernel runs)
 
   const AttnScan scan = attn_scan(P);
   const AttnSplit split = attn_split<W>(P, scan);
@@ -777,54 +786,52 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
   // first, ...), only its last can be a warp's first
   if (lane == 0) open[2 * warp] = open_first, open[2 * warp + 1] = open_last;
   __syncthreads();
+  // each lane a piece: which of them are of its segment
+  static_assert(2 * W <= 32, "a lane for each piece");
+  const int2 piece = lane < 2 * W ? open[lane] : make_int2(-1, 0);
+  const unsigned alike = __match_any_sync(0xffffffffu, piece.x >= 0 ? piece.x : -1 - lane);
   // a thread for each piece and head: the segment's maximum and sum, the piece's factor
 #pragma unroll 1
   for (int e = threadIdx.x; e < 2 * W * 8 * NT; e += W * 32) {
-    const int seg = open[e / (8 * NT)].x;
-    if (seg < 0) continue;
+    const int p = e / (8 * NT);
+    const unsigned mask = __shfl_sync(0xffffffffu, alike, p);
     const float2* ml = stats + e % (8 * NT);
     float top = kAttnNone, sum = 0.0f;
 #pragma unroll 4
     for (int q = 0; q < 2 * W; ++q)
-      if (open[q].x == seg) top = fmaxf(top, ml[q * (8 * NT)].x);
+      if ((mask >> q) & 1) top = fmaxf(top, ml[q * (8 * NT)].x);
 #pragma unroll 4
     for (int q = 0; q < 2 * W; ++q)
-      if (open[q].x == seg) sum += ex2(ml[q * (8 * NT)].x - top) * ml[q * (8 * NT)].y;
+      if ((mask >> q) & 1) sum += ex2(ml[q * (8 * NT)].x - top) * ml[q * (8 * NT)].y;
     factor[e] = ex2(stats[e].x - top);
     total[e] = make_float2(top, sum);
   }
   __syncthreads();
-  int seen = -1;
+  unsigned leaders = __ballot_sync(0xffffffffu, piece.x >= 0 && (alike & ((1u << lane) - 1)) == 0);
 #pragma unroll 1
-  for (int p0 = 0; p0 < 2 * W; ++p0) {
-    const int2 first = open[p0];
-    if (first.x < 0 || first.x == seen) continue;
-    seen = first.x;
-    const AttnSegment s = attn_segment(P, seen);
+  for (; leaders; leaders &= leaders - 1) {
+    const int p0 = __ffs(leaders) - 1;
+    const unsigned mask = __shfl_sync(0xffffffffu, alike, p0);
+    const int p1 = 31 - __clz(mask);  // its last piece
+    const AttnSegment s = attn_segment(P, __shfl_sync(0xffffffffu, piece.x, p0));
+    const int starts = __shfl_sync(0xffffffffu, piece.y, p0) & 1;
+    const bool whole = starts && (__shfl_sync(0xffffffffu, piece.y, p1) & 2);
     const int live = min(8 * NT, P.group - s.block * 8 * NT);
-    int tail = -1, ends = 0;  // its last piece where that is a warp's first
-#pragma unroll 4
-    for (int q = 0; q < 2 * W; ++q)
-      if (open[q].x == seen) {
-        ends = open[q].y & 2;
-        if (q % 2 == 0) tail = q;
-      }
-    const bool starts = first.y & 1, whole = starts && ends;
     const int slot = 2 * blockIdx.x + starts;  // where it goes on in other CTAs
 #pragma unroll 1
     for (int i = warp; i < L::kItems; i += W) {
       const int n = (i / (2 * MT)) * 8 + 2 * c + (i & 1), at = i * 32 + lane;
       if (n >= live) continue;
       float2 acc = make_float2(0.0f, 0.0f);
-      if (tail >= 0) {
+      if ((p1 & 1) == 0) {  // a warp's first
         const float2 v = reinterpret_cast<const float2*>(
-            P.part_o + (int64_t(blockIdx.x) * W + (tail >> 1)) * L::kPiece)[at];
-        const float f = factor[tail * (8 * NT) + n];
+            P.part_o + (int64_t(blockIdx.x) * W + (p1 >> 1)) * L::kPiece)[at];
+        const float f = factor[p1 * (8 * NT) + n];
         acc = make_float2(f * v.x, f * v.y);
       }
 #pragma unroll 4
       for (int w = 0; w < W; ++w)
-        if (open[2 * w + 1].x == seen) {
+        if ((mask >> (2 * w + 1)) & 1) {
           const float2 v = reinterpret_cast<const float2*>(attn_smem + w * L::kRing)[at];
           const float f = factor[(2 * w + 1) * (8 * NT) + n];
           acc.x += f * v.x;
@@ -863,46 +870,51 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   using L = AttnLayout<TYPE, D, NT>;
   __shared__ float2 sums[kJoinWarps][kJoinItems][32];
   __shared__ float2 stats[kJoinWarps][kJoinItems][4];
-  wait_for_producers();
-  allow_dependents();
+  // Which pieces there are is found while the attention kernel runs: it began once the kernels before
+  // it were complete, so the lengths are there.
   const AttnScan scan = attn_scan(P);
   const AttnSplit split = attn_split<L::kWarps>(P, scan);
-  if (split.mode != kByTile) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int quota = split.quota * L::kWarps;  // of a CTA
   const bool by_segment = P.segments <= P.grid;
-  // the sequence, and the segment's first weighted tile
-  const int64_t t = (int64_t(blockIdx.x) + 1) * quota - 1;  // the CTA's last tile
-  AttnSegment s;
-  int64_t first;
-  int count;
+  AttnSegment s = {0, 0, 0};
+  int64_t first = 0;  // the segment's first weighted tile
+  int count = 0;
   if (by_segment) {
     s = attn_segment(P, blockIdx.x);
-    const int per = (P.batch + 31) >> 5;
-    int before = __shfl_sync(0xffffffffu, scan.incl - scan.mine, s.b / per);
+    const int per = (P.batch + 31) >> 5, owner = int(uint32_t(s.b) / uint32_t(per));
+    int before = __shfl_sync(0xffffffffu, scan.incl - scan.mine, owner);
 #pragma unroll 1
-    for (int i = s.b / per * per; i < s.b; ++i) before += attn_weight(attn_span(P, i));
+    for (int i = owner * per; i < s.b; ++i) before += attn_weight(attn_span(P, i));
     count = attn_weight(attn_span(P, s.b));
-    if (count == 0) return;
     first = int64_t(before) * P.heads + int64_t(s.h * P.blocks + s.block) * count;
   } else {
-    if (t >= int64_t(scan.total) * P.heads) return;
-    const AttnPlace at = attn_find(P, scan, int(fast_div(t, P.by_heads)));
-    count = attn_weight(attn_span(P, at.b));
-    const uint32_t hb = uint32_t(t - int64_t(at.before) * P.heads) / uint32_t(count);
-    s = attn_segment(P, int(hb));
-    s.b = at.b;
-    first = int64_t(at.before) * P.heads + int64_t(hb) * count;
-    if (first + kAttnExtra < int64_t(blockIdx.x) * quota) return;  // began in an earlier CTA
+    const int64_t t = (int64_t(blockIdx.x) + 1) * quota - 1;  // the CTA's last tile
+    if (t < int64_t(scan.total) * P.heads) {
+      const AttnPlace at = attn_find(P, scan, int(fast_div(t, P.by_heads)));
+      count = attn_weight(attn_span(P, at.b));
+      const uint32_t hb = uint32_t(t - int64_t(at.before) * P.heads) / uint32_t(count);
+      s = attn_segment(P, int(hb));
+      s.b = at.b;
+      first = int64_t(at.before) * P.heads + int64_t(hb) * count;
+    }
   }
-  const int c0 = int((first + kAttnExtra) / quota), pieces = int((first + count - 1) / quota) - c0 + 1;
-  if (pieces == 1 || (!by_segment && c0 != int(blockIdx.x))) return;
+  const int64_t end = first + count - 1;
+  const int c0 = end < UINT32_MAX ? int(uint32_t(first + kAttnExtra) / uint32_t(quota))
+                                  : int((first + kAttnExtra) / quota);
+  const int c1 = end < UINT32_MAX ? int(uint32_t(end) / uint32_t(quota)) : int(end / quota);
+  // (a segment that began in an earlier CTA is joined there)
+  const int pieces =
+      split.mode == kByTile && count > 0 && (by_segment || c0 == int(blockIdx.x)) ? c1 - c0 + 1 : 0;
+  wait_for_producers();
+  allow_dependents();
+  if (pieces < 2) return;
   const int live = min(8 * NT, P.group - s.block * 8 * NT);
   const int item0 = blockIdx.y * kJoinItems;
   float2 ml[kJoinItems], acc[kJoinItems];
 #pragma unroll
   for (int i = 0; i < kJoinItems; ++i) ml[i] = make_float2(kAttnNone, 0.0f), acc[i] = make_float2(0.0f, 0.0f);
-#pragma unroll 2
+#pragma unroll 4
   for (int p = warp; p < pieces; p += kJoinWarps) {
     const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);  // the first piece is its CTA's last
     const float2* from = reinterpret_cast<const float2*>(
