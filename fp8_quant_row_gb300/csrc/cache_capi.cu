@@ -143,7 +143,8 @@ fp8q_status launch_heads(fp8q::HeadsParams p, const DeviceInfo& dev, cudaStream_
   // time for the angles and the barrier.
   p.group_tokens = 1;
   int64_t best = INT64_MAX;
-  for (int t = 1; t <= fp8q::kHeadsTokens; t *= 2) {
+  const int most = std::min(fp8q::kHeadsTokens, 2 * fp8q::kHeadsAngles * fp8q::kHeadsThreads / D);
+  for (int t = 1; t <= most; t *= 2) {
     const int64_t rounds = ((p.tokens + t - 1) / t + resident - 1) / resident;
     const int64_t cost = rounds * ((steps * t + kWarps - 1) / kWarps + 3);
     if (cost < best) best = cost, p.group_tokens = t;

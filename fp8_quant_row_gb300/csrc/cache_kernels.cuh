@@ -122,18 +122,6 @@ __device__ __forceinline__ void cp_async_if(uint32_t dst, const void* src, bool 
                  : "memory");
 }
 
-// The same where `in` is known to hold for ALL.
-template <int BYTES, bool ALL>
-__device__ __forceinline__ void cp_async_part(uint32_t dst, const void* src, bool in) {
-  if (!ALL)
-    cp_async_if<BYTES>(dst, src, in);
-  else if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
-                 : "memory");
-}
-
 __device__ __forceinline__ uint4 lds_words(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -184,8 +172,9 @@ __device__ __forceinline__ void store_row(const f2 (&a)[4], const f2 (&b)[4], in
   }
 }
 
-// A CTA takes groups of T tokens, 8 / T warps a token. The group's angles are formed once, a thread
-// each, into one of two buffers (one barrier a group); then each warp takes steps of 32 / (D / 16)
+// A CTA takes groups of T tokens, 8 / T warps a token. A group's angles are formed once, a thread one
+// or two, into one of two buffers while the group before it is worked on (its positions are asked for
+// before that), with one barrier a group. Each warp takes steps of 32 / (D / 16)
 // heads, q's first, then k's and v's. A step's rows come through a ring of the warp's own (cp.async,
 // each lane the pieces that it reads), two steps ahead of the current one and on into the next group.
 // `parts` CTAs share a token's steps where there are few tokens. CACHE: k and v go to the cache (else
@@ -204,14 +193,14 @@ template <int N>
 struct Kind {
   static constexpr int value = N;
 };
-constexpr int kHeadsThreads = 256, kHeadsWarps = 8, kHeadsTokens = 8, kHeadsStages = 3;
+constexpr int kHeadsThreads = 256, kHeadsWarps = 8, kHeadsTokens = 8, kHeadsStages = 3, kHeadsAngles = 2;
 
 template <int D, int ROPE, bool CACHE, int TYPE>
 __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_constant__ HeadsParams P) {
   constexpr int LPH = D / 16, HPW = 32 / LPH, PAIRS = D / 2;
   __shared__ RopeTable table;
-  __shared__ __align__(16) float cos_s[2][ROPE ? kHeadsTokens * PAIRS : 1];
-  __shared__ __align__(16) float sin_s[2][ROPE ? kHeadsTokens * PAIRS : 1];
+  __shared__ __align__(16) float cos_s[2][ROPE ? kHeadsAngles * kHeadsThreads : 1];
+  __shared__ __align__(16) float sin_s[2][ROPE ? kHeadsAngles * kHeadsThreads : 1];
   __shared__ uint4 ring_s[kHeadsWarps][kHeadsStages][2][32];
   __shared__ float4 weight_s[2][D / 4];  // q's, k's: values 0-3 of each chunk, then values 4-7
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / LPH, u = lane % LPH;
@@ -291,24 +280,34 @@ __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_co
           __uint_as_float(wv[j] << 16);
   }
   __syncthreads();
-  int buffer = 0, stage = 0;
-  for (int64_t group = blockIdx.x / P.parts; group < groups; group += grid, buffer ^= 1) {
-    const int64_t token = group * T + mine;
-    const bool exists = token < P.tokens;
-    int64_t slot = 0;
-    if (CACHE && exists) slot = P.slots[token];
+  // The thread's angles of the group to come, and this warp's slot there.
+  int64_t position[kHeadsAngles] = {}, slot_next = 0;
+  auto ask = [&](int64_t group) {
+    if (group >= groups) return;
     if constexpr (ROPE != kRopeNone) {
-      const int count = int(min(int64_t(T), P.tokens - group * T)) * pairs;
-      for (int i = threadIdx.x; i < count; i += kHeadsThreads) {
-        const int t = i / pairs, pair = i - t * pairs;
-        const uint64_t turn =
-            uint64_t(rope_position(P.rope, table.axis[pair], group * T + t)) * table.step[pair];
-        turn_cos_sin(uint32_t(turn >> 32), cos_s[buffer][t * PAIRS + pair],
-                     sin_s[buffer][t * PAIRS + pair]);
+#pragma unroll
+      for (int j = 0; j < kHeadsAngles; ++j) {
+        const int i = threadIdx.x + j * kHeadsThreads, t = i / PAIRS, pair = i % PAIRS;
+        if (t < T && pair < pairs && group * T + t < P.tokens)
+          position[j] = rope_position(P.rope, table.axis[pair], group * T + t);
       }
-      __syncthreads();
     }
-    if (!exists) continue;
+    if (CACHE && group * T + mine < P.tokens) slot_next = P.slots[group * T + mine];
+  };
+  auto form = [&](int buffer) {
+    if constexpr (ROPE != kRopeNone) {
+#pragma unroll
+      for (int j = 0; j < kHeadsAngles; ++j) {
+        const int i = threadIdx.x + j * kHeadsThreads, t = i / PAIRS, pair = i % PAIRS;
+        if (t < T && pair < pairs)
+          turn_cos_sin(uint32_t((uint64_t(position[j]) * table.step[pair]) >> 32), cos_s[buffer][i],
+                       sin_s[buffer][i]);
+      }
+    }
+  };
+  int stage = 0;
+  auto work = [&](int64_t token, int64_t slot, int buffer) {
+    if (token >= P.tokens) return;
     // cos and sin of the lane's pairs, two to a word pair
     f2 cs[ROPE ? 4 : 1], sn[ROPE ? 4 : 1];
     if constexpr (ROPE != kRopeNone) {
@@ -428,6 +427,16 @@ __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_co
     run(Kind<0>(), 0, q_steps, P.q_heads);
     run(Kind<1>(), q_steps, q_steps + kv_steps, P.kv_heads);
     if constexpr (CACHE) run(Kind<2>(), q_steps + kv_steps, steps, P.kv_heads);
+  };
+  int buffer = 0;
+  ask(blockIdx.x / P.parts);
+  form(0);
+  for (int64_t group = blockIdx.x / P.parts; group < groups; group += grid, buffer ^= 1) {
+    const int64_t token = group * T + mine, slot = slot_next;
+    if (ROPE != kRopeNone) __syncthreads();
+    ask(group + grid);
+    work(token, slot, buffer);
+    form(buffer ^ 1);
   }
 }
 
