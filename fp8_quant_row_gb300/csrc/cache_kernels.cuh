@@ -486,10 +486,14 @@ __device__ __forceinline__ uint4 dequant8(uint2 w, float s) {
 }
 
 // A CTA takes 16 output rows, that is tokens: their places are looked up once, then each lane copies
-// eight values of one head's row, tokens first (a page holds a head's tokens side by side).
+// 16 bytes of one head's row at a time, tokens first (a page holds a head's tokens side by side), four
+// of them under way at once.
+constexpr int kReadAhead = 4;
+
 template <int D, int TYPE>
 __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_constant__ ReadParams P) {
-  constexpr int E = TYPE == kCacheBf16 ? 2 : 1, LPR = D / 8;
+  constexpr bool QUANT = TYPE != kCacheBf16;
+  constexpr int E = QUANT ? 1 : 2, LPR = D * E / 16;  // lanes a row
   __shared__ int64_t page_s[kReadRows];
   __shared__ int at_s[kReadRows];
   wait_for_producers();
@@ -519,27 +523,42 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_c
   __syncthreads();
   const int H = P.cache.heads;
   const int work = 2 * H * kReadRows * LPR;
-  for (int i = threadIdx.x; i < work; i += kReadThreads) {
-    const int u = i % LPR, r = (i / LPR) % kReadRows, hk = i / (LPR * kReadRows);
-    const int h = hk >> 1;
-    const bool is_v = hk & 1;
-    const int64_t page = page_s[r];
-    if (page == -1) continue;  // not a row of any sequence
-    uint4 out = make_uint4(0, 0, 0, 0);
-    if (page >= 0) {
-      const int64_t at = int64_t(h) * P.cache.page_size + at_s[r];
-      const uint8_t* src = (is_v ? P.cache.v + page * P.cache.v_stride
-                                 : P.cache.k + page * P.cache.k_stride) + (at * D + u * 8) * E;
-      if (TYPE == kCacheBf16) {
-        out = ld_stream(reinterpret_cast<const uint4*>(src));
-      } else {
-        const float s = is_v ? P.cache.v_scale[page * P.cache.vs_stride + at]
-                             : P.cache.k_scale[page * P.cache.ks_stride + at];
-        out = dequant8<TYPE>(__ldcs(reinterpret_cast<const uint2*>(src)), s);
+  for (int i0 = threadIdx.x; i0 < work; i0 += kReadThreads * kReadAhead) {
+    uint4 x[kReadAhead];
+    float s[kReadAhead];
+    uint16_t* dst[kReadAhead];
+#pragma unroll
+    for (int j = 0; j < kReadAhead; ++j) {
+      const int i = i0 + j * kReadThreads;
+      const int u = i % LPR, r = (i / LPR) % kReadRows, hk = i / (LPR * kReadRows);
+      const int h = hk >> 1;
+      const bool is_v = hk & 1;
+      const int64_t page = i < work ? page_s[r] : -1;
+      x[j] = make_uint4(0, 0, 0, 0);
+      s[j] = 0.0f;
+      // (-1: not a row of any sequence)
+      dst[j] = page == -1 ? nullptr : (is_v ? P.v : P.k) + ((row0 + r) * H + h) * D + u * (16 / E);
+      if (page >= 0) {
+        const int64_t at = int64_t(h) * P.cache.page_size + at_s[r];
+        const uint8_t* src = (is_v ? P.cache.v + page * P.cache.v_stride
+                                   : P.cache.k + page * P.cache.k_stride) + at * (D * E) + u * 16;
+        x[j] = ld_stream(reinterpret_cast<const uint4*>(src));
+        if (QUANT)
+          s[j] = is_v ? P.cache.v_scale[page * P.cache.vs_stride + at]
+                      : P.cache.k_scale[page * P.cache.ks_stride + at];
       }
     }
-    uint16_t* dst = (is_v ? P.v : P.k) + ((row0 + r) * H + h) * D + u * 8;
-    st_stream(reinterpret_cast<uint4*>(dst), out);
+#pragma unroll
+    for (int j = 0; j < kReadAhead; ++j) {
+      if (!dst[j]) continue;
+      uint4* to = reinterpret_cast<uint4*>(dst[j]);
+      if (QUANT) {
+        st_stream(to, dequant8<TYPE>(make_uint2(x[j].x, x[j].y), s[j]));
+        st_stream(to + 1, dequant8<TYPE>(make_uint2(x[j].z, x[j].w), s[j]));
+      } else {
+        st_stream(to, x[j]);
+      }
+    }
   }
 }
 

@@ -818,9 +818,9 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
     const bool whole = starts && (__shfl_sync(0xffffffffu, piece.y, p1) & 2);
     const int live = min(8 * NT, P.group - s.block * 8 * NT);
     const int slot = 2 * blockIdx.x + starts;  // where it goes on in other CTAs
-#pragma unroll 1
-    for (int i = warp; i < L::kItems; i += W) {
-      const int n = (i / (2 * MT)) * 8 + 2 * c + (i & 1), at = i * 32 + lane;
+#pragma unroll
+    for (int i0 = 0; i0 < L::kItems / W; ++i0) {
+      const int i = i0 * W + warp, n = (i / (2 * MT)) * 8 + 2 * c + (i & 1), at = i * 32 + lane;
       if (n >= live) continue;
       float2 acc = make_float2(0.0f, 0.0f);
       if ((p1 & 1) == 0) {  // a warp's first
