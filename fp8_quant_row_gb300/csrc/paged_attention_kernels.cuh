@@ -109,8 +109,8 @@ struct AttnSpan {
   int lo, hi, first, n;
 };
 // Where tiles are shared out, a segment counts as so many more: its queries, page lookups and
-// accumulators cost a warp about that (33 sequences of 1 .. 2000 tokens, 8 heads: 38.8 us with 0).
-constexpr int kAttnExtra = 3;
+// accumulators cost a warp about that (33 sequences of 1 .. 2000 tokens, 8 heads: 24.3 us, 25.4 with 3).
+constexpr int kAttnExtra = 8;
 __device__ __forceinline__ int attn_weight(const AttnSpan& s) { return s.n ? s.n + kAttnExtra : 0; }
 
 __device__ __forceinline__ AttnSpan attn_span(const AttnParams& P, int b) {
