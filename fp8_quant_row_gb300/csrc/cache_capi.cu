@@ -221,7 +221,7 @@ fp8q_status launch_read_dim(const fp8q::ReadParams& p, int64_t head_dim, cudaStr
 int attn_columns(int64_t group, int64_t head_dim) { return group > 8 && head_dim <= 128 ? 2 : 1; }
 
 struct AttnShape {
-  int nt, blocks, warps, grid, segments;
+  int nt, blocks, warps, grid, ctas, segments;
   bool join;  // sequences may be long enough for several CTAs
 };
 
@@ -236,6 +236,9 @@ AttnShape attn_shape(const fp8q_paged_cache& c, int64_t batch, int64_t q_heads, 
   s.warps = fp8q::attn_warps(c.type, int(c.head_dim), s.nt);
   s.segments = int(segments);
   s.grid = int(std::min<int64_t>(sms * fp8q::attn_ctas(c.type, int(c.head_dim), s.nt), segments * std::max<int64_t>(most, 1)));
+  // (as many tiles a warp as kMuchWork at least, if every sequence fills its table)
+  const bool much = segments * most >= int64_t(fp8q::kMuchWork) * s.grid * s.warps;
+  s.ctas = s.grid * (much && 2 * segments >= s.grid && (s.nt == 1 || c.type == FP8Q_BF16) ? 2 : 1);
   s.join = most > s.warps;  // (AttnSplit: by tile only then)
   return s;
 }
@@ -254,9 +257,9 @@ fp8q_status check_attention(const fp8q_paged_cache& c, int64_t batch, int64_t q_
 }
 
 // A slot for each warp and two for each CTA (AttnParams::part_o, part_ml).
-int64_t workspace_slots(const AttnShape& s) { return int64_t(s.grid) * (s.warps + 2); }
+int64_t workspace_slots(const AttnShape& s) { return int64_t(s.ctas) * (s.warps + 2); }
 int64_t workspace_bytes_of(const AttnShape& s, int64_t head_dim) {
-  return s.join ? (workspace_slots(s) * head_dim + int64_t(2) * s.grid * 2) * 8 * s.nt * 4 : 0;
+  return s.join ? (workspace_slots(s) * head_dim + int64_t(2) * s.ctas * 2) * 8 * s.nt * 4 : 0;
 }
 
 fp8q::FastDiv fast_div_by(int64_t d) { return fp8q::FastDiv{d == 1 ? 0 : UINT64_MAX / uint64_t(d) + 1}; }
@@ -294,11 +297,11 @@ fp8q_status launch_attention(const fp8q::AttnParams& p, const AttnShape& s, cuda
   if (st != FP8Q_OK) return st;
   st = tile_map<L>(&map_v, p.cache.v, p.cache.v_stride, p.cache);
   if (st != FP8Q_OK) return st;
-  st = launch(fn, dim3(unsigned(s.grid)), dim3(L::kWarps * 32), size_t(L::kBytes), stream, p, map_k,
+  st = launch(fn, dim3(unsigned(s.ctas)), dim3(L::kWarps * 32), size_t(L::kBytes), stream, p, map_k,
               map_v);
   if (st != FP8Q_OK || !s.join) return st;
   return launch(fp8q::attn_join_kernel<TYPE, D, NT>,
-                dim3(unsigned(std::min(p.segments, p.grid)), L::kItems / fp8q::kJoinItems),
+                dim3(unsigned(std::min(p.segments, p.ctas)), L::kItems / fp8q::kJoinItems),
                 dim3(fp8q::kJoinWarps * 32), 0, stream, p);
 }
 
@@ -562,6 +565,7 @@ fp8q_status fp8q_paged_attention(void* out, float* lse, const void* q, int64_t q
   p.group = int(q_heads / cache->heads);
   p.blocks = s.blocks;
   p.grid = s.grid;
+  p.ctas = s.ctas;
   p.segments = s.segments;
   p.heads = int(cache->heads) * s.blocks;
   p.warp_rounds = int((int64_t(s.segments) + int64_t(s.grid) * s.warps - 1) / (int64_t(s.grid) * s.warps));

@@ -58,7 +58,7 @@ struct AttnParams {
   float2* part_ml;
   int batch, width, window;  // width: pages a sequence may have
   int q_heads, group, blocks;  // heads a key/value head; blocks of 8 NT of them
-  int grid;             // CTAs of the attention kernel
+  int grid, ctas;       // CTAs that are resident at once; all: as many, or twice as many
   int segments, heads;  // heads: blocks of heads a sequence
   int warp_rounds;      // segments a warp, if each warp takes whole ones
   FastDiv by_warps, by_heads, by_blocks;  // by grid * warps, by heads, by blocks
@@ -181,22 +181,52 @@ __device__ __forceinline__ AttnPlace attn_find(const AttnParams& P, const AttnSc
 //   kByWarp     each warp whole segments
 // Costs in tiles of a warp (about 0.5 us). Never by tile where no sequence has more tiles than a CTA
 // has warps: the host launches no join then.
+// SMs do not draw on the memory alike: with equal shares of long sequences the slowest quarter of them
+// takes 15% longer than the rest. So the host launches twice the resident CTAs where there may be
+// much work, and if there is, the first half takes kFirstShare of it and the second, launched as the
+// first ones end, the rest in small shares (64 x 4000 tokens, 16 heads of bf16: 318 us, 338 with equal
+// shares; 32 x 16000, E4M3 175 and 186; shares of 0.84 to 0.92 within 2%). Not for few segments, whose
+// last would fall into hundreds of pieces (1 x 131072: 79 us, 55 with equal shares), nor for two blocks
+// of 8-bit heads, which are bound by instructions.
 constexpr int kByTile = 0, kBySegment = 1, kByWarp = 2;
-constexpr int kCostJoin = 8, kCostMerge = 2;
+constexpr int kCostJoin = 8, kCostMerge = 2, kMuchWork = 20;
+constexpr float kFirstShare = 0.9f;
 struct AttnSplit {
-  int mode, quota;  // quota: by tile, of a warp
+  int mode, quota, rest;  // quota: by tile, of a warp of the first CTAs; rest: of the others
 };
 template <int W>
 __device__ __forceinline__ AttnSplit attn_split(const AttnParams& P, const AttnScan& scan) {
   AttnSplit s;
   s.quota = max(int(fast_div(int64_t(scan.total) * P.heads + (P.grid * W - 1), P.by_warps)), 1);
+  s.rest = 0;
   const int by_tile = scan.most <= W ? INT32_MAX : s.quota + kCostJoin;
   const int by_segment =
       P.segments <= P.grid ? (scan.most + W - 1) / W + kCostMerge : INT32_MAX;
   const int by_warp = (P.warp_rounds == 1 ? 0 : s.quota) + scan.most;
   s.mode = by_segment <= by_tile ? kBySegment : kByTile;
   if (by_warp < min(by_tile, by_segment)) s.mode = kByWarp;
+  if (s.mode == kByTile && P.ctas > P.grid && s.quota >= kMuchWork) {
+    const int first = __float2int_ru(__fmul_rn(float(s.quota), kFirstShare));
+    s.rest = s.quota - first;  // (the quota was rounded up: together they reach the end)
+    s.quota = first;
+  }
   return s;
+}
+
+// By tile: a CTA's first weighted tile, and its warps' quota.
+template <int W>
+__device__ __forceinline__ int64_t attn_begin(const AttnParams& P, const AttnSplit& s, int cta) {
+  const int over = max(cta - P.grid, 0);
+  return (int64_t(cta - over) * s.quota + int64_t(over) * s.rest) * W;
+}
+// The CTA that has a weighted tile.
+template <int W>
+__device__ __forceinline__ int attn_cta(const AttnParams& P, const AttnSplit& s, int64_t t) {
+  const int64_t border = int64_t(P.grid) * s.quota * W;
+  const uint32_t size = uint32_t(t < border ? s.quota : s.rest) * W;
+  const int64_t at = t < border ? t : t - border;
+  const int n = at <= UINT32_MAX ? int(uint32_t(at) / size) : int(at / size);
+  return t < border ? n : n + P.grid;
 }
 
 // A segment: sequence, key/value head, block of that head's queries.
@@ -326,6 +356,10 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
   const AttnSplit split = attn_split<W>(P, scan);
   const bool by_warp = split.mode == kByWarp;
   const int unit = blockIdx.x * W + warp, units = P.grid * W;
+  // the second half, where there is nothing for it
+  if (int(blockIdx.x) >= P.grid &&
+      (split.rest == 0 || attn_begin<W>(P, split, blockIdx.x) >= int64_t(scan.total) * P.heads))
+    return;
 
   // This warp's share: from weighted tile `at0` of segment s0 on, `share` of them (by warp: segment
   // after segment). `extra` ones stand before a segment's tiles.
@@ -333,9 +367,11 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
   AttnSegment s0 = {0, 0, 0};
   int at0 = 0, share = 0;
   if (split.mode == kByTile) {
-    const int64_t t0 = int64_t(split.quota) * unit, all = int64_t(scan.total) * P.heads;
+    const int quota = int(blockIdx.x) < P.grid ? split.quota : split.rest;
+    const int64_t t0 = attn_begin<W>(P, split, blockIdx.x) + int64_t(quota) * warp;
+    const int64_t all = int64_t(scan.total) * P.heads;
     if (t0 < all) {
-      share = int(min(int64_t(split.quota), all - t0));
+      share = int(min(int64_t(quota), all - t0));
       const AttnPlace at = attn_find(P, scan, int(fast_div(t0, P.by_heads)));
       const uint32_t local = uint32_t(t0 - int64_t(at.before) * P.heads);
       const uint32_t n = attn_weight(attn_span(P, at.b)), hb = local / n;
@@ -842,14 +878,14 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
         attn_store<TYPE, D>(P, int64_t(s.b) * P.q_heads + s.h * P.group + s.block * 8 * NT + n,
                             (i >> 1) % MT, r, acc, ml);
       } else {
-        reinterpret_cast<float2*>(P.part_o + int64_t(units + slot) * L::kPiece)[at] = acc;
+        reinterpret_cast<float2*>(P.part_o + (int64_t(P.ctas) * W + slot) * L::kPiece)[at] = acc;
         if (r == 0 && ((i >> 1) % MT) == 0) P.part_ml[slot * (8 * NT) + n] = ml;
       }
     }
   }
   // sequences without tokens: no warp has them
 #pragma unroll 1
-  for (int64_t seg = unit; seg < P.segments; seg += units) {
+  for (int64_t seg = unit; int(blockIdx.x) < P.grid && seg < P.segments; seg += units) {
     const AttnSegment s = attn_segment(P, int(seg));
     if (attn_span(P, s.b).n > 0) continue;
     const int64_t row = int64_t(s.b) * P.q_heads + s.h * P.group + s.block * 8 * NT;
@@ -875,8 +911,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   const AttnScan scan = attn_scan(P);
   const AttnSplit split = attn_split<L::kWarps>(P, scan);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const int quota = split.quota * L::kWarps;  // of a CTA
-  const bool by_segment = P.segments <= P.grid;
+  constexpr int W = L::kWarps;
+  const bool by_segment = P.segments <= P.ctas;
   AttnSegment s = {0, 0, 0};
   int64_t first = 0;  // the segment's first weighted tile
   int count = 0;
@@ -889,8 +925,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     count = attn_weight(attn_span(P, s.b));
     first = int64_t(before) * P.heads + int64_t(s.h * P.blocks + s.block) * count;
   } else {
-    const int64_t t = (int64_t(blockIdx.x) + 1) * quota - 1;  // the CTA's last tile
-    if (t < int64_t(scan.total) * P.heads) {
+    const int64_t t = attn_begin<W>(P, split, blockIdx.x + 1) - 1;  // the CTA's last tile
+    if (t < int64_t(scan.total) * P.heads && (split.rest > 0 || int(blockIdx.x) < P.grid)) {
       const AttnPlace at = attn_find(P, scan, int(fast_div(t, P.by_heads)));
       count = attn_weight(attn_span(P, at.b));
       const uint32_t hb = uint32_t(t - int64_t(at.before) * P.heads) / uint32_t(count);
@@ -899,13 +935,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
       first = int64_t(at.before) * P.heads + int64_t(hb) * count;
     }
   }
-  const int64_t end = first + count - 1;
-  const int c0 = end < UINT32_MAX ? int(uint32_t(first + kAttnExtra) / uint32_t(quota))
-                                  : int((first + kAttnExtra) / quota);
-  const int c1 = end < UINT32_MAX ? int(uint32_t(end) / uint32_t(quota)) : int(end / quota);
+  const bool some = split.mode == kByTile && count > 0;
+  const int c0 = some ? attn_cta<W>(P, split, first + kAttnExtra) : 0;
+  const int c1 = some ? attn_cta<W>(P, split, first + count - 1) : 0;
   // (a segment that began in an earlier CTA is joined there)
-  const int pieces =
-      split.mode == kByTile && count > 0 && (by_segment || c0 == int(blockIdx.x)) ? c1 - c0 + 1 : 0;
+  const int pieces = some && (by_segment || c0 == int(blockIdx.x)) ? c1 - c0 + 1 : 0;
   wait_for_producers();
   allow_dependents();
   if (pieces < 2) return;
@@ -918,7 +952,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   for (int p = warp; p < pieces; p += kJoinWarps) {
     const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);  // the first piece is its CTA's last
     const float2* from = reinterpret_cast<const float2*>(
-        P.part_o + (int64_t(P.grid) * L::kWarps + slot) * L::kPiece) + item0 * 32 + lane;
+        P.part_o + (int64_t(P.ctas) * W + slot) * L::kPiece) + item0 * 32 + lane;
     const float2* stat = P.part_ml + slot * (8 * NT) + (item0 / (2 * L::MT)) * 8 + 2 * c;
     // (the four items are of one block of eight heads, in turn its heads 2c and 2c + 1)
     const bool in0 = (item0 / (2 * L::MT)) * 8 + 2 * c < live, in1 = (item0 / (2 * L::MT)) * 8 + 2 * c + 1 < live;

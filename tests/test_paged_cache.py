@@ -513,6 +513,20 @@ def test_paged_attention_splits(dtype, lengths, heads, kv):
 
 @gpu
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("batch,high,heads,kv", [(40, 9000, 8, 4), (90, 6000, 8, 8), (19, 20000, 80, 8)],
+                         ids=["some", "many", "wide"])
+def test_paged_attention_much_work(dtype, batch, high, heads, kv):
+    """Enough tiles for a second round of CTAs with smaller shares: fewer and more segments than CTAs,
+    lengths of zero among them, the longest first and last, and twice the same bits."""
+    lengths = [round(high * (i * 7 % batch) / (batch - 1)) for i in range(batch)]
+    lengths[1], lengths[batch // 2], lengths[-1] = 0, 0, high
+    q, cache, table, lens, o, lse = attention_case(dtype, 64, heads, kv, 64, lengths)
+    again = fq.paged_attention(q, cache, table, lens, return_lse=True)
+    assert same(again[0], o) and same(again[1], lse)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("window", [1, 15, 16, 100, 1000, 10 ** 6])
 def test_paged_attention_window(dtype, window):
     attention_case(dtype, 128, 8, 2, 16, [1, 15, 16, 17, 101, 0, 1500, 20000], window=window, joint=True)
