@@ -176,12 +176,16 @@ __device__ __forceinline__ void store_row(const f2 (&a)[4], const f2 (&b)[4], in
 // or two, into one of two buffers while the group before it is worked on (its positions are asked for
 // before that), with one barrier a group. Each warp takes steps of 32 / (D / 16)
 // heads, q's first, then k's and v's. A step's rows come through a ring of the warp's own (cp.async,
-// each lane the pieces that it reads), two steps ahead of the current one and on into the next group.
+// each lane the pieces that it reads), three steps ahead of the current one and on into the next group.
 // `parts` CTAs share a token's steps where there are few tokens. CACHE: k and v go to the cache (else
 // k to k_out).
 // A lane's chunks: with rotated halves a pair of chunks `half` apart (of the first 2 half of a row; of
 // the others one from either half of them), so that the pairs (i, i + pairs) lie in one lane for a part
 // of a head too; else one from either half of the row.
+// Bound: the issue of instructions before HBM, so two CTAs an SM with registers for all: at three a
+// third more instructions went into forming addresses again (8192 tokens of 48 + 8 heads into E4M3:
+// 53.4 us, 49.2 with two).
+
 // 1 / sqrt(x): the approximate instruction (2^-22) and one Newton step, within an ulp.
 __device__ __forceinline__ float heads_rsqrt(float x) {
   float y;
@@ -193,10 +197,10 @@ template <int N>
 struct Kind {
   static constexpr int value = N;
 };
-constexpr int kHeadsThreads = 256, kHeadsWarps = 8, kHeadsTokens = 8, kHeadsStages = 3, kHeadsAngles = 2;
+constexpr int kHeadsThreads = 256, kHeadsWarps = 8, kHeadsTokens = 8, kHeadsStages = 4, kHeadsAngles = 2;
 
 template <int D, int ROPE, bool CACHE, int TYPE>
-__global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_constant__ HeadsParams P) {
+__global__ void __launch_bounds__(kHeadsThreads, 2) heads_kernel(const __grid_constant__ HeadsParams P) {
   constexpr int LPH = D / 16, HPW = 32 / LPH, PAIRS = D / 2;
   __shared__ RopeTable table;
   __shared__ __align__(16) float cos_s[2][ROPE ? kHeadsAngles * kHeadsThreads : 1];
@@ -382,14 +386,16 @@ __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const __grid_co
           }
         }
         if constexpr (KIND < 2 && ROPE == kRopeHalves) {
-          if (u < half) {
+          auto turn = [&]() {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const f2 x = a[j], y = b[j];
               a[j] = fma2(y, neg2(sn[j]), mul2(x, cs[j]));
               b[j] = fma2(x, sn[j], mul2(y, cs[j]));
             }
-          }
+          };
+          if (half == LPH) turn();  // (no lane apart)
+          else if (u < half) turn();
         } else if constexpr (KIND < 2 && ROPE == kRopePairs) {
           auto turn = [&](f2 v, int j) {
             const float c = (j & 1) ? f2_hi(cs[j / 2]) : f2_lo(cs[j / 2]);
