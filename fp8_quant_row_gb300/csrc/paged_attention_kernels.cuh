@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
           uint32_t e = max(m & 0xFFFFu, m >> 16) >> 7;  // exponent of the head's largest value
           e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
           e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-          e = min(max(e, 10u), 244u);  // (smaller ones count as zero in effect, larger ones overflow)
+          e = min(max(e, 10u), 254u);
           const float up = __uint_as_float((254u - e + 8u) << 23);  // 2^(127 + 8 - e): below 2^9
 #pragma unroll
           for (int i = 0; i < KP * KS; ++i)

@@ -382,6 +382,7 @@ typedef struct fp8q_rotary {
  *   q_weight, k_weight  in [head_dim] bf16, 16-byte aligned; NULL: no norm
  *   rotary        NULL: no rotation
  *   q_heads, kv_heads   1 .. 4096;  head_dim 64, 128 or 256;  eps > 0 where there is a weight
+ *   A head whose squares leave fp32 (|x| from about 2^60) is normed to NaN.
  *   Aliasing: an output may not overlap another output or an input, but for the exact case above.
  */
 fp8q_status fp8q_qk_norm_rope(void* q_out, int64_t q_out_ld, void* k_out, int64_t k_out_ld,
@@ -443,7 +444,8 @@ fp8q_status fp8q_cache_read(void* k_out, void* v_out, const fp8q_paged_cache* ca
  *                   are read. A page outside the cache is left out of the sums and sets
  *                   FP8Q_DEVERR_BAD_INDEX
  *   lengths     in  [batch] int32 (device); clamped to 0 .. width*page_size
- *   q_heads     a multiple of cache->heads;  width*page_size < 2^30;  scale finite;  window >= 0
+ *   q_heads     a multiple of cache->heads;  width*page_size < 2^30;  scale finite;  window >= 0;
+ *               (width*page_size/16 + 8) * max(q_heads, batch) < 2^31
  *   workspace   device buffer of workspace_bytes >= fp8q_paged_attention_workspace(...), 16-byte
  *               aligned, contents irrelevant before and after; calls that may run at the same time
  *               need one each. NULL where that size is 0

@@ -542,6 +542,54 @@ def test_paged_attention_scales(dtype, scale, q_scale):
 
 @gpu
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("page", [16, 80, 176, 512, 1024])
+def test_paged_attention_page_sizes(dtype, page):
+    """Pages of 1, 5, 11, 32 and 64 tiles, more of them in a sequence than a warp looks up at once."""
+    attention_case(dtype, 64, 4, 2, page, [40 * page, 33 * page + 1, 32 * page, page - 1, 5], joint=page == 80)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("dim", [64, 256])
+def test_no_pages_no_sequences(dtype, dim):
+    """Caches without a page, tables without a column, batches without a sequence."""
+    empty, some = fq.paged_cache(0, 16, 2, dim, dtype=dtype), fq.paged_cache(3, 16, 2, dim, dtype=dtype)
+    q = normal((5, 4, dim), 1)
+    lens = torch.tensor([0, 7, -3, 10 ** 9, 1], dtype=torch.int32, device="cuda")
+    none = torch.zeros(5, 0, dtype=torch.int32, device="cuda")
+    for cache, table in ((empty, none), (some, none), (empty, torch.zeros(5, 40, dtype=torch.int32, device="cuda"))):
+        o, lse = fq.paged_attention(q, cache, table, lens, return_lse=True)
+        assert not o.any() and bool((lse == -math.inf).all())
+    assert fq.paged_attention(q[:0], some, none[:0], lens[:0]).shape == (0, 4, dim)
+    k, v = fq.cache_read(empty, none, torch.zeros(6, dtype=torch.int64, device="cuda"), 0)
+    assert k.shape == (0, 2, dim)
+    assert fq.cache_write(q[:0, :2], q[:0, :2], some, torch.zeros(0, dtype=torch.int64, device="cuda"), q=q[:0]).shape == (0, 4, dim)
+    assert not some.k.view(torch.uint8).any()
+    # lengths beyond the table count as its pages' tokens
+    k64, v64, _ = filled(some, torch.tensor([[0, 2, 1]], dtype=torch.int32, device="cuda"), [48], 2)
+    o = fq.paged_attention(q[:1], some, torch.tensor([[0, 2, 1]], dtype=torch.int32, device="cuda"), lens[3:4])
+    check_attention(o[0], None, q[0], k64, v64, dim ** -0.5, dtype)
+    assert fq.device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("power", [-130, -100, 120])
+def test_paged_attention_far_queries(dtype, power):
+    """Queries near the ends of bf16's range, with a scale that brings the logits back (in fp32)."""
+    q_scale = 2.0 ** power
+    q = (normal((1, 8, 128), 1).float() * q_scale).to(BF16)
+    cache = fq.paged_cache(8, 16, 2, 128, dtype=dtype)
+    table = scattered(1, 8, 8, 1)
+    k64, v64, _ = filled(cache, table, [100], 2)
+    scale = 2.0 ** min(-power, 120) * 0.1
+    lens = torch.tensor([100], dtype=torch.int32, device="cuda")
+    o, lse = fq.paged_attention(q, cache, table, lens, scale=scale, return_lse=True)
+    check_attention(o[0], lse[0], q[0], k64, v64, scale, dtype)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
 def test_paged_attention_heads_of_unlike_size(dtype):
     """Query heads of one block that differ by 2^30, rising logits (the maximum is raised again and
     again), and values whose scales rise and fall by 2^40."""
