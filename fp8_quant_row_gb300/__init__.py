@@ -238,10 +238,15 @@ def _native():
         loader = importlib.machinery.ExtensionFileLoader(name, NATIVE)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
         loader.exec_module(m)
-        m.init(*(ctypes.cast(getattr(_capi.lib(), f), ctypes.c_void_p).value for f in
-                 ("fp8q_rms_norm_quant", "fp8q_silu_mul_quant", "fp8q_int8_matmul",
-                  "fp8q_qk_norm_rope", "fp8q_cache_write", "fp8q_cache_read",
-                  "fp8q_paged_attention", "fp8q_paged_attention_workspace")), _capi.check)
+
+        def address(name):
+            return ctypes.cast(getattr(_capi.lib(), name), ctypes.c_void_p).value
+
+        m.init(*(address(f) for f in
+                 ("fp8q_rms_norm_quant", "fp8q_silu_mul_quant", "fp8q_int8_matmul")), _capi.check)
+        m.init_cache(*(address(f) for f in
+                       ("fp8q_qk_norm_rope", "fp8q_cache_write", "fp8q_cache_read",
+                        "fp8q_paged_attention", "fp8q_paged_attention_workspace")))
         _native_module = m
     return _native_module
 

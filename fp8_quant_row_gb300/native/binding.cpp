@@ -645,23 +645,32 @@ PyObject* paged_attention(PyObject* const* arg, Py_ssize_t n) {
   return l ? results({&o, &*l}) : o.object();
 }
 
-// init(...): the C entry points' addresses and the error raiser
+// init(rms, silu, matmul, check): the C entry points' addresses and the error raiser
 PyObject* init(PyObject* const* arg, Py_ssize_t n) {
-  arguments(n, 9);
-  void* f[8];
-  for (int i = 0; i < 8; ++i) f[i] = PyLong_AsVoidPtr(arg[i]);
+  arguments(n, 4);
+  void* f[3];
+  for (int i = 0; i < 3; ++i) f[i] = PyLong_AsVoidPtr(arg[i]);
   if (PyErr_Occurred()) throw Refused{};
   g_rms = reinterpret_cast<RmsFn>(f[0]);
   g_silu = reinterpret_cast<SiluFn>(f[1]);
   g_matmul = reinterpret_cast<MatmulFn>(f[2]);
-  g_rope = reinterpret_cast<RopeFn>(f[3]);
-  g_write = reinterpret_cast<WriteFn>(f[4]);
-  g_read = reinterpret_cast<ReadFn>(f[5]);
-  g_attn = reinterpret_cast<AttnFn>(f[6]);
-  g_attn_size = reinterpret_cast<AttnSizeFn>(f[7]);
   Py_XDECREF(g_check);
-  Py_INCREF(arg[8]);
-  g_check = arg[8];
+  Py_INCREF(arg[3]);
+  g_check = arg[3];
+  Py_RETURN_NONE;
+}
+
+// init_cache(rope, write, read, attention, workspace): the paged cache's entry points
+PyObject* init_cache(PyObject* const* arg, Py_ssize_t n) {
+  arguments(n, 5);
+  void* f[5];
+  for (int i = 0; i < 5; ++i) f[i] = PyLong_AsVoidPtr(arg[i]);
+  if (PyErr_Occurred()) throw Refused{};
+  g_rope = reinterpret_cast<RopeFn>(f[0]);
+  g_write = reinterpret_cast<WriteFn>(f[1]);
+  g_read = reinterpret_cast<ReadFn>(f[2]);
+  g_attn = reinterpret_cast<AttnFn>(f[3]);
+  g_attn_size = reinterpret_cast<AttnSizeFn>(f[4]);
   Py_RETURN_NONE;
 }
 
@@ -683,7 +692,8 @@ PyMethodDef method(const char* name) {
           METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<init>("init"), method<rms_norm_quant>("rms_norm_quant"),
+PyMethodDef g_methods[] = {method<init>("init"), method<init_cache>("init_cache"),
+                           method<rms_norm_quant>("rms_norm_quant"),
                            method<silu_mul_quant>("silu_mul_quant"),
                            method<int8_matmul>("int8_matmul"), method<qk_norm_rope>("qk_norm_rope"),
                            method<cache_write>("cache_write"), method<cache_read>("cache_read"),
