@@ -250,8 +250,10 @@ fp8q_status check_attention(const fp8q_paged_cache& c, int64_t batch, int64_t q_
   if (batch < 0 || batch > (1 << 20) || q_heads < 1 || q_heads > kMaxHeads * 64 ||
       q_heads % c.heads != 0 || batch * q_heads > INT32_MAX || width < 0 ||
       width * c.page_size >= (int64_t(1) << 30) ||
-      // (tiles of a sequence over all heads, of all sequences, with what the split adds to each)
-      (width * (c.page_size / 16) + fp8q::kAttnExtra) * std::max(q_heads, batch) > INT32_MAX)
+      // (tiles of a sequence over all heads, of all sequences, with what the split adds to each; of all
+      // over all, so that a warp's share stays below 2^31 where 512 warps are resident)
+      (width * (c.page_size / 16) + fp8q::kAttnExtra) * std::max(q_heads, batch) > INT32_MAX ||
+      (width * (c.page_size / 16) + fp8q::kAttnExtra) * batch * q_heads > (int64_t(1) << 40))
     return FP8Q_ERR_SHAPE;
   return FP8Q_OK;
 }

@@ -672,6 +672,70 @@ def test_paged_attention_repeats_captured_and_on_other_streams(dtype):
 
 
 @gpu
+def test_threads_at_once():
+    """Several Python threads, each on a stream of its own, writing to caches of their own and attending:
+    the results of one after the other."""
+    import threading
+
+    def one(i):
+        dtype = TYPES[i % 3]
+        lengths = [100 + 900 * i, 17, 0, 2000]
+        cache = fq.paged_cache(300, 16, 2, 128, dtype=dtype)
+        pages = torch.arange(300, device="cuda").int()
+        table = pages[:280].view(4, 70) if i < 2 else pages[:290].view(2, 145)
+        lengths = lengths[-len(table):]
+        lengths = [min(n, table.shape[1] * 16) for n in lengths]
+        filled(cache, table, lengths, i)
+        q = normal((len(lengths), 16, 128), 50 + i)
+        lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        return [fq.paged_attention(q, cache, table, lens) for _ in range(10)]
+
+    want = [one(i) for i in range(4)]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got[i] = one(i)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(want, got):
+        assert all(same(x, a[0]) for x in a + b)
+    assert fq.device_error() == 0
+
+
+@gpu
+def test_captured_writes():
+    """cache_write and cache_read in a graph: new inputs, slots and positions at each replay."""
+    d, h, kv, t = 128, 4, 2, 33
+    cache = fq.paged_cache(8, 16, kv, d)
+    f, _ = fq.rotary_axes((d,))
+    q, k, v = normal((t, h, d), 1), normal((t, kv, d), 2), normal((t, kv, d), 3)
+    slots, pos = torch.arange(t, device="cuda"), torch.arange(t, device="cuda")
+    table = torch.arange(8, device="cuda").int()[None]
+    off = torch.tensor([0, 128], device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qo = fq.cache_write(k, v, cache, slots, q=q, inv_freq=f, positions=pos)
+        ko, vo = fq.cache_read(cache, table, off, 128)
+    for i in range(3):
+        k.copy_(normal((t, kv, d), 10 + i)), q.copy_(normal((t, h, d), 20 + i))
+        slots.copy_(torch.randperm(128, generator=gen(i), device="cuda")[:t]), pos.add_(1000 * i)
+        g.replay()
+        again = fq.PagedCache(*(x.clone() for x in cache))
+        want = fq.cache_write(k, v, again, slots, q=q, inv_freq=f, positions=pos)
+        assert same(want, qo) and same(again.k, cache.k) and same(again.k_scale, cache.k_scale)
+        for x, y in zip(fq.cache_read(again, table, off, 128), (ko, vo)):
+            assert same(x, y)
+
+
+@gpu
 def test_offsets_beyond_32_bits():
     """A cache of 9 GB of keys: bytes, values and scales past 2^32."""
     for dtype, pages in ((INT8, 1 << 16), (BF16, 1 << 15)):
@@ -897,6 +961,36 @@ def test_bindings_refuse_what_is_not_on_a_gpu():
     for bad in ((), (3,), (0,), (16, -2)):
         with pytest.raises(ValueError):
             fq.rotary_axes(bad, device="cpu")
+
+
+from tests.test_launch_shapes import fake  # noqa: E402,F401
+
+
+def test_attention_launches(fake):  # noqa: F811
+    """Seen through the stand-in for the runtime: a join only where a sequence may have more tiles than a
+    CTA has warps, as many CTAs as are resident, twice as many where there may be much work."""
+    got = fake("""
+    class Cache(ctypes.Structure):
+        _fields_ = [(n, P) for n in ("k", "v", "ks", "vs")] + [(n, I64) for n in ("a", "b", "c", "d", "pages", "page", "heads", "dim")] + [("type", ctypes.c_int)]
+    L.fp8q_paged_attention_workspace.restype = I64
+    def call(batch, width, heads, kv, dim=128, type=1, page=16):
+        n = kv * page
+        c = Cache(1 << 40, 2 << 40, 3 << 40, 4 << 40, n * dim, n * dim, n, n, 1000, page, kv, dim, type)
+        before = F.fake_launches()
+        size = L.fp8q_paged_attention_workspace(ctypes.byref(c), I64(batch), I64(heads), I64(width))
+        st = L.fp8q_paged_attention(P(5 << 40), None, P(6 << 40), I64(heads * dim), ctypes.byref(c), P(7 << 40), I64(width), I64(width),
+                                    P(8 << 40), I64(batch), I64(heads), ctypes.c_float(1), I64(0), P(9 << 40), I64(size), None)
+        n = F.fake_launches() - before
+        l = F.fake_launch_at(before)
+        return [st, n, l.grid, l.block, size > 0]
+    print(json.dumps([call(1, 8, 32, 8), call(1, 9, 32, 8), call(2, 1, 32, 8), call(64, 512, 32, 8), call(1, 8192, 32, 8),
+                      call(64, 512, 128, 8), call(64, 512, 128, 8, type=2), call(1, 4, 32, 8, dim=256, type=2), call(1, 5, 32, 8, dim=256, type=2),
+                      call(4096, 65528, 4096, 8), call(4096, 65529, 4096, 8), call(0, 8, 32, 8)]))
+    """)
+    assert got[-1][:2] == [0, 0]  # no sequences: no launch
+    assert got[-3][:2] == [0, 2] and got[-2][:2] == [SHAPE, 0]  # 2^40 tiles of heads, and more
+    assert got[:-3] == [[0, 1, 64, 256, False], [0, 2, 72, 256, True], [0, 1, 16, 256, False], [0, 2, 608, 256, True],
+                   [0, 2, 304, 256, True], [0, 2, 152, 256, True], [0, 2, 304, 256, True], [0, 1, 32, 128, False], [0, 2, 40, 128, True]]
 
 
 def test_rotary_axes():
