@@ -396,6 +396,15 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                : "memory");
 }
 
+// True in one lane of the warp (all lanes take part).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // True once the phase with parity `parity` has completed (the thread may be suspended for a
 // hardware-chosen time inside the instruction while it is pending).
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {

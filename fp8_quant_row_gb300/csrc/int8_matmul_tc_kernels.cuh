@@ -198,13 +198,6 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b_lo, ui
         "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(ADD ? 1u : add)
         : "memory");
 }
-__device__ __forceinline__ bool elect_lane() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
 // One arrival on `bar` (in both CTAs of a pair) once the matrix instructions so far are done.
 template <int CG>
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
