@@ -288,7 +288,7 @@ template <int TYPE, int D, int NT>
 fp8q_status launch_attention(const fp8q::AttnParams& p, const AttnShape& s, cudaStream_t stream) {
   using L = fp8q::AttnLayout<TYPE, D, NT>;
   static_assert(L::kStages >= 2 && L::kStages <= 16 && L::kBytes <= L::kMost, "a ring fits its SM's share");
-  static_assert(L::kItems % fp8q::kJoinItems == 0, "whole CTAs of the join");
+  static_assert(L::kItems % (2 * fp8q::kJoinItems) == 0, "whole CTAs of the join");
   auto* fn = fp8q::paged_attention_kernel<TYPE, D, NT>;
   int bps = 0;
   fp8q_status st = blocks_per_sm(reinterpret_cast<const void*>(fn), L::kWarps * 32, L::kBytes, &bps);
@@ -304,8 +304,13 @@ fp8q_status launch_attention(const fp8q::AttnParams& p, const AttnShape& s, cuda
   st = launch(fn, dim3(unsigned(s.ctas)), dim3(L::kWarps * 32), size_t(L::kBytes), stream, p, map_k,
               map_v);
   if (st != FP8Q_OK || !s.join) return st;
-  return launch(fp8q::attn_join_kernel<TYPE, D, NT>,
-                dim3(unsigned(std::min(p.segments, p.ctas)), L::kItems / fp8q::kJoinItems),
+  // Two parts of a piece a CTA of the join where there would be more than kJoinMany CTAs an SM.
+  constexpr int kGroups = L::kItems / fp8q::kJoinItems;
+  const int segments = std::min(p.segments, p.ctas);
+  if (segments * kGroups > fp8q::kJoinMany * (p.grid / L::kCtas))
+    return launch(fp8q::attn_join_kernel<TYPE, D, NT, 2>, dim3(unsigned(segments), kGroups / 2),
+                  dim3(fp8q::kJoinWarps * 32), 0, stream, p);
+  return launch(fp8q::attn_join_kernel<TYPE, D, NT, 1>, dim3(unsigned(segments), kGroups),
                 dim3(fp8q::kJoinWarps * 32), 0, stream, p);
 }
 

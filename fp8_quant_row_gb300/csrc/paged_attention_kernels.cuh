@@ -911,10 +911,14 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
 
 // Joins the pieces of segments that several CTAs shared. A CTA for each segment, or, where there are
 // more of them, for each CTA of the attention kernel and the segment that goes on behind it, and for
-// four of a piece's pairs of values; its warps take the pieces in turn.
-constexpr int kJoinWarps = 8, kJoinItems = 4;
+// four of a piece's pairs of values, times PARTS; a part's warps take the pieces in turn. Many CTAs take
+// long to launch, few segments have many pieces: two parts where one would make more than kJoinMany CTAs
+// an SM (64 sequences of 3 to 8192 tokens, 8 heads: 101.1 us, 104.4 with one part, 101.7 with four;
+// 33 of 1 to 2000 22.2, 24.8, 23.0), else one (20 of 1000 to 8000, int8, 640 CTAs: 46.6 us, 47.7 with
+// two, 52.5 with four; 1 x 131072, 64 heads over 8, int8, 55.9 and 59.8 with two).
+constexpr int kJoinWarps = 8, kJoinItems = 4, kJoinMany = 5;
 
-template <int TYPE, int D, int NT>
+template <int TYPE, int D, int NT, int PARTS>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams P) {
   using L = AttnLayout<TYPE, D, NT>;
   __shared__ float2 sums[kJoinWarps][kJoinItems][32];
@@ -957,12 +961,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   allow_dependents();
   if (pieces < 2) return;
   const int live = min(8 * NT, P.group - s.block * 8 * NT);
-  const int item0 = blockIdx.y * kJoinItems;
+  constexpr int kTurns = kJoinWarps / PARTS;  // warps of a part
+  const int item0 = (blockIdx.y * PARTS + warp % PARTS) * kJoinItems;
   float2 ml[kJoinItems], acc[kJoinItems];
 #pragma unroll
   for (int i = 0; i < kJoinItems; ++i) ml[i] = make_float2(kAttnNone, 0.0f), acc[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-  for (int p = warp; p < pieces; p += kJoinWarps) {
+  for (int p = warp / PARTS; p < pieces; p += kTurns) {
     const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);  // the first piece is its CTA's last
     const float2* from = reinterpret_cast<const float2*>(
         P.part_o + (int64_t(P.ctas) * W + slot) * L::kPiece) + item0 * 32 + lane;
@@ -986,22 +991,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     if (r == 0) stats[warp][i][c] = ml[i];
   }
   __syncthreads();
-  if (warp >= kJoinItems) return;
-  const int it = item0 + warp, n = (it / (2 * L::MT)) * 8 + 2 * c + (it & 1);
-  if (n >= live) return;
-  float top = kAttnNone, sum = 0.0f;
-  float2 a = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int e = warp; e < PARTS * kJoinItems; e += kJoinWarps) {
+    const int part = e / kJoinItems, i = e % kJoinItems;
+    const int it = blockIdx.y * (PARTS * kJoinItems) + e, n = (it / (2 * L::MT)) * 8 + 2 * c + (it & 1);
+    if (n >= live) continue;
+    float top = kAttnNone, sum = 0.0f;
+    float2 a = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, stats[w][warp][c].x);
+    for (int w = part; w < kJoinWarps; w += PARTS) top = fmaxf(top, stats[w][i][c].x);
 #pragma unroll 4
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float f = ex2(stats[w][warp][c].x - top);
-    sum += f * stats[w][warp][c].y;
-    a.x += f * sums[w][warp][lane].x;
-    a.y += f * sums[w][warp][lane].y;
+    for (int w = part; w < kJoinWarps; w += PARTS) {
+      const float f = ex2(stats[w][i][c].x - top);
+      sum += f * stats[w][i][c].y;
+      a.x += f * sums[w][i][lane].x;
+      a.y += f * sums[w][i][lane].y;
+    }
+    attn_store<TYPE, D>(P, int64_t(s.b) * P.q_heads + s.h * P.group + s.block * 8 * NT + n,
+                        (it >> 1) % L::MT, r, a, make_float2(top, sum));
   }
-  attn_store<TYPE, D>(P, int64_t(s.b) * P.q_heads + s.h * P.group + s.block * 8 * NT + n,
-                      (it >> 1) % L::MT, r, a, make_float2(top, sum));
 }
 
 }  // namespace fp8q
