@@ -109,7 +109,7 @@ struct AttnSpan {
   int lo, hi, first, n;
 };
 // Where tiles are shared out, a segment counts as so many more: its queries, page lookups and
-// accumulators cost a warp about that (33 sequences of 1 .. 2000 tokens, 8 heads: 24.3 us, 25.4 with 3).
+// accumulators cost a warp about that (33 sequences of 1 .. 2000 tokens, 8 heads: 22.2 us, 23.5 with 3).
 constexpr int kAttnExtra = 8;
 __device__ __forceinline__ int attn_weight(const AttnSpan& s) { return s.n ? s.n + kAttnExtra : 0; }
 
@@ -183,13 +183,14 @@ __device__ __forceinline__ AttnPlace attn_find(const AttnParams& P, const AttnSc
 // has warps: the host launches no join then.
 // SMs do not draw on the memory alike: with equal shares of long sequences the slowest quarter of them
 // takes 15% longer than the rest. So the host launches twice the resident CTAs where there may be
-// much work, and if there is, the first half takes kFirstShare of it and the second, launched as the
-// first ones end, the rest in small shares (64 x 4000 tokens, 16 heads of bf16: 318 us, 338 with equal
-// shares; 32 x 16000, E4M3 175 and 186; shares of 0.84 to 0.92 within 2%). Not for few segments, whose
-// last would fall into hundreds of pieces (1 x 131072: 79 us, 55 with equal shares), nor for two blocks
-// of 8-bit heads, which are bound by instructions.
+// much work, and if there is (kMuchWork tiles a warp), the first half takes kFirstShare of it and the
+// second, launched as the first ones end, the rest in small shares (64 x 4000 tokens, 16 heads of bf16:
+// 310 us, 328 with equal shares; 32 x 16000, E4M3 168 and 178; shares of 0.86 and 0.94 171 and 176).
+// Not with less, where the pieces cost more than the balance gives (20 sequences of 1000 to 8000, int8,
+// 20 tiles a warp: 46.6 us, 43.3 with equal shares), nor for few segments, whose last would fall into
+// hundreds of pieces (1 x 131072: 79 us, 55 with equal shares), nor for two blocks of 8-bit heads (no gain).
 constexpr int kByTile = 0, kBySegment = 1, kByWarp = 2;
-constexpr int kCostJoin = 8, kCostMerge = 2, kMuchWork = 20;
+constexpr int kCostJoin = 8, kCostMerge = 2, kMuchWork = 40;
 constexpr float kFirstShare = 0.9f;
 struct AttnSplit {
   int mode, quota, rest;  // quota: by tile, of a warp of the first CTAs; rest: of the others
