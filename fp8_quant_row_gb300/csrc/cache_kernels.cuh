@@ -184,7 +184,8 @@ __device__ __forceinline__ void store_row(const f2 (&a)[4], const f2 (&b)[4], in
 // of a head too; else one from either half of the row.
 // Bound: the issue of instructions before HBM, so two CTAs an SM with registers for all: at three a
 // third more instructions went into forming addresses again (8192 tokens of 48 + 8 heads into E4M3:
-// 53.4 us, 49.2 with two).
+// 53.4 us, 49.2 with two). Measured: these 45.3 us (82% of the copy's 6754.5 GB/s), q and k of 4352
+// tokens of 24 + 24 heads over three axes 18.7 (85%; 55% of the issue slots), one token 2.7 to 3.0.
 
 // 1 / sqrt(x): the approximate instruction (2^-22) and one Newton step, within an ulp.
 __device__ __forceinline__ float heads_rsqrt(float x) {
@@ -493,7 +494,9 @@ __device__ __forceinline__ uint4 dequant8(uint2 w, float s) {
 
 // A CTA takes 16 output rows, that is tokens: their places are looked up once, then each lane copies
 // 16 bytes of one head's row at a time, tokens first (a page holds a head's tokens side by side), four
-// of them under way at once.
+// of them under way at once. Measured: 16 sequences of 100 to 16384 tokens of 8 heads, bf16 160 us (100% of
+// the copy's rate), E4M3 135.6 (89%), int8 146 (83%: conversions); 32 rows a CTA the same for these and
+// 4.2 for 3.0 us where there are few, 64 rows 142 and 154.
 constexpr int kReadAhead = 4;
 
 template <int D, int TYPE>
