@@ -513,7 +513,7 @@ def test_paged_attention_splits(dtype, lengths, heads, kv):
 
 @gpu
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
-@pytest.mark.parametrize("batch,high,heads,kv", [(40, 9000, 8, 4), (90, 6000, 8, 8), (19, 20000, 80, 8)],
+@pytest.mark.parametrize("batch,high,heads,kv", [(40, 20000, 8, 4), (90, 6000, 8, 8), (19, 20000, 80, 8)],
                          ids=["some", "many", "wide"])
 def test_paged_attention_much_work(dtype, batch, high, heads, kv):
     """Enough tiles for a second round of CTAs with smaller shares: fewer and more segments than CTAs,
@@ -523,6 +523,15 @@ def test_paged_attention_much_work(dtype, batch, high, heads, kv):
     q, cache, table, lens, o, lse = attention_case(dtype, 64, heads, kv, 64, lengths)
     again = fq.paged_attention(q, cache, table, lens, return_lse=True)
     assert same(again[0], o) and same(again[1], lse)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("dim,batch,high,heads,kv", [(64, 100, 4000, 8, 8), (128, 100, 4000, 8, 8), (256, 50, 8000, 8, 4),
+                                                     (128, 100, 1000, 96, 8), (64, 100, 1000, 30, 3), (64, 400, 300, 2, 2)], ids=str)
+def test_paged_attention_many_segments(dtype, dim, batch, high, heads, kv):
+    """Many segments over several CTAs each: both forms of the join, with small last shares and without."""
+    attention_case(dtype, dim, heads, kv, 64, [high * i // (batch - 1) for i in range(batch)])
 
 
 @gpu
