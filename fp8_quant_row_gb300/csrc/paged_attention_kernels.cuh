@@ -692,7 +692,8 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
               const int e = min(max(int(__float_as_uint(wt) >> 23) & 255, 27), 227);
               float k1 = __uint_as_float(uint32_t(254 + 8 - e) << 23);
               k1 = fminf(k1, __fdividef(kf[j][x], f));
-              gain = __fdividef(k1, kf[j][x]) * f;
+              // (the factors may be more than 2^128 apart where all before counts for nothing)
+              gain = f == 0.0f ? 0.0f : __fdividef(k1, kf[j][x]) * f;
               kf[j][x] = k1;
               w[j][x] = p[j][x] * k1 * vs[0];
               w[j][x + 2] = p[j][x + 2] * k1 * vs[1];

@@ -1,0 +1,77 @@
+"""The paged cache's attention at the ends of its numbers: values, queries and logits near the ends of
+fp32's range, infinities, tables much wider than the sequences."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import fp8_quant_row_gb300 as fq
+from tests.test_paged_cache import (BF16, TYPES, check_attention, garbage, gen, gpu, ids, normal,
+                                    rows_of, same, scattered)
+
+# (sequences, tokens): each sequence a warp's, a CTA's, shared by CTAs and joined. The number of tiles
+# leaves the remainder 0 by 3.
+WHERE = {"warp": (400, 48), "cta": (1, 336), "join": (1, 20016)}
+where = pytest.mark.parametrize("shape", WHERE.values(), ids=WHERE)
+types = pytest.mark.parametrize("dtype", TYPES, ids=ids)
+
+
+def attend(dtype, k, v, q, batch, scale=None):
+    """Writes k, v [batch * n, heads, dim] and attends: (out, log-sum, k and v as stored, in 64 bits)."""
+    n, heads, dim, page = len(k) // batch, k.shape[1], k.shape[2], 16
+    width = -(-n // page)
+    cache = garbage(batch * width, page, heads, dim, dtype)
+    table = scattered(batch, width, batch * width, 7)
+    t = torch.arange(n, device="cuda")
+    slots = (table[:, t // page].long() * page + t % page).flatten()
+    fq.cache_write(k, v, cache, slots)
+    gk, gv, sk, sv = rows_of(cache, slots)
+    k64, v64 = gk.double(), gv.double()
+    if sk is not None:
+        k64, v64 = k64 * sk.double()[..., None], v64 * sv.double()[..., None]
+    lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    o, lse = fq.paged_attention(q, cache, table, lens, scale=scale, return_lse=True)
+    assert fq.device_error() == 0
+    return o, lse, k64, v64
+
+
+def check_all(o, lse, q, k64, v64, scale, dtype, some=5):
+    n = len(k64) // len(q)
+    for b in list(range(len(q)))[::-(-len(q) // some)]:
+        check_attention(o[b], lse[b], q[b], k64[b * n:(b + 1) * n], v64[b * n:(b + 1) * n], scale, dtype)
+    assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all())
+
+
+def check_mean(o, lse, v, logit, size_of_logit):
+    """One sequence whose weights are all the same, v [n, kv heads, dim] those tokens' values. A weight
+    times its value's scale is rounded to fp16 (2^-11; on a grid of 2^-33 of the largest), sums of n / 16
+    steps to 2^-21 each. The logit is a sum of 64 products in four steps of 2^-21 of their magnitudes' sum,
+    the log-sum rounded a few times at its size."""
+    n, kv, dim = v.shape
+    want = v.mean(0).repeat_interleave(len(o) // kv, 0)
+    size = v.abs().mean(0).repeat_interleave(len(o) // kv, 0)
+    largest = v.abs().amax((0, 2)).repeat_interleave(len(o) // kv, 0)[:, None]
+    tol = 2.0 ** -8 * want.abs() + 1.01 * ((2.0 ** -11 + n / 16 * 2.0 ** -21 + 2.0 ** -20) * size + 2.0 ** -33 * largest)
+    err = (o.double() - want).abs()
+    assert bool((err <= tol).all()), (float((err / tol).max()), float(err.max()))
+    ref = logit + math.log(n)
+    assert bool(((lse.double() - ref).abs() <= 4 * 2.0 ** -21 * size_of_logit + 2.0 ** -20 * abs(ref)).all()), (lse.tolist(), ref)
+
+
+@gpu
+@types
+@where
+def test_rising_logits_over_rows_of_zeros(dtype, shape):
+    """Tiles of large values, of zeros and of ordinary ones in turn, each tile's logits 130 powers of two
+    above the last one's: what came before counts for nothing, whatever the factors of its weights. (Weights
+    below 2^-94 of the largest may count as zero: 2^-130 of values of 2^40 here.)"""
+    batch, n = shape
+    tile = (torch.arange(n, device="cuda") // 16).repeat(batch)
+    k = torch.zeros(batch * n, 2, 64, dtype=BF16, device="cuda")
+    k[..., 0] = (90.0 * tile)[:, None].to(BF16)
+    v = normal((batch * n, 2, 64), 1) * torch.tensor([2.0 ** 40, 0.0, 1.0], device="cuda")[tile % 3][:, None, None].to(BF16)
+    q = normal((batch, 4, 64), 2)
+    q[..., 0] = 1.0
+    check_all(*(x := attend(dtype, k, v, q, batch, 1.0))[:2], q, *x[2:], 1.0, dtype)
