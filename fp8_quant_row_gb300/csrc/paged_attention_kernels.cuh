@@ -687,9 +687,10 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
               float wt = fmaxf(p[j][x] * vs[0], p[j][x + 2] * vs[1]);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) wt = fmaxf(wt, __shfl_xor_sync(0xffffffffu, wt, d));
-              // a power of two that takes the tile's largest weight to 2^8 .. 2^9, no larger than
-              // what keeps the sums so far from growing
-              const int e = min(max(int(__float_as_uint(wt) >> 23) & 255, 27), 227);
+              // a power of two that takes the tile's largest weight to 2^8 .. 2^9 (from 2^108, for rows
+              // of zeros, down to 2^-119 at the end of fp32), no larger than what keeps the sums so far
+              // from growing
+              const int e = min(max(int(__float_as_uint(wt) >> 23) & 255, 27), 254);
               float k1 = __uint_as_float(uint32_t(254 + 8 - e) << 23);
               k1 = fminf(k1, __fdividef(kf[j][x], f));
               // (the factors may be more than 2^128 apart where all before counts for nothing)

@@ -8,13 +8,14 @@ import pytest
 import torch
 
 import fp8_quant_row_gb300 as fq
-from tests.test_paged_cache import (BF16, TYPES, check_attention, garbage, gen, gpu, ids, normal,
+from tests.test_paged_cache import (BF16, E4M3, INT8, TYPES, check_attention, garbage, gpu, ids, normal,
                                     rows_of, same, scattered)
 
 # (sequences, tokens): each sequence a warp's, a CTA's, shared by CTAs and joined. The number of tiles
 # leaves the remainder 0 by 3.
 WHERE = {"warp": (400, 48), "cta": (1, 336), "join": (1, 20016)}
 where = pytest.mark.parametrize("shape", WHERE.values(), ids=WHERE)
+eight = pytest.mark.parametrize("dtype", [INT8, E4M3], ids=ids)
 types = pytest.mark.parametrize("dtype", TYPES, ids=ids)
 
 
@@ -75,3 +76,28 @@ def test_rising_logits_over_rows_of_zeros(dtype, shape):
     q = normal((batch, 4, 64), 2)
     q[..., 0] = 1.0
     check_all(*(x := attend(dtype, k, v, q, batch, 1.0))[:2], q, *x[2:], 1.0, dtype)
+
+
+@gpu
+@eight
+@pytest.mark.parametrize("shape", [WHERE["warp"]], ids=["warp"])
+@pytest.mark.parametrize("power", [108, 120, 124])
+def test_large_values(dtype, shape, power):
+    """Values up to the end of bf16's range, ordinary ones beside them."""
+    batch, n = shape
+    k, q = normal((batch * n, 2, 64), 1), normal((batch, 4, 64), 2, 1.5)
+    v = normal((batch * n, 2, 64), 3) * torch.where(torch.arange(batch * n, device="cuda") % 5 < 3, 2.0 ** power, 1.0)[:, None, None].to(BF16)
+    check_all(*(x := attend(dtype, k, v, q, batch))[:2], q, *x[2:], 0.125, dtype)
+
+
+@gpu
+@eight
+@pytest.mark.parametrize("shape", [WHERE["warp"]], ids=["warp"])
+def test_the_largest_values(dtype, shape):
+    """All values bf16's largest: their mean is no larger."""
+    batch, n = shape
+    v = torch.full((batch * n, 2, 64), torch.finfo(BF16).max, dtype=BF16, device="cuda")
+    k, q = normal((batch * n, 2, 64), 1), normal((batch, 2, 64), 2)
+    o, _, _, _ = attend(dtype, k, v, q, batch)
+    # fp16 weights 2^-11, sums at most n / 16 2^-21: less than the half step (2^-9) to either side
+    assert bool((o == torch.finfo(BF16).max).all())
