@@ -59,7 +59,8 @@ struct AttnParams {
   const int32_t* lengths;
   uint16_t* out;  // [batch, q_heads, D]
   float* lse;     // [batch, q_heads] or null
-  // Sums of pieces of segments: values (AttnLayout::kPiece of them) and for each head the maximum
+  // Pieces of segments: their outputs (AttnLayout::kPiece values; divided by their sums, so that
+  // they are no larger than the values they come from) and for each head the maximum
   // (log2 units) and the sum; a slot for each warp's first piece, then two for each CTA.
   float* part_o;
   float2* part_ml;
@@ -320,13 +321,16 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
   return sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Two values of a head's row of the output, from sums over all its tokens.
+// 1 / sum, any finite number for a sum of 0. (No branch: loads are asked for ahead across it.)
+__device__ __forceinline__ float attn_inverse(float sum) {
+  return __fdividef(1.0f, fmaxf(sum, 0x1p-100f));
+}
+
+// Two values of a head's row of the output.
 template <int TYPE, int D>
 __device__ __forceinline__ void attn_store(const AttnParams& P, int64_t row, int block, int r, float2 o,
                                            float2 ml) {
-  const float inv = ml.y == 0.0f ? 0.0f : __fdividef(1.0f, ml.y);
-  *reinterpret_cast<uint32_t*>(P.out + row * D + AttnValues<TYPE, D>::of(block, r)) =
-      pack_bf16x2(o.x * inv, o.y * inv);
+  *reinterpret_cast<uint32_t*>(P.out + row * D + AttnValues<TYPE, D>::of(block, r)) = pack_bf16x2(o.x, o.y);
   if (P.lse && r == 0 && block == 0) P.lse[row] = attn_lse(ml.x, ml.y);
 }
 
@@ -792,7 +796,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         float f = QUANT ? __fdividef(1.0f, kf[j][x]) : 1.0f;
-        if (whole) f = l[j][x] == 0.0f ? 0.0f : __fdividef(f, l[j][x]);
+        f = l[j][x] == 0.0f ? 0.0f : __fdividef(f, l[j][x]);
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[j][i][x] *= f, o[j][i][x + 2] *= f;
       }
@@ -849,7 +853,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
   static_assert(2 * W <= 32, "a lane for each piece");
   const int2 piece = lane < 2 * W ? open[lane] : make_int2(-1, 0);
   const unsigned alike = __match_any_sync(0xffffffffu, piece.x >= 0 ? piece.x : -1 - lane);
-  // a thread for each piece and head: the segment's maximum and sum, the piece's factor
+  // a thread for each piece and head: the segment's maximum and sum, the piece's share
 #pragma unroll 1
   for (int e = threadIdx.x; e < 2 * W * 8 * NT; e += W * 32) {
     const int p = e / (8 * NT);
@@ -862,7 +866,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
 #pragma unroll 4
     for (int q = 0; q < 2 * W; ++q)
       if ((mask >> q) & 1) sum += ex2(ml[q * (8 * NT)].x - top) * ml[q * (8 * NT)].y;
-    factor[e] = ex2(stats[e].x - top);
+    factor[e] = ex2(stats[e].x - top) * stats[e].y * attn_inverse(sum);
     total[e] = make_float2(top, sum);
   }
   __syncthreads();
@@ -932,7 +936,7 @@ template <int TYPE, int D, int NT, int PARTS>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams P) {
   using L = AttnLayout<TYPE, D, NT>;
   __shared__ float2 sums[kJoinWarps][kJoinItems][32];
-  __shared__ float2 stats[kJoinWarps][kJoinItems][4];
+  __shared__ float2 stats[kJoinWarps][2][4];
   // Which pieces there are is found while the attention kernel runs: it began once the kernels before
   // it were complete, so the lengths are there.
   const AttnScan scan = attn_scan(P);
@@ -971,34 +975,58 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   allow_dependents();
   if (pieces < 2) return;
   const int live = min(8 * NT, P.group - s.block * 8 * NT);
+  // Pieces whose loads a warp has under way together: two where segments are few and have many (1 x 2000
+  // tokens: 9.3 us, 11.5 with one), one where the join's CTAs are many and wait for registers (256 x 300:
+  // 33.1 us, 34.1 with two).
+  constexpr int kJoinAhead = PARTS == 2 ? 1 : 2;
   constexpr int kTurns = kJoinWarps / PARTS;  // warps of a part
   const int item0 = (blockIdx.y * PARTS + warp % PARTS) * kJoinItems;
-  float2 ml[kJoinItems], acc[kJoinItems];
+  float2 ml[2] = {{kAttnNone, 0.0f}, {kAttnNone, 0.0f}}, acc[kJoinItems];
 #pragma unroll
-  for (int i = 0; i < kJoinItems; ++i) ml[i] = make_float2(kAttnNone, 0.0f), acc[i] = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-  for (int p = warp / PARTS; p < pieces; p += kTurns) {
-    const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);  // the first piece is its CTA's last
-    const float2* from = reinterpret_cast<const float2*>(
-        P.part_o + (int64_t(P.ctas) * W + slot) * L::kPiece) + item0 * 32 + lane;
-    const float2* stat = P.part_ml + slot * (8 * NT) + (item0 / (2 * L::MT)) * 8 + 2 * c;
-    // (the four items are of one block of eight heads, in turn its heads 2c and 2c + 1)
-    const bool in0 = (item0 / (2 * L::MT)) * 8 + 2 * c < live, in1 = (item0 / (2 * L::MT)) * 8 + 2 * c + 1 < live;
-    const float2 none = make_float2(kAttnNone, 0.0f), zero = make_float2(0.0f, 0.0f);
-    const float2 x[2] = {in0 ? stat[0] : none, in1 ? stat[1] : none};
+  for (int i = 0; i < kJoinItems; ++i) acc[i] = make_float2(0.0f, 0.0f);
+  // (the four items are of one block of eight heads, in turn its heads 2c and 2c + 1)
+  const bool in[2] = {(item0 / (2 * L::MT)) * 8 + 2 * c < live, (item0 / (2 * L::MT)) * 8 + 2 * c + 1 < live};
+#pragma unroll 1
+  for (int p0 = warp / PARTS; p0 < pieces; p0 += kJoinAhead * kTurns) {
+    float2 x[kJoinAhead][2], v[kJoinAhead][kJoinItems];
 #pragma unroll
-    for (int i = 0; i < kJoinItems; ++i) {
-      const float2 v = (i & 1 ? in1 : in0) ? from[i * 32] : zero;
-      const float top = fmaxf(ml[i].x, x[i & 1].x);
-      const float f0 = ex2(ml[i].x - top), f1 = ex2(x[i & 1].x - top);
-      ml[i] = make_float2(top, f0 * ml[i].y + f1 * x[i & 1].y);
-      acc[i] = make_float2(f0 * acc[i].x + f1 * v.x, f0 * acc[i].y + f1 * v.y);
+    for (int k = 0; k < kJoinAhead; ++k) {
+      const int p = p0 + k * kTurns;
+      const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);  // the first piece is its CTA's last
+      const float2* from = reinterpret_cast<const float2*>(
+          P.part_o + (int64_t(P.ctas) * W + slot) * L::kPiece) + item0 * 32 + lane;
+      const float2* stat = P.part_ml + slot * (8 * NT) + (item0 / (2 * L::MT)) * 8 + 2 * c;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) x[k][i] = p < pieces && in[i] ? stat[i] : make_float2(kAttnNone, 0.0f);
+#pragma unroll
+      for (int i = 0; i < kJoinItems; ++i)
+        v[k][i] = p < pieces && in[i & 1] ? from[i * 32] : make_float2(0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float top = ml[i].x;
+#pragma unroll
+      for (int k = 0; k < kJoinAhead; ++k) top = fmaxf(top, x[k][i].x);
+      float old = ex2(ml[i].x - top) * ml[i].y, sum = old;
+#pragma unroll
+      for (int k = 0; k < kJoinAhead; ++k) x[k][i].y *= ex2(x[k][i].x - top), sum += x[k][i].y;
+      ml[i] = make_float2(top, sum);
+      const float inv = attn_inverse(sum);
+      old *= inv;
+#pragma unroll
+      for (int j = i; j < kJoinItems; j += 2) acc[j].x *= old, acc[j].y *= old;
+#pragma unroll
+      for (int k = 0; k < kJoinAhead; ++k) {
+        const float f = x[k][i].y * inv;
+#pragma unroll
+        for (int j = i; j < kJoinItems; j += 2) acc[j].x += f * v[k][j].x, acc[j].y += f * v[k][j].y;
+      }
     }
   }
 #pragma unroll
   for (int i = 0; i < kJoinItems; ++i) {
     sums[warp][i][lane] = acc[i];
-    if (r == 0) stats[warp][i][c] = ml[i];
+    if (r == 0 && i < 2) stats[warp][i][c] = ml[i];
   }
   __syncthreads();
 #pragma unroll
@@ -1008,14 +1036,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     if (n >= live) continue;
     float top = kAttnNone, sum = 0.0f;
     float2 a = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-    for (int w = part; w < kJoinWarps; w += PARTS) top = fmaxf(top, stats[w][i][c].x);
-#pragma unroll 4
-    for (int w = part; w < kJoinWarps; w += PARTS) {
-      const float f = ex2(stats[w][i][c].x - top);
-      sum += f * stats[w][i][c].y;
-      a.x += f * sums[w][i][lane].x;
-      a.y += f * sums[w][i][lane].y;
+    float share[kTurns];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) top = fmaxf(top, stats[k * PARTS + part][i & 1][c].x);
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+      const float2 x = stats[k * PARTS + part][i & 1][c];
+      share[k] = ex2(x.x - top) * x.y;
+      sum += share[k];
+    }
+    const float inv = attn_inverse(sum);
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+      const float f = share[k] * inv;
+      const float2 x = sums[k * PARTS + part][i][lane];
+      a.x += f * x.x;
+      a.y += f * x.y;
     }
     attn_store<TYPE, D>(P, int64_t(s.b) * P.q_heads + s.h * P.group + s.block * 8 * NT + n,
                         (it >> 1) % L::MT, r, a, make_float2(top, sum));

@@ -80,7 +80,7 @@ def test_rising_logits_over_rows_of_zeros(dtype, shape):
 
 @gpu
 @eight
-@pytest.mark.parametrize("shape", [WHERE["warp"]], ids=["warp"])
+@where
 @pytest.mark.parametrize("power", [108, 120, 124])
 def test_large_values(dtype, shape, power):
     """Values up to the end of bf16's range, ordinary ones beside them."""
@@ -92,7 +92,7 @@ def test_large_values(dtype, shape, power):
 
 @gpu
 @eight
-@pytest.mark.parametrize("shape", [WHERE["warp"]], ids=["warp"])
+@where
 def test_the_largest_values(dtype, shape):
     """All values bf16's largest: their mean is no larger."""
     batch, n = shape
