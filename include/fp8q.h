@@ -433,9 +433,8 @@ fp8q_status fp8q_cache_read(void* k_out, void* v_out, const fp8q_paged_cache* ca
  *   s_t = scale * q . k_t,  out = sum_t exp(s_t) v_t / sum_t exp(s_t),  lse = ln sum_t exp(s_t)
  * over t in [max(0, n - window), n) (window 0: all). A sequence without tokens gets zeros and
  * lse -infinity. Logits, maxima and sums are fp32, 8-bit codes exact, a weight times its value's
- * scale is rounded to fp16 (and to a multiple of 2^-33 of the largest; bf16 cache: to 16 bits), the
- * output once to bf16. Keys and values outside
- * the range may hold anything.
+ * scale is rounded to fp16 (and to a multiple of 2^-33 of the largest; bf16 cache: to 16 bits, and
+ * sums to 2^-117), the output once to bf16. Keys and values outside the range may hold anything.
  *
  *   out         out [batch, q_heads, head_dim] bf16, contiguous, 16-byte aligned
  *   lse         out [batch, q_heads] fp32 or NULL

@@ -8,14 +8,13 @@ import pytest
 import torch
 
 import fp8_quant_row_gb300 as fq
-from tests.test_paged_cache import (BF16, E4M3, INT8, TYPES, check_attention, garbage, gpu, ids, normal,
+from tests.test_paged_cache import (BF16, TYPES, check_attention, garbage, gpu, ids, normal,
                                     rows_of, same, scattered)
 
 # (sequences, tokens): each sequence a warp's, a CTA's, shared by CTAs and joined. The number of tiles
 # leaves the remainder 0 by 3.
 WHERE = {"warp": (400, 48), "cta": (1, 336), "join": (1, 20016)}
 where = pytest.mark.parametrize("shape", WHERE.values(), ids=WHERE)
-eight = pytest.mark.parametrize("dtype", [INT8, E4M3], ids=ids)
 types = pytest.mark.parametrize("dtype", TYPES, ids=ids)
 
 
@@ -79,7 +78,7 @@ def test_rising_logits_over_rows_of_zeros(dtype, shape):
 
 
 @gpu
-@eight
+@types
 @where
 @pytest.mark.parametrize("power", [108, 120, 124])
 def test_large_values(dtype, shape, power):
@@ -91,7 +90,18 @@ def test_large_values(dtype, shape, power):
 
 
 @gpu
-@eight
+@types
+@where
+def test_small_values(dtype, shape):
+    """Values of 2^-98, little above what 8-bit rows take for zeros (2^-100)."""
+    batch, n = shape
+    k, q = normal((batch * n, 2, 64), 1), normal((batch, 4, 64), 2, 1.5)
+    v = (normal((batch * n, 2, 64), 3).float() * 2.0 ** -98).to(BF16)
+    check_all(*(x := attend(dtype, k, v, q, batch))[:2], q, *x[2:], 0.125, dtype)
+
+
+@gpu
+@types
 @where
 def test_the_largest_values(dtype, shape):
     """All values bf16's largest: their mean is no larger."""
