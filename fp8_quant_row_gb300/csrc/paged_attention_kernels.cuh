@@ -75,7 +75,9 @@ struct AttnParams {
   int page_tiles;
 };
 
-constexpr float kAttnNone = -1e30f;  // the maximum before any token
+// The maximum before any token: no logit lies below it but -infinity (an infinite maximum would make
+// NaN of the difference with itself).
+constexpr float kAttnNone = -3.402823466e38f;
 
 // Warps of a CTA and CTAs an SM: sixteen warps where their registers (accumulators D / 4 NT, queries
 // as many) leave room for that, else eight to twelve. (Two blocks of heads of 64: 12 warps 46.7 us, eight

@@ -111,3 +111,22 @@ def test_the_largest_values(dtype, shape):
     o, _, _, _ = attend(dtype, k, v, q, batch)
     # fp16 weights 2^-11, sums at most n / 16 2^-21: less than the half step (2^-9) to either side
     assert bool((o == torch.finfo(BF16).max).all())
+
+
+@gpu
+@types
+@where
+@pytest.mark.parametrize("logit", [-1e31, -1e37, -1e38])
+def test_low_logits(dtype, shape, logit):
+    """Every logit far below zero, every other token's twice as far: the mean of the rest's values."""
+    batch, n = shape
+    even = torch.arange(batch * n, device="cuda") % 2 == 0
+    k = torch.zeros(batch * n, 2, 64, dtype=BF16, device="cuda")
+    k[..., 0] = torch.where(even, logit, 2 * logit)[:, None].to(BF16)
+    v = normal((batch * n, 2, 64), 1)
+    q = torch.zeros(batch, 4, 64, dtype=BF16, device="cuda")
+    q[..., 0] = 1.0
+    o, lse, k64, v64 = attend(dtype, k, v, q, batch, 1.0)
+    for b in range(0, batch, 90):
+        at = torch.arange(b * n, (b + 1) * n, 2, device="cuda")
+        check_mean(o[b], lse[b], v64[at], float(k64[0, 0, 0]), abs(float(k64[0, 0, 0])))
