@@ -656,8 +656,9 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          t[j][x] = (s[j][0][x] + s[j][1][x]) * fac[j][x & 1];
-          if (QUANT) t[j][x] *= ks[x >> 1];
+          // (the head's factor with the key's scale first: a far query's sum times its factor may leave
+          // fp32 where the logit does not)
+          t[j][x] = (s[j][0][x] + s[j][1][x]) * (QUANT ? fac[j][x & 1] * ks[x >> 1] : fac[j][x & 1]);
         }
       }
       if (edge) {

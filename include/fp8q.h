@@ -435,6 +435,9 @@ fp8q_status fp8q_cache_read(void* k_out, void* v_out, const fp8q_paged_cache* ca
  * lse -infinity. Logits, maxima and sums are fp32, 8-bit codes exact, a weight times its value's
  * scale is rounded to fp16 (and to a multiple of 2^-33 of the largest; bf16 cache: to 16 bits, and
  * sums to 2^-117), the output once to bf16. Keys and values outside the range may hold anything.
+ * Finite inputs give finite results where, with Q and K the largest |q| and |k|, head_dim * Q * K,
+ * scale times it and scale * Q are below 2^126. A logit of -infinity is a weight of 0 (nothing but
+ * these: as no tokens), one of +infinity or NaN makes its head NaN.
  *
  *   out         out [batch, q_heads, head_dim] bf16, contiguous, 16-byte aligned
  *   lse         out [batch, q_heads] fp32 or NULL

@@ -130,3 +130,23 @@ def test_low_logits(dtype, shape, logit):
     for b in range(0, batch, 90):
         at = torch.arange(b * n, (b + 1) * n, 2, device="cuda")
         check_mean(o[b], lse[b], v64[at], float(k64[0, 0, 0]), abs(float(k64[0, 0, 0])))
+
+
+@gpu
+@types
+@where
+@pytest.mark.parametrize("power", [100, 118, 124])
+def test_far_queries_on_small_keys(dtype, shape, power):
+    """Queries near the end of bf16's range over keys of 2^-90 (alike, so that all weights are): the
+    logits are within fp32, and so is the way to them."""
+    batch, n = shape
+    k = (normal((1, 2, 64), 1).float() * 2.0 ** -90).to(BF16).repeat(batch * n, 1, 1)
+    v = normal((batch * n, 2, 64), 2)
+    one = (normal((1, 4, 64), 3).float() * 2.0 ** power).to(BF16)
+    q = one.repeat(batch, 1, 1)
+    o, lse, k64, v64 = attend(dtype, k, v, q, batch)
+    s, m = (torch.einsum("hgd,hd->hg", x.view(2, 2, 64), y).flatten() / 8 for x, y in
+            ((one[0].double(), k64[0]), (one[0].double().abs(), k64[0].abs())))
+    for b in range(0, batch, 90):
+        for h in range(4):
+            check_mean(o[b, h:h + 1], lse[b, h:h + 1], v64[b * n:(b + 1) * n, h // 2:h // 2 + 1], float(s[h]), float(m[h]))
