@@ -226,17 +226,17 @@ __device__ __forceinline__ AttnSplit attn_split(const AttnParams& P, const AttnS
 
 // By tile: a CTA's first weighted tile, and its warps' quota.
 template <int W>
-__device__ __forceinline__ int64_t attn_begin(const AttnParams& P, const AttnSplit& s, int cta) {
+__host__ __device__ __forceinline__ int64_t attn_begin(const AttnParams& P, const AttnSplit& s, int cta) {
   const int over = max(cta - P.grid, 0);
   return (int64_t(cta - over) * s.quota + int64_t(over) * s.rest) * W;
 }
-// The CTA that has a weighted tile.
+// The CTA that has a weighted tile. (These two run on the host as well, where their sizes are tested.)
 template <int W>
-__device__ __forceinline__ int attn_cta(const AttnParams& P, const AttnSplit& s, int64_t t) {
+__host__ __device__ __forceinline__ int attn_cta(const AttnParams& P, const AttnSplit& s, int64_t t) {
   const int64_t border = int64_t(P.grid) * s.quota * W;
-  const uint32_t size = uint32_t(t < border ? s.quota : s.rest) * W;
-  const int64_t at = t < border ? t : t - border;
-  const int n = at <= UINT32_MAX ? int(uint32_t(at) / size) : int(at / size);
+  // (a quota is below 2^31, a CTA's tiles are not below 2^32: only small numbers are divided in 32 bits)
+  const int64_t size = int64_t(t < border ? s.quota : s.rest) * W, at = t < border ? t : t - border;
+  const int n = (at | size) <= int64_t(UINT32_MAX) ? int(uint32_t(at) / uint32_t(size)) : int(at / size);
   return t < border ? n : n + P.grid;
 }
 
