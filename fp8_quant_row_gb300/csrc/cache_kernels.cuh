@@ -108,18 +108,11 @@ __device__ __forceinline__ int64_t rope_position(const RopeView& r, int axis, in
                 : static_cast<const int32_t*>(r.positions)[at];
 }
 
-// A copy to shared memory, zeros where `in` is false.
-template <int BYTES>
+// A copy of 16 bytes to shared memory, zeros where `in` is false.
 __device__ __forceinline__ void cp_async_if(uint32_t dst, const void* src, bool in) {
-  static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "a copy of 4, 8 or 16 bytes");
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 16 : 0)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
-                 "r"(in ? BYTES : 0)
-                 : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
 }
 
 __device__ __forceinline__ uint4 lds_words(uint32_t addr) {
@@ -244,8 +237,8 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_kernel(const __grid_co
     if (f_more) {
       const bool in = f_h < f_heads;
       const uint4* row = reinterpret_cast<const uint4*>(in ? f_src : f_row);
-      cp_async_if<16>(ring + fs, row + ca, in);
-      cp_async_if<16>(ring + fs + 512, row + cb, in);
+      cp_async_if(ring + fs, row + ca, in);
+      cp_async_if(ring + fs + 512, row + cb, in);
       f_step += stride;
       f_h += ahead;
       f_src += ahead * D;
