@@ -1,5 +1,5 @@
 """The paged cache's attention at the ends of its numbers: values, queries and logits near the ends of
-fp32's range, infinities, tables much wider than the sequences."""
+fp32's range, infinities, tables much wider than the sequences, caches that are refused."""
 from __future__ import annotations
 
 import math
@@ -8,8 +8,8 @@ import pytest
 import torch
 
 import fp8_quant_row_gb300 as fq
-from tests.test_paged_cache import (BF16, TYPES, check_attention, garbage, gpu, ids, normal,
-                                    rows_of, same, scattered)
+from tests.test_paged_cache import (A, ALIGN, BAD_CACHES, BF16, L, NULL, TYPES, c_cache, check_attention,  # noqa: F401
+                                    garbage, gpu, ids, normal, rows_of, scattered)
 
 # (sequences, tokens): each sequence a warp's, a CTA's, shared by CTAs and joined. The number of tiles
 # leaves the remainder 0 by 3.
@@ -150,3 +150,71 @@ def test_far_queries_on_small_keys(dtype, shape, power):
     for b in range(0, batch, 90):
         for h in range(4):
             check_mean(o[b, h:h + 1], lse[b, h:h + 1], v64[b * n:(b + 1) * n, h // 2:h // 2 + 1], float(s[h]), float(m[h]))
+
+
+@gpu
+@types
+def test_infinite_logits(dtype):
+    """-infinity is a weight of zero (nothing but that: zeros, and a log-sum of -infinity), +infinity a
+    NaN in its head and in no other."""
+    n, dim, kv = 300, 64, 3
+    k, v = normal((n, kv, dim), 1), normal((n, kv, dim), 2)
+    k[..., 0] = k[..., 0].abs() + 1
+    q = normal((1, 6, dim), 3)
+    q[..., 0] = 1.0
+    inf = float("inf")
+    if dtype == BF16:  # (8-bit rows with an infinity have the scale NaN)
+        gone = torch.arange(n, device="cuda") % 7 == 2
+        k[gone, 0, 0], k[5, 1, 0] = -inf, inf
+        o, lse, k64, v64 = attend(dtype, k, v, q, 1)
+        rest = ~gone
+        check_attention(o[0, :2], lse[0, :2], q[0, :2], k64[rest, :1], v64[rest, :1], dim ** -0.5, dtype)
+        assert bool(torch.isnan(o[0, 2:4]).all()) and bool(torch.isnan(lse[0, 2:4]).all())
+        check_attention(o[0, 4:], lse[0, 4:], q[0, 4:], k64[:, 2:], v64[:, 2:], dim ** -0.5, dtype)
+        k[gone, 0, 0], k[5, 1, 0] = 1.0, 1.0
+    q[0, 0, 0], q[0, 3, 0] = -inf, inf
+    o, lse, k64, v64 = attend(dtype, k, v, q, 1)
+    assert not o[0, 0].any() and float(lse[0, 0]) == -inf
+    assert bool(torch.isnan(o[0, 3]).all()) and bool(torch.isnan(lse[0, 3]))
+    for h in (1, 2, 4, 5):
+        c = slice(h // 2, h // 2 + 1)
+        check_attention(o[0, h:h + 1], lse[0, h:h + 1], q[0, h:h + 1], k64[:, c], v64[:, c], dim ** -0.5, dtype)
+
+
+@gpu
+@types
+@pytest.mark.parametrize("lengths,window", [([5, 0, 130, 17], 0), ([1] * 60, 0), ([3000, 2, 900], 0), ([3000, 2, 900], 40)], ids=str)
+def test_wide_tables(dtype, lengths, window):
+    """A table for much longer sequences (whose entries are no pages): the same answers as from one that
+    is as wide as the longest."""
+    page, kv, dim = 16, 2, 128
+    width = -(-max(lengths) // page)
+    cache = garbage(len(lengths) * width, page, kv, dim, dtype)
+    table = scattered(len(lengths), width, len(lengths) * width, 1)
+    slots = torch.cat([table[b].long()[(t := torch.arange(n, device="cuda")) // page] * page + t % page for b, n in enumerate(lengths)])
+    k, v = normal((len(slots), kv, dim), 2), normal((len(slots), kv, dim), 3)
+    fq.cache_write(k, v, cache, slots)
+    gk, gv, sk, sv = rows_of(cache, slots)
+    k64, v64 = (g.double() if s is None else g.double() * s.double()[..., None] for g, s in ((gk, sk), (gv, sv)))
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    q = normal((len(lengths), 8, dim), 4)
+    for wide in (1, 16, 300):
+        t = torch.full((len(lengths), wide * width), -1, dtype=torch.int32, device="cuda")
+        t[:, :width] = table
+        o, lse = fq.paged_attention(q, cache, t, lens, window=window, return_lse=True)
+        end = 0
+        for b, n in enumerate(lengths):
+            first, end = end + (max(0, n - window) if window else 0), end + n
+            check_attention(o[b], lse[b], q[b], k64[first:end], v64[first:end], dim ** -0.5, dtype)
+    assert fq.device_error() == 0
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES, ids=str)
+def test_a_refused_cache_is_refused_by_every_call(L, bad, status):
+    """The status of the cache's own fault, from each entry point (rows and heads as the sound cache's)."""
+    c = c_cache(**bad)
+    assert L.fp8q_cache_write(c, 10 * A, None, 0, None, 0, 11 * A, 1024, 12 * A, 1024, None, None, 1e-6, None, 4, 0, None) == status
+    assert L.fp8q_cache_read(13 * A, 14 * A, c, 15 * A, 10, 10, 16 * A, 2, 5, None) == status
+    assert L.fp8q_paged_attention(13 * A, None, 17 * A, 1 << 20, c, 15 * A, 10, 10, 16 * A, 2, 32, 1.0, 0, 18 * A, 1 << 30, None) == status
+    if status not in (NULL, ALIGN):
+        assert L.fp8q_paged_attention_workspace(c, 2, 32, 10) == -1
