@@ -528,7 +528,8 @@ fp8q_status fp8q_paged_attention(void* out, float* lse, const void* q, int64_t q
   if (!fine_rows(q_ld, q_heads, cache->head_dim) || (batch > 1 && table_ld < width) ||
       table_ld > kMaxLd)
     return FP8Q_ERR_SHAPE;
-  if (!std::isfinite(scale) || window < 0) return FP8Q_ERR_VALUE;
+  const float scale_log2 = scale * 1.4426950408889634f;  // logits in log2 units
+  if (!std::isfinite(scale_log2) || window < 0) return FP8Q_ERR_VALUE;
   if (batch == 0) return FP8Q_OK;
   if (!out || !q || !lengths || (width > 0 && !page_table)) return FP8Q_ERR_NULL;
   st = check_cache_pointers(*cache);
@@ -581,7 +582,7 @@ fp8q_status fp8q_paged_attention(void* out, float* lse, const void* q, int64_t q
   p.by_warps = fast_div_by(int64_t(s.grid) * s.warps);
   p.by_heads = fast_div_by(p.heads);
   p.by_blocks = fast_div_by(p.blocks);
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.page_tiles = int(cache->page_size / 16);
   p.tile_magic = uint32_t(((int64_t(1) << 32) + p.page_tiles - 1) / p.page_tiles);
   switch (cache->type) {

@@ -446,7 +446,7 @@ fp8q_status fp8q_cache_read(void* k_out, void* v_out, const fp8q_paged_cache* ca
  *                   are read. A page outside the cache is left out of the sums and sets
  *                   FP8Q_DEVERR_BAD_INDEX
  *   lengths     in  [batch] int32 (device); clamped to 0 .. width*page_size
- *   q_heads     a multiple of cache->heads;  width*page_size < 2^30;  scale finite;  window >= 0;
+ *   q_heads     a multiple of cache->heads;  width*page_size < 2^30;  |scale| <= 2^127;  window >= 0;
  *               with n = width*page_size/16 + 8: n * max(q_heads, batch) < 2^31 and
  *               n * batch * q_heads <= 2^40
  *   workspace   device buffer of workspace_bytes >= fp8q_paged_attention_workspace(...), 16-byte

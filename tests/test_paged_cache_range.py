@@ -8,8 +8,8 @@ import pytest
 import torch
 
 import fp8_quant_row_gb300 as fq
-from tests.test_paged_cache import (A, ALIGN, BAD_CACHES, BF16, L, NULL, TYPES, c_cache, check_attention,  # noqa: F401
-                                    garbage, gpu, ids, normal, rows_of, scattered)
+from tests.test_paged_cache import (A, ALIGN, BAD_CACHES, BF16, L, NULL, OK, TYPES, VALUE, c_cache,  # noqa: F401
+                                    check_attention, garbage, gpu, ids, normal, rows_of, scattered)
 
 # (sequences, tokens): each sequence a warp's, a CTA's, shared by CTAs and joined. The number of tiles
 # leaves the remainder 0 by 3.
@@ -218,3 +218,10 @@ def test_a_refused_cache_is_refused_by_every_call(L, bad, status):
     assert L.fp8q_paged_attention(13 * A, None, 17 * A, 1 << 20, c, 15 * A, 10, 10, 16 * A, 2, 32, 1.0, 0, 18 * A, 1 << 30, None) == status
     if status not in (NULL, ALIGN):
         assert L.fp8q_paged_attention_workspace(c, 2, 32, 10) == -1
+
+
+@pytest.mark.parametrize("scale,status", [(3e38, VALUE), (-3e38, VALUE), (math.inf, VALUE), (math.nan, VALUE), (2.0 ** 127, OK), (-1e38, OK)])
+def test_scales_refused(L, scale, status):
+    """A scale that is beyond fp32 in log2 units (times 1.44) would make every logit a NaN or infinite.
+    (No sequences: nothing is launched.)"""
+    assert L.fp8q_paged_attention(13 * A, None, 17 * A, 4096, c_cache(), 15 * A, 10, 10, 16 * A, 0, 32, scale, 0, 18 * A, 1 << 30, None) == status
