@@ -13,6 +13,21 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: long-running CPU test")
 
 
+# Host-side tests that also make calls which are not refused, with addresses that are no memory: without a
+# device these stop before the launch.
+NO_DEVICE = ("test_qk_norm_rope_refusals", "test_cache_write_refusals")
+
+
+def pytest_collection_modifyitems(items):
+    mine = [i for i in items if i.name in NO_DEVICE]
+    if not mine:
+        return
+    import torch
+    if torch.cuda.is_available():
+        for i in mine:
+            i.add_marker(pytest.mark.skip(reason="would launch kernels on addresses that are no memory"))
+
+
 # Mismatch counts of the one-ulp parity checks (LayerNorm y, QKV-epilogue q and k: elements
 # that differ from the oracle by one bf16 ulp), reported at the end of the run.
 PARITY_COUNTS = []
