@@ -7,7 +7,8 @@
 // (a, b) -> (a c - b s, b c + a s) for its angle; all in fp32, one rounding at the end (bf16, or
 // the codes of 8-bit rows). Angles are kept as turns in 64-bit fixed point: a pair's step is
 // inv_freq 2^64 / (2 pi), a position times its step modulo 2^64 is the turn's fraction, exact
-// integer arithmetic at any position; only the step is rounded (2^-53 relative, the double's own).
+// integer arithmetic at any position; only the step is rounded (2^-52 of itself, 1 / (2 pi) and the
+// product, and 2^-65 turns).
 //
 // A head's row lies in D / 16 lanes, two chunks of eight values each, one from either half of the
 // row: the pairs of both rotations of a whole head, (i, i + D/2) and (2i, 2i + 1), then lie in one
@@ -24,7 +25,7 @@
 namespace fp8q {
 
 constexpr int kCacheInt8 = 0, kCacheE4m3 = 1, kCacheBf16 = 2;
-constexpr unsigned kDevErrBadIndex = 2u;  // a slot, page or length outside the cache
+constexpr unsigned kDevErrBadIndex = 2u;  // a slot or page outside the cache
 
 struct CacheView {
   uint8_t* k;
@@ -38,8 +39,8 @@ struct CacheView {
   int page_size, heads;
 };
 
-// x / page_size for 0 <= x < 2^48, by x * ceil(2^64 / d): the excess x (M d - 2^64) is below
-// 2^48 * 2^10 < 2^64 / d.
+// x / page_size for 0 <= x < 2^48, by the high word of x M, M = ceil(2^64 / d): exact where
+// x (M d - 2^64) < 2^64, and M d - 2^64 < d <= 2^10.
 __device__ __forceinline__ int64_t page_of(int64_t x, uint64_t magic) {
   return int64_t(__umul64hi(uint64_t(x), magic));
 }

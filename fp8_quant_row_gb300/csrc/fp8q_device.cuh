@@ -53,8 +53,8 @@ __device__ __forceinline__ void wait_for_producers() {
 
 // Lets the next kernel in the stream (launched with programmatic serialization) be scheduled
 // onto SMs this grid frees; it still waits in griddepcontrol.wait for this grid to complete.
-// Only for persistent grids whose CTAs are all resident from the start, so waiting dependents
-// never hold resources one of our own CTAs still needs.
+// It is scheduled once every CTA of this grid has called this or has ended, so waiting dependents
+// never hold resources that one of our own CTAs still needs, in grids larger than what is resident too.
 __device__ __forceinline__ void allow_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -361,10 +361,10 @@ namespace fp8q {
 // device error word, mbarriers and bulk (TMA) copies
 // ------------------------------------------------------------------------------------------
 
-// Bits set by a kernel that gave up on a wait (a wait only runs out when a phase it depends
-// on never completes, i.e. on a defect): the kernel records the bit, stops taking work and
-// returns. The host reads and clears the word with fp8q_device_error(). Each translation unit of the
-// library has a word of its own.
+// Bits of the device error word. kDevErrWaitTimeout is set by a kernel that gave up on a wait (a
+// wait only runs out when a phase it depends on never completes, i.e. on a defect): the kernel records
+// the bit, stops taking work and returns. (cache_kernels.cuh has another bit.) The host reads and clears
+// the word with fp8q_device_error(). Each translation unit of the library has a word of its own.
 constexpr unsigned kDevErrWaitTimeout = 1u;
 static __device__ unsigned int g_device_error = 0u;
 

@@ -167,7 +167,9 @@ inline bool same(Range a, Range b) { return a.p == b.p && a.bytes == b.bytes; }
 // unrelated pending error of another library on the same thread is never reported as ours.
 // Launches allow programmatic dependent launch: a kernel may be scheduled while the previous
 // kernel in the stream drains, and every kernel executes griddepcontrol.wait before its first
-// global-memory access, so producer -> consumer ordering is unchanged.
+// global-memory access, so producer -> consumer ordering is unchanged. One exception: attn_join_kernel
+// reads the sequences' lengths before its wait. It follows paged_attention_kernel, which lets it start only
+// after its own wait, when whatever wrote the lengths is complete.
 template <typename... Args>
 fp8q_status launch(void (*fn)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                    Args... args) {

@@ -19,18 +19,18 @@
 //
 // int8 and E4M3 codes are exact in fp16. q (bf16) goes to fp16 times a power of two for each head,
 // exact down to 2^-24 of its head's largest value. A token's key scale multiplies its logit; its
-// value scale its weight, which is rounded to fp16 (2^-12 relative, against the output's 2^-9).
+// value scale its weight, which is rounded to fp16 (2^-11 relative, against the output's 2^-8).
 // Over a bf16 cache the weights go as two bf16 (16 bits of them).
 //
 // Weights are taken relative to a running maximum that is only raised when a logit exceeds it by
 // 2^6 (a vote, no shuffles in most tiles); with value scales, a second factor keeps the fp16 weights
 // below 2^15; over a bf16 cache the maximum is set 2^32 too high, which does the same for the sums.
 //
-// Measured (of 6754.5 GB/s, the copy's): bf16 64 x 4000 tokens under 16 heads 306 us (102%), 32
-// sequences of 500 to 4096 under 24 heads 141.5 (95%), E4M3 32 x 16000 under 32 heads over 8 166-168 (95%), 64 of
-// 3 to 8192 101 (81%), int8 1 x 131072 under 64 over 8 55.6 (74%), 33 of 1 to 2000 22.1 (48%), one of 57
-// 5.1. About 12 us are fixed: lengths, page table and first tiles one after another, the CTA's sums, the
-// join. With 64 x 4000 under 128 heads over 8 (115 us, 70%) two warps a scheduler wait for their
+// Measured (of 6754.5 GB/s, the copy's): bf16 64 x 4000 tokens under 16 heads 306 us (101%), 32
+// sequences of 500 to 4096 under 24 heads 139.6 (96%), E4M3 32 x 16000 under 32 heads over 8 167 (96%), 64 of
+// 3 to 8192 99.8 (82%), int8 1 x 131072 under 64 over 8 54.4 (75%), 33 of 1 to 2000 21.9 (47%), one of 57
+// 5.0. About 12 us are fixed: lengths, page table and first tiles one after another, the CTA's sums, the
+// join. With 64 x 4000 under 128 heads over 8 (114.5 us, 70%) two warps a scheduler wait for their
 // instructions' results; twelve warps an SM, 168 registers, change it by 2% either way.
 #pragma once
 
@@ -934,9 +934,10 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
 // more of them, for each CTA of the attention kernel and the segment that goes on behind it, and for
 // four of a piece's pairs of values, times PARTS; a part's warps take the pieces in turn. Many CTAs take
 // long to launch, few segments have many pieces: two parts where one would make more than kJoinMany CTAs
-// an SM (64 sequences of 3 to 8192 tokens, 8 heads: 101.1 us, 104.4 with one part, 101.7 with four;
-// 33 of 1 to 2000 22.2, 24.8, 23.0), else one (20 of 1000 to 8000, int8, 640 CTAs: 46.6 us, 47.7 with
-// two, 52.5 with four; 1 x 131072, 64 heads over 8, int8, 55.9 and 59.8 with two).
+// an SM (64 sequences of 3 to 8192 tokens, 8 heads: 100.4 us, 103.0 with one part; 33 of 1 to 2000 21.9
+// and 24.3; 32 of 24 heads in bf16 140.0 and 143.4), else one (1 x 131072, 64 heads over 8, int8, 55.0 us, 58.6 with
+// two; 1 x 2000 9.3 and 10.6; 32 x 8000 of 64 over 4 heads of 64 37.9 and 39.2). A sum of pieces is never
+// formed before it is divided, so that values up to fp32's largest stay finite.
 constexpr int kJoinWarps = 8, kJoinItems = 4, kJoinMany = 5;
 
 template <int TYPE, int D, int NT, int PARTS>

@@ -373,7 +373,8 @@ typedef struct fp8q_rotary {
  *   n_j = x_j * w_j / sqrt(mean_i(x_i^2) + eps)      (n = x without a weight)
  *   (a, b) -> (a cos t - b sin t, b cos t + a sin t) for each rotated pair of n,
  *             t = inv_freq[i] * position[axis[i]][token]
- * Angles are reduced exactly, at any position (the frequency is rounded to 2^-53 of itself).
+ * Angles are reduced exactly, at any position; the frequency, in turns, is off by up to 2^-52 of itself
+ * and 2^-65 turns (at position 10^9 and frequency 1 that is an angle of 2.3e-7).
  *
  *   q_out, k_out  out [tokens, heads, head_dim] bf16, row strides q_out_ld, k_out_ld; may be exactly
  *                     q (k) with its stride
@@ -445,7 +446,8 @@ fp8q_status fp8q_cache_read(void* k_out, void* v_out, const fp8q_paged_cache* ca
  *   page_table  in  [batch, width] int32, row stride table_ld; only entries of pages within the range
  *                   are read. A page outside the cache is left out of the sums and sets
  *                   FP8Q_DEVERR_BAD_INDEX
- *   lengths     in  [batch] int32 (device); clamped to 0 .. width*page_size
+ *   lengths     in  [batch] int32 (device); clamped to 0 .. width*page_size (0 where the cache has
+ *                   no pages)
  *   q_heads     a multiple of cache->heads;  width*page_size < 2^30;  |scale| <= 2^127;  window >= 0;
  *               with n = width*page_size/16 + 8: n * max(q_heads, batch) < 2^31 and
  *               n * batch * q_heads <= 2^40
@@ -469,14 +471,15 @@ int64_t fp8q_paged_attention_workspace(const fp8q_paged_cache* cache, int64_t ba
 #define FP8Q_DEVERR_BAD_INDEX 2u    /* a slot or page outside the cache (the access was left out) */
 
 /*
- * Reads and clears the device error word of the current device. Every wait inside the
+ * Reads and clears the device error word of the current device. A slot or page outside its cache
+ * sets FP8Q_DEVERR_BAD_INDEX (see the paged cache's calls). Every wait inside the
  * library's kernels is bounded (about two seconds of SM clock); a wait that runs out sets
  * FP8Q_DEVERR_WAIT_TIMEOUT, and the kernel stops taking work and returns with its outputs
- * incomplete. Only a defect can cause this: every phase a kernel waits for is completed by
+ * incomplete. Only a defect can cause that: every phase a kernel waits for is completed by
  * the same CTA (a bulk copy landing, or another warp's arrival), never by the host or another
  * kernel. Diagnostic call, not for the hot path: it synchronises with the device
  * (cudaMemcpyFromSymbol) and is not capturable in a CUDA graph.
- *   bits  out  host pointer; receives the word (0: no wait ran out since the last call)
+ *   bits  out  host pointer; receives the word (0: neither happened since the last call)
  */
 fp8q_status fp8q_device_error(unsigned int* bits);
 
