@@ -24,7 +24,7 @@
 //
 // Weights are taken relative to a running maximum that is only raised when a logit exceeds it by
 // 2^6 (a vote, no shuffles in most tiles); with value scales, a second factor keeps the fp16 weights
-// below 2^15; over a bf16 cache the maximum is set 2^32 too high, which does the same for the sums.
+// below 2^15; over a bf16 cache weights times 2^-32 do the same for the sums.
 //
 // Measured (of 6754.5 GB/s, the copy's): bf16 64 x 4000 tokens under 16 heads 306 us (101%), 32
 // sequences of 500 to 4096 under 24 heads 139.6 (96%), E4M3 32 x 16000 under 32 heads over 8 167 (96%), 64 of
@@ -345,10 +345,9 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
   constexpr bool QUANT = TYPE != kCacheBf16;
   constexpr int W = L::kWarps, S = L::kStages, E = L::E, KP = L::KP, VP = L::VP, MT = L::MT;
   constexpr int KS = QUANT ? 4 : 2;  // matrix steps (16 values of a key row) a piece
-  // How far above the largest logit the maximum is set: over a bf16 cache weights are up to 2^-26, so
-  // that their sums with values up to bf16's largest stay within fp32 for 2^26 tokens (8-bit caches have
-  // the factor kf for that).
-  constexpr float kAbove = QUANT ? 0.0f : 32.0f, kMostWeight = QUANT ? 64.0f : 0x1p-26f;
+  // A bf16 cache's weights (up to 2^6) go into the products times 2^-32, so that sums with values up to
+  // bf16's largest stay within fp32 for 2^26 tokens (8-bit caches have the factor kf for that).
+  constexpr float kDown = 0x1p-32f;
   extern __shared__ __align__(1024) uint8_t attn_smem[];
   // (The warp's number from one lane: what follows from it, addresses and the walk over segments, then
   // stays in uniform registers, where the copies want it. With an elected lane asking for them, 64 x 4000
@@ -676,8 +675,8 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           p[j][x] = ex2(t[j][x] - m[j][x & 1]);
-          w[j][x] = QUANT ? p[j][x] * kf[j][x & 1] * vs[x >> 1] : p[j][x];
-          over |= p[j][x] > kMostWeight;
+          w[j][x] = QUANT ? p[j][x] * kf[j][x & 1] * vs[x >> 1] : p[j][x] * kDown;
+          over |= p[j][x] > 64.0f;
           if (QUANT) over |= w[j][x] > 32768.0f;
         }
       if (__any_sync(0xffffffffu, over)) {
@@ -688,7 +687,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
             float top = fmaxf(t[j][x], t[j][x + 2]);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float m1 = fmaxf(m[j][x], top + kAbove), f = ex2(m[j][x] - m1);
+            const float m1 = fmaxf(m[j][x], top), f = ex2(m[j][x] - m1);
             m[j][x] = m1;
             l[j][x] *= f;
             float gain = f;
@@ -710,8 +709,8 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
               w[j][x] = p[j][x] * k1 * vs[0];
               w[j][x + 2] = p[j][x + 2] * k1 * vs[1];
             } else {
-              w[j][x] = p[j][x];
-              w[j][x + 2] = p[j][x + 2];
+              w[j][x] = p[j][x] * kDown;
+              w[j][x + 2] = p[j][x + 2] * kDown;
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[j][i][x] *= gain, o[j][i][x + 2] *= gain;
@@ -802,7 +801,7 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float f = QUANT ? __fdividef(1.0f, kf[j][x]) : 1.0f;
+        float f = __fdividef(1.0f, QUANT ? kf[j][x] : kDown);
         f = l[j][x] == 0.0f ? 0.0f : __fdividef(f, l[j][x]);
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[j][i][x] *= f, o[j][i][x + 2] *= f;

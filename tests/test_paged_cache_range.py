@@ -154,6 +154,24 @@ def test_far_queries_on_small_keys(dtype, shape, power):
 
 @gpu
 @types
+def test_the_log_sum_of_one_token(dtype):
+    """One token's log-sum is its logit, which the product gives exactly here (one value): a product with the scale,
+    one by log2(e) and its own back (2^-24 each, and the constants' 2^-25), the scale of 8-bit keys (2^-24, and
+    the factor's): 2^-21 of it in all, whatever its size."""
+    n = 2000
+    k = torch.zeros(n, 1, 64, dtype=BF16, device="cuda")
+    k[:, 0, 0] = torch.linspace(0.01, 9, n, device="cuda").to(BF16)
+    v = normal((n, 1, 64), 1)
+    q = torch.zeros(n, 1, 64, dtype=BF16, device="cuda")
+    q[..., 0] = 1.0
+    o, lse, k64, v64 = attend(dtype, k, v, q, n, 0.37)
+    want = k64[:, 0, 0] * 0.37
+    assert bool(((lse[:, 0].double() - want).abs() <= 2.0 ** -21 * want).all()), float(((lse[:, 0].double() - want).abs() / want).max())
+    assert bool(((o[:, 0].double() - v64[:, 0]).abs() <= (2.0 ** -8 + 2.0 ** -10) * v64[:, 0].abs()).all())
+
+
+@gpu
+@types
 def test_infinite_logits(dtype):
     """-infinity is a weight of zero (nothing but that: zeros, and a log-sum of -infinity), +infinity a
     NaN in its head and in no other."""
