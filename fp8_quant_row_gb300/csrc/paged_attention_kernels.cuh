@@ -24,7 +24,7 @@
 //
 // Weights are taken relative to a running maximum that is only raised when a logit exceeds it by
 // 2^6 (a vote, no shuffles in most tiles); with value scales, a second factor keeps the fp16 weights
-// below 2^15; over a bf16 cache weights times 2^-32 do the same for the sums.
+// below 2^15; over a bf16 cache weights times 2^-24 do the same for the sums.
 //
 // Measured (of 6754.5 GB/s, the copy's): bf16 64 x 4000 tokens under 16 heads 306 us (101%), 32
 // sequences of 500 to 4096 under 24 heads 139.6 (96%), E4M3 32 x 16000 under 32 heads over 8 167 (96%), 64 of
@@ -345,9 +345,10 @@ __global__ void __launch_bounds__(AttnLayout<TYPE, D, NT>::kWarps * 32, AttnLayo
   constexpr bool QUANT = TYPE != kCacheBf16;
   constexpr int W = L::kWarps, S = L::kStages, E = L::E, KP = L::KP, VP = L::VP, MT = L::MT;
   constexpr int KS = QUANT ? 4 : 2;  // matrix steps (16 values of a key row) a piece
-  // A bf16 cache's weights (up to 2^6) go into the products times 2^-32, so that sums with values up to
-  // bf16's largest stay within fp32 for 2^26 tokens (8-bit caches have the factor kf for that).
-  constexpr float kDown = 0x1p-32f;
+  // A bf16 cache's weights (up to 2^6) go into the products times 2^-24, so that a warp's sums of 2^18
+  // tokens' values up to bf16's largest stay within fp32 (8-bit caches have the factor kf for that); weights
+  // below 2^-102 of the largest lose bits for it, below 2^-109 all.
+  constexpr float kDown = 0x1p-24f;
   extern __shared__ __align__(1024) uint8_t attn_smem[];
   // (The warp's number from one lane: what follows from it, addresses and the walk over segments, then
   // stays in uniform registers, where the copies want it. With an elected lane asking for them, 64 x 4000

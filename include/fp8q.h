@@ -434,8 +434,9 @@ fp8q_status fp8q_cache_read(void* k_out, void* v_out, const fp8q_paged_cache* ca
  *   s_t = scale * q . k_t,  out = sum_t exp(s_t) v_t / sum_t exp(s_t),  lse = ln sum_t exp(s_t)
  * over t in [max(0, n - window), n) (window 0: all). A sequence without tokens gets zeros and
  * lse -infinity. Logits, maxima and sums are fp32, 8-bit codes exact, a weight times its value's
- * scale is rounded to fp16 (and to a multiple of 2^-33 of the largest; bf16 cache: to 16 bits, and
- * sums to 2^-117), the output once to bf16. Keys and values outside the range may hold anything.
+ * scale is rounded to fp16 (and to a multiple of 2^-33 of the largest; bf16 cache: to 16 bits and to
+ * 2^-109 of the largest), sums to 2^-123, the output once to bf16. Keys and values outside the range
+ * may hold anything.
  * Finite inputs give finite results where, with Q and K the largest |q| and |k|, head_dim * Q * K,
  * scale times it and scale * Q are below 2^126. A logit of -infinity is a weight of 0 (nothing but
  * these: as no tokens), one of +infinity or NaN makes its head NaN.

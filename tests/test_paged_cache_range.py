@@ -103,6 +103,21 @@ def test_small_values(dtype, shape):
 @gpu
 @types
 @where
+def test_small_weights_of_large_values(dtype, shape):
+    """A token whose weight is 2^-95 of the others', with values so large that it makes the output."""
+    batch, n = shape
+    first = torch.arange(batch * n, device="cuda") % n == 0
+    k = torch.zeros(batch * n, 2, 64, dtype=BF16, device="cuda")
+    k[..., 0] = torch.where(first, 0.0, 66.0)[:, None].to(BF16)
+    v = (normal((batch * n, 2, 64), 1).float() * torch.where(first, 2.0 ** 110, 2.0 ** -40)[:, None, None]).to(BF16)
+    q = torch.zeros(batch, 4, 64, dtype=BF16, device="cuda")
+    q[..., 0] = 1.0
+    check_all(*(x := attend(dtype, k, v, q, batch, 1.0))[:2], q, *x[2:], 1.0, dtype)
+
+
+@gpu
+@types
+@where
 def test_the_largest_values(dtype, shape):
     """All values bf16's largest: their mean is no larger."""
     batch, n = shape
